@@ -58,6 +58,7 @@ typedef struct kvc_cache* kvc_t;
 #define KVC_DEV_BAD_LENS 1u     /* some lens[b] < 1 (or < 0 for prefill) or > T_max */
 #define KVC_DEV_WAIT_TIMEOUT 2u /* an in-kernel wait gave up (internal error; output invalid) */
 #define KVC_DEV_BAD_BLOCK 4u    /* a paged call met a block-table entry outside [0, num_blocks) */
+#define KVC_DEV_BAD_SEQ 8u      /* cu_seqlens or groups do not ascend from 0 within their bounds */
 
 /* Create a cache of `layers` layers, each holding K and V of shape [B, H_kv, T_max, D].
  * Supported: dtype KVC_BF16 with D in {64, 128, 256}; KVC_F32 with D in {4, 64, 128, 256};
@@ -260,6 +261,87 @@ int kvc_paged_decode_step(kvc_t h, int layer, const void* q, const void* k_new, 
                           void* out, const int32_t* block_table, const int32_t* lens, void* stream);
 /* Paged geometry (any pointer may be NULL); KVC_EINVAL for a contiguous handle. */
 int kvc_get_paged_shape(kvc_t h, int* num_blocks, int* block_size, int* max_blocks);
+
+/* ---------------------------------------------------------------------------------------
+ * Ragged batches over a paged cache: each sequence brings any number of new tokens (none, one,
+ * a chunk of a prompt), packed one after another.  The pages describe the pieces (chunked prefill
+ * and its lower-right causal mask, "第 1 周 · Day 4" §3.3; positions of new tokens, §3.2; shared
+ * prefixes, "11.7 KV Cache" §8); the packed layout is this library's:
+ *   - q [N, H_q, D], k and v [N, H_kv, D], out [N, H_q, D] in the cache dtype: one row of heads
+ *     per new token.  Consecutive tokens are `stride` elements apart (a view of a joint qkv
+ *     projection has a larger stride than H * D); the heads of a token are contiguous.  Base
+ *     pointers and strides are multiples of 16 bytes, stride >= H * D.
+ *   - cu_seqlens (int32 [B + 1], device): sequence b's new tokens are rows [cu[b], cu[b + 1]),
+ *     T_b of them.  cu[0] = 0, cu does not decrease, cu[B] <= N; else KVC_DEV_BAD_SEQ is set and
+ *     the call writes nothing.  Rows [cu[B], N) are padding: neither read nor written.
+ *   - lens[b] counts the sequence's positions with its new tokens: row i of sequence b is position
+ *     lens[b] - T_b + i.  T_b <= lens[b] <= T_max, else KVC_DEV_BAD_LENS is set, that sequence's
+ *     rows are not appended and its attention outputs are zero.  lens[b] of a sequence without new
+ *     tokens is not looked at.
+ * All of it is read on the device, so a captured graph serves changing batches.  N >= 1.  The
+ * handle's device must be the current one (else KVC_EINVAL). */
+
+/* Rotary positions.  The first rot_dim dimensions of a head (even, 2 <= rot_dim <= D) are
+ * rot_dim / 2 pairs; pair i turns by the angle a_i = position * inv_freq[i]:
+ *     (x1, x2) -> scale * (x1 cos a_i - x2 sin a_i, x2 cos a_i + x1 sin a_i)
+ * layout KVC_ROPE_HALF pairs dimensions (i, i + rot_dim / 2), KVC_ROPE_ADJACENT (2i, 2i + 1).
+ * With several axes (time, height, width, ...) pair i takes its position from axis[i] in
+ * [0, n_axes), 1 <= n_axes <= 8; axis = NULL puts every pair on axis 0.  inv_freq (double) and axis
+ * are HOST arrays of rot_dim / 2 entries; frequency scaling for long contexts is the caller's choice of
+ * them and of scale (finite).  The angle is kept as a 64-bit fraction of a turn, so positions far
+ * from 0 lose nothing.  A plain host object: no device memory, usable with any handle (create
+ * returns KVC_EUNSUPPORTED for rot_dim > 256). */
+typedef struct kvc_rope* kvc_rope_t;
+#define KVC_ROPE_HALF 0
+#define KVC_ROPE_ADJACENT 1
+int kvc_rope_create(kvc_rope_t* out, int rot_dim, const double* inv_freq, int layout, int n_axes,
+                    const int32_t* axis, float scale);
+int kvc_rope_destroy(kvc_rope_t r);
+
+/* Append with rotation: k, rotated by its position, and v as it is go to the sequences' new slots
+ * lens[b] - T_b + i of `layer` through the block table; q, rotated, goes to q_out (which may be q
+ * itself with the same stride; otherwise the two do not overlap).  q = q_out = NULL appends only.
+ * positions (int32 [n_axes, N] with axis rows pos_stride >= N elements apart, device) gives each
+ * row's position per axis; NULL takes the slot for every axis.  Products in fp32, rounded once to
+ * the cache dtype.  Only the new slots change; two rows must not share a slot (a block that two
+ * sequences both write).  A row whose table entry is out of range is not stored
+ * (KVC_DEV_BAD_BLOCK); its q is still rotated. */
+int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, int64_t q_stride,
+                          void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* positions,
+                          int64_t pos_stride, const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* lens, int N, void* stream);
+
+/* Attention of the new tokens over the paged cache: row i of sequence b, head j sees positions
+ * [0, lens[b] - T_b + i] (its own included; append first):
+ *     out = softmax_t(q . K_t / sqrt(D)) V,   fp32 softmax and sums, rounded once.
+ * Values at positions a row does not see never reach it, whatever they are.  Computed on CUDA
+ * cores in fp32, whatever the handle's math mode.  ws is device scratch of at least
+ * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
+ * once the call has completed on its stream; calls that may run at the same time need one each. */
+int kvc_paged_attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,
+                          int64_t out_stride, const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* lens, int N, void* ws, uint64_t ws_bytes, void* stream);
+
+/* The same attention for a batch whose sequences share prefixes: group g is the consecutive
+ * sequences [groups[g], groups[g + 1]) (int32 [NG + 1], device; groups[0] = 0, not decreasing,
+ * groups[NG] = B, else KVC_DEV_BAD_SEQ and nothing is written), whose first prefix_lens[g]
+ * positions (int32 [NG], device) lie in the same blocks.  Each K / V row of a prefix is read for all
+ * rows of the group together (through the table of the group's first sequence), the rest of a
+ * sequence per sequence, and the two softmax states are merged: the outputs are those of
+ * kvc_paged_attn_ragged up to rounding.  A prefix is used down to whole blocks (its last, partial
+ * block is read per sequence through that sequence's own table).  The new tokens lie behind the
+ * prefix: lens[b] - T_b >= prefix_lens[g], else sequence b is invalid as above; a prefix outside
+ * [0, T_max] makes its group's sequences invalid.  1 <= NG <= B. */
+int kvc_paged_attn_shared(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,
+                          int64_t out_stride, const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* lens, int N, const int32_t* groups,
+                          const int32_t* prefix_lens, int NG, void* ws, uint64_t ws_bytes,
+                          void* stream);
+
+/* Scratch of the two attention calls for N rows and NG groups (NG = 0: kvc_paged_attn_ragged), at
+ * the handle's present kvc_set_ctas setting. */
+int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes);
 
 /* Shape query: writes layers, B, H_q, H_kv, D, T_max, dtype (any pointer may be NULL). */
 int kvc_get_shape(kvc_t h, int* layers, int* B, int* H_q, int* H_kv, int* D, int* T_max,

@@ -16,6 +16,7 @@ namespace kvc {
 constexpr uint32_t DEV_BAD_LENS = 1u;      // mirrors KVC_DEV_BAD_LENS
 constexpr uint32_t DEV_WAIT_TIMEOUT = 2u;  // mirrors KVC_DEV_WAIT_TIMEOUT
 constexpr uint32_t DEV_BAD_BLOCK = 4u;     // mirrors KVC_DEV_BAD_BLOCK
+constexpr uint32_t DEV_BAD_SEQ = 8u;       // mirrors KVC_DEV_BAD_SEQ
 constexpr int MAX_B = 1024;
 // An in-kernel wait that has not completed after this long gives up, flags
 // DEV_WAIT_TIMEOUT and lets the kernel run to its end (no hang, output marked invalid).
@@ -340,6 +341,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Two floats -> a bf16 pair (a in the low half), round to nearest even.
+__device__ __forceinline__ uint32_t bf16x2_rn(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <typename T>
 struct Elem;
 template <>
@@ -361,6 +368,9 @@ struct Elem<__nv_bfloat16> {
     __device__ __forceinline__ static void store(void* base, size_t idx, float x) {
         reinterpret_cast<__nv_bfloat16*>(base)[idx] = __float2bfloat16_rn(x);
     }
+    __device__ __forceinline__ static uint4 pack(const float (&f)[8]) {
+        return make_uint4(bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
+    }
 };
 template <>
 struct Elem<float> {
@@ -376,6 +386,9 @@ struct Elem<float> {
     }
     __device__ __forceinline__ static void store(void* base, size_t idx, float x) {
         reinterpret_cast<float*>(base)[idx] = x;
+    }
+    __device__ __forceinline__ static uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
 // Symmetric int8 quantization of one bf16 row of D = 128 values, as the cache stores it:

@@ -19,8 +19,9 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "kvc.h")
 
 KVC_BF16, KVC_F32 = 0, 1
 KVC_OK, KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA, KVC_ERANGE, KVC_EDEVICE, KVC_EUNSUPPORTED = range(7)
-KVC_DEV_BAD_LENS, KVC_DEV_WAIT_TIMEOUT, KVC_DEV_BAD_BLOCK = 1, 2, 4
+KVC_DEV_BAD_LENS, KVC_DEV_WAIT_TIMEOUT, KVC_DEV_BAD_BLOCK, KVC_DEV_BAD_SEQ = 1, 2, 4, 8
 KVC_CACHE_PLAIN, KVC_CACHE_INT8, KVC_CACHE_FP8 = 0, 1, 2
+KVC_ROPE_HALF, KVC_ROPE_ADJACENT = 0, 1
 
 _lib = None
 
@@ -85,6 +86,12 @@ def load() -> ctypes.CDLL:
         "kvc_paged_decode_attn": (I, [P, I, P, P, P, P, P]),
         "kvc_paged_decode_step": (I, [P, I, P, P, P, P, P, P, P]),
         "kvc_get_paged_shape": (I, [P] + [ctypes.POINTER(I)] * 3),
+        "kvc_rope_create": (I, [ctypes.POINTER(P), I, P, I, I, P, ctypes.c_float]),
+        "kvc_rope_destroy": (I, [P]),
+        "kvc_paged_append_rope": (I, [P, I, P, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, P, I, P]),
+        "kvc_paged_attn_ragged": (I, [P, I, P, I64, P, I64, P, P, P, I, P, U64, P]),
+        "kvc_paged_attn_shared": (I, [P, I, P, I64, P, I64, P, P, P, I, P, P, I, P, U64, P]),
+        "kvc_paged_attn_workspace": (I, [P, I, I, ctypes.POINTER(U64)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -117,6 +124,13 @@ def _stream(stream) -> int:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _as_stream(stream):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream()
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
 
 
 def _check(status: int, what: str):
@@ -236,6 +250,49 @@ def kvc_get_paged_shape(h) -> dict:
     vals = [ctypes.c_int() for _ in range(3)]
     _check(load().kvc_get_paged_shape(h, *[ctypes.byref(v) for v in vals]), "kvc_get_paged_shape")
     return dict(zip(("num_blocks", "block_size", "max_blocks"), (v.value for v in vals)))
+
+
+def kvc_rope_create(rot_dim, inv_freq, layout=KVC_ROPE_HALF, n_axes=1, axis=None, scale=1.0) -> int:
+    """inv_freq, axis: sequences of rot_dim / 2 entries (axis None: every pair on axis 0)."""
+    f = (ctypes.c_double * len(inv_freq))(*inv_freq)
+    a = None if axis is None else (ctypes.c_int32 * len(axis))(*axis)
+    if len(f) != rot_dim // 2 or (a is not None and len(a) != rot_dim // 2):
+        raise ValueError(f"rot_dim {rot_dim} takes {rot_dim // 2} frequencies (and axes)")
+    r = ctypes.c_void_p()
+    _check(load().kvc_rope_create(ctypes.byref(r), rot_dim, f, layout, n_axes, a, scale), "kvc_rope_create")
+    return r.value
+
+
+def kvc_rope_destroy(r) -> None:
+    _check(load().kvc_rope_destroy(r), "kvc_rope_destroy")
+
+
+def kvc_paged_append_rope(h, layer, rope, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, positions,
+                          pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
+    _check(load().kvc_paged_append_rope(h, layer, rope, _ptr(q), q_stride, _ptr(q_out), q_out_stride, _ptr(k),
+                                        k_stride, _ptr(v), v_stride, _ptr(positions), pos_stride,
+                                        _ptr(block_table), _ptr(cu_seqlens), _ptr(lens), N, _stream(stream)),
+           "kvc_paged_append_rope")
+
+
+def kvc_paged_attn_ragged(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, ws, ws_bytes,
+                          stream=None) -> None:
+    _check(load().kvc_paged_attn_ragged(h, layer, _ptr(q), q_stride, _ptr(out), out_stride, _ptr(block_table),
+                                        _ptr(cu_seqlens), _ptr(lens), N, _ptr(ws), ws_bytes, _stream(stream)),
+           "kvc_paged_attn_ragged")
+
+
+def kvc_paged_attn_shared(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, groups,
+                          prefix_lens, NG, ws, ws_bytes, stream=None) -> None:
+    _check(load().kvc_paged_attn_shared(h, layer, _ptr(q), q_stride, _ptr(out), out_stride, _ptr(block_table),
+                                        _ptr(cu_seqlens), _ptr(lens), N, _ptr(groups), _ptr(prefix_lens), NG,
+                                        _ptr(ws), ws_bytes, _stream(stream)), "kvc_paged_attn_shared")
+
+
+def kvc_paged_attn_workspace(h, N, NG=0) -> int:
+    n = ctypes.c_uint64()
+    _check(load().kvc_paged_attn_workspace(h, N, NG, ctypes.byref(n)), "kvc_paged_attn_workspace")
+    return n.value
 
 
 def kvc_bytes(h) -> int:
@@ -418,6 +475,48 @@ def _wrap_device(ptr: int, shape, dtype):
     return t
 
 
+class Rope:
+    """Rotary positions of rot_dim = 2 len(inv_freq) dimensions (see kvc_rope_create): layout "half"
+    pairs dimensions (i, i + rot_dim / 2), "adjacent" (2i, 2i + 1); axis[i] is the position axis of
+    pair i (None: one axis)."""
+
+    def __init__(self, inv_freq, layout="half", axis=None, scale=1.0):
+        inv_freq = [float(f) for f in inv_freq]
+        axis = None if axis is None else [int(a) for a in axis]
+        self.rot_dim, self.n_axes = 2 * len(inv_freq), 1 if not axis else max(axis) + 1
+        self.r = None
+        self.r = kvc_rope_create(self.rot_dim, inv_freq,
+                                 {"half": KVC_ROPE_HALF, "adjacent": KVC_ROPE_ADJACENT}[layout], self.n_axes, axis,
+                                 scale)
+
+    def close(self):
+        if self.r:
+            kvc_rope_destroy(self.r)
+            self.r = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _packed(t, heads, D, dtype, what):
+    """(tensor, elements between tokens) of a packed [N, heads, D] tensor."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != dtype:
+        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype}, got {tuple(t.shape)} {t.dtype}")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and heads > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {s}")
+    return s[0] if t.shape[0] > 1 else max(s[0], heads * D)
+
+
+def _index(t, what, *shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: want contiguous int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
 class PagedKVCache(KVCache):
     """Owns one paged kvc handle: per layer, K and V block pools [num_blocks, H_kv, block_size, D]
     reached through a caller-owned block table [B, max_blocks] (int32, device)."""
@@ -447,6 +546,83 @@ class PagedKVCache(KVCache):
 
     def decode_step(self, layer, q, k_new, v_new, out, block_table, lens, stream=None):
         kvc_paged_decode_step(self.h, layer, q, k_new, v_new, out, block_table, lens, stream)
+
+
+    def _batch(self, block_table, cu_seqlens, lens):
+        _index(block_table, "block_table", self.B, self.max_blocks)
+        _index(cu_seqlens, "cu_seqlens", self.B + 1)
+        _index(lens, "lens", self.B)
+
+    def append_rope(self, layer, rope, q, k, v, block_table, cu_seqlens, lens, q_out=None, positions=None,
+                    stream=None):
+        """Append packed new tokens: k [N, H_kv, D] rotated by `rope` and v as it is into the cache, q
+        [N, H_q, D] rotated into q_out (None: in place; q None: append only).  Sequence b's tokens are
+        rows cu_seqlens[b] .. cu_seqlens[b + 1], lens[b] counts its positions with them.  positions
+        int32 [n_axes, N] or, for one axis, [N] (None: the slot in the sequence)."""
+        N, D, dt = k.shape[0], self.D, self.torch_dtype
+        ks, vs = _packed(k, self.H_kv, D, dt, "k"), _packed(v, self.H_kv, D, dt, "v")
+        if v.shape[0] != N:
+            raise ValueError(f"v: want {N} rows, got {v.shape[0]}")
+        qs = qos = 0
+        if q is not None:
+            q_out = q if q_out is None else q_out
+            qs, qos = _packed(q, self.H_q, D, dt, "q"), _packed(q_out, self.H_q, D, dt, "q_out")
+            if q.shape[0] != N or q_out.shape[0] != N:
+                raise ValueError(f"q, q_out: want {N} rows, got {q.shape[0]}, {q_out.shape[0]}")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        ps = 0
+        if positions is not None:
+            if positions.dim() == 1 and rope.n_axes == 1:
+                positions = positions[None]
+            import torch
+            if positions.dtype != torch.int32 or tuple(positions.shape) != (rope.n_axes, N) or (
+                    N > 1 and positions.stride(1) != 1):
+                raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}], got {positions.dtype} "
+                                 f"{list(positions.shape)}")
+            ps = max(positions.stride(0), N)
+        self._batch(block_table, cu_seqlens, lens)
+        kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
+                              cu_seqlens, lens, N, stream)
+
+    def attn_workspace_bytes(self, N, groups=0) -> int:
+        """Scratch bytes of attn_ragged (groups = 0) or attn_shared for N packed rows."""
+        return kvc_paged_attn_workspace(self.h, N, groups)
+
+    def _scratch(self, workspace, N, groups, stream):
+        import torch
+        if workspace is None:
+            # allocated on the call's stream, so that its next use is ordered behind this call
+            with torch.cuda.stream(_as_stream(stream)):
+                workspace = torch.empty(self.attn_workspace_bytes(N, groups), dtype=torch.uint8, device="cuda")
+        return workspace, workspace.numel() * workspace.element_size()
+
+    def attn_ragged(self, layer, q, out, block_table, cu_seqlens, lens, workspace=None, stream=None):
+        """Attention of packed new tokens q [N, H_q, D] -> out over the cache: token i of sequence b sees
+        positions up to lens[b] - T_b + i (append first).  workspace: a contiguous device tensor of at
+        least attn_workspace_bytes(N) bytes (None: allocated for the call)."""
+        N, dt = q.shape[0], self.torch_dtype
+        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
+        if out.shape[0] != N:
+            raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
+        self._batch(block_table, cu_seqlens, lens)
+        ws, nb = self._scratch(workspace, N, 0, stream)
+        kvc_paged_attn_ragged(self.h, layer, q, qs, out, os_, block_table, cu_seqlens, lens, N, ws, nb, stream)
+
+    def attn_shared(self, layer, q, out, block_table, cu_seqlens, lens, groups, prefix_lens, workspace=None,
+                    stream=None):
+        """attn_ragged for groups of consecutive sequences [groups[g], groups[g + 1]) (int32 [NG + 1])
+        whose first prefix_lens[g] (int32 [NG]) positions lie in the same blocks."""
+        N, dt, NG = q.shape[0], self.torch_dtype, prefix_lens.shape[0]
+        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
+        if out.shape[0] != N:
+            raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
+        self._batch(block_table, cu_seqlens, lens)
+        _index(groups, "groups", NG + 1)
+        _index(prefix_lens, "prefix_lens", NG)
+        ws, nb = self._scratch(workspace, N, NG, stream)
+        kvc_paged_attn_shared(self.h, layer, q, qs, out, os_, block_table, cu_seqlens, lens, N, groups, prefix_lens,
+                              NG, ws, nb, stream)
 
 
 class RollingKVCache(KVCache):

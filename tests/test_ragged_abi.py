@@ -1,0 +1,62 @@
+"""Host-side checks of the ragged calls: rotary tables and refusals that need no GPU."""
+import ctypes
+
+import pytest
+
+from kv_cache_decode_kvc_gb300 import kvc
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_decode_kvc_gb300 import build
+    build.build()
+    return kvc.load()
+
+
+def test_rope_create_and_destroy(lib):
+    r = kvc.Rope([1.0, 0.1, 0.01], layout="adjacent", axis=[0, 2, 1], scale=0.5)
+    assert r.rot_dim == 6 and r.n_axes == 3 and r.r
+    r.close()
+    assert lib.kvc_rope_destroy(None) == kvc.KVC_OK
+
+
+@pytest.mark.parametrize("rot,freq,layout,axes,axis,scale,status", [
+    (0, [1.0], 0, 1, None, 1.0, kvc.KVC_EINVAL),
+    (3, [1.0, 1.0], 0, 1, None, 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, float("inf")], 0, 1, None, 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, float("nan")], 0, 1, None, 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, 1.0], 2, 1, None, 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, 1.0], 0, 0, None, 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, 1.0], 0, 2, [0, 2], 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, 1.0], 0, 2, [0, -1], 1.0, kvc.KVC_EINVAL),
+    (4, [1.0, 1.0], 0, 1, None, float("nan"), kvc.KVC_EINVAL),
+    (258, [1.0] * 129, 0, 1, None, 1.0, kvc.KVC_EUNSUPPORTED),
+    (4, [1.0, 1.0], 0, 9, None, 1.0, kvc.KVC_EUNSUPPORTED),
+])
+def test_rope_create_refuses(lib, rot, freq, layout, axes, axis, scale, status):
+    out = ctypes.c_void_p(5)
+    f = (ctypes.c_double * len(freq))(*freq)
+    a = None if axis is None else (ctypes.c_int32 * len(axis))(*axis)
+    assert lib.kvc_rope_create(ctypes.byref(out), rot, f, layout, axes, a, scale) == status
+    assert out.value is None
+
+
+def test_rope_create_refuses_null(lib):
+    out = ctypes.c_void_p(5)
+    assert lib.kvc_rope_create(None, 4, None, 0, 1, None, 1.0) == kvc.KVC_EINVAL
+    assert lib.kvc_rope_create(ctypes.byref(out), 4, None, 0, 1, None, 1.0) == kvc.KVC_EINVAL
+    with pytest.raises(ValueError):
+        kvc.kvc_rope_create(4, [1.0])
+    with pytest.raises(kvc.KvcError):
+        kvc.Rope([1.0, float("inf")])
+
+
+def test_null_handles_are_refused(lib):
+    r = kvc.Rope([1.0])
+    n = ctypes.c_uint64()
+    assert lib.kvc_paged_append_rope(None, 0, r.r, 16, 16, 16, 16, 16, 16, 16, 16, None, 0, 16, 16, 16, 1,
+                                     None) == kvc.KVC_EINVAL
+    assert lib.kvc_paged_attn_ragged(None, 0, 16, 16, 16, 16, 16, 16, 16, 1, 256, 1 << 40, None) == kvc.KVC_EINVAL
+    assert lib.kvc_paged_attn_shared(None, 0, 16, 16, 16, 16, 16, 16, 16, 1, 16, 16, 1, 256, 1 << 40,
+                                     None) == kvc.KVC_EINVAL
+    assert lib.kvc_paged_attn_workspace(None, 1, 0, ctypes.byref(n)) == kvc.KVC_EINVAL
