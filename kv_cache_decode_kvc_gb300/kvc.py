@@ -410,7 +410,7 @@ class KVCache:
         import torch
         kp, vp = kvc_layer_ptrs(self.h, layer)
         shape = (self.B, self.H_kv, self.T_max, self.D)
-        return _wrap_device(kp, shape, self.torch_dtype), _wrap_device(vp, shape, self.torch_dtype)
+        return _wrap_device(kp, shape, self.torch_dtype, self), _wrap_device(vp, shape, self.torch_dtype, self)
 
     def prefill_write(self, layer, K, V, lens, stream=None):
         kvc_prefill_write(self.h, layer, K, V, K.shape[2], lens, stream)
@@ -457,12 +457,15 @@ class KVCache:
         return kvc_get_launch_overlap(self.h)
 
 
-def _wrap_device(ptr: int, shape, dtype):
-    """A torch tensor over library-owned device memory (the handle must outlive it)."""
+def _wrap_device(ptr: int, shape, dtype, owner):
+    """A torch tensor over device memory of `owner`'s handle.  The tensor keeps the owner alive (it
+    holds the interface object), so a view that outlives the last other reference to its cache does
+    not dangle; after owner.close() it does."""
     import torch
 
     class _Iface:
         def __init__(self):
+            self.owner = owner
             typestr = {torch.bfloat16: "<i2", torch.float32: "<f4", torch.int8: "|i1", torch.uint8: "|u1"}[dtype]
             self.__cuda_array_interface__ = {
                 "shape": tuple(shape), "typestr": typestr, "data": (ptr, False), "version": 2,
@@ -533,7 +536,7 @@ class PagedKVCache(KVCache):
         """torch views (no copy) of layer `layer`'s K and V block pools."""
         kp, vp = kvc_layer_ptrs(self.h, layer)
         shape = (self.num_blocks, self.H_kv, self.block_size, self.D)
-        return _wrap_device(kp, shape, self.torch_dtype), _wrap_device(vp, shape, self.torch_dtype)
+        return _wrap_device(kp, shape, self.torch_dtype, self), _wrap_device(vp, shape, self.torch_dtype, self)
 
     def prefill_write(self, layer, K, V, block_table, lens, stream=None):
         kvc_paged_prefill_write(self.h, layer, K, V, K.shape[2], block_table, lens, stream)
@@ -655,5 +658,5 @@ class QuantKVCache(KVCache):
         ks, vs = kvc_layer_scales(self.h, layer)
         shape = (self.B, self.H_kv, self.T_max, self.D)
         cdt = torch.uint8 if self.fp8 else torch.int8
-        return (_wrap_device(kp, shape, cdt), _wrap_device(vp, shape, cdt),
-                _wrap_device(ks, shape[:3], torch.float32), _wrap_device(vs, shape[:3], torch.float32))
+        return (_wrap_device(kp, shape, cdt, self), _wrap_device(vp, shape, cdt, self),
+                _wrap_device(ks, shape[:3], torch.float32, self), _wrap_device(vs, shape[:3], torch.float32, self))
