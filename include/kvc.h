@@ -315,8 +315,9 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
 /* Attention of the new tokens over the paged cache: row i of sequence b, head j sees positions
  * [0, lens[b] - T_b + i] (its own included; append first):
  *     out = softmax_t(q . K_t / sqrt(D)) V,   fp32 softmax and sums, rounded once.
- * Values at positions a row does not see never reach it, whatever they are.  Computed on CUDA
- * cores in fp32, whatever the handle's math mode.  ws is device scratch of at least
+ * Values at positions a row does not see never reach it, whatever they are.  bf16 caches with D =
+ * 64 or 128 run on the tcgen05 tensor cores (softmax weights enter the second product as bf16),
+ * every other shape, or math mode 1, on CUDA cores in fp32.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each. */
 int kvc_paged_attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,

@@ -27,6 +27,7 @@ def _units():
     units = [("kvc_host", "kvc_host.cu", []), ("kvc_copy", "kvc_copy.cu", []),
              ("kvc_noalloc", "kvc_noalloc.cu", []), ("kvc_selftest", "kvc_selftest.cu", []),
              ("kvc_ragged_host", "kvc_ragged_host.cu", []), ("kvc_ragged", "kvc_ragged.cu", []),
+             ("kvc_ragged_tc5", "kvc_ragged_tc5.cu", []),
              ("kvc_rope", "kvc_rope.cu", [])]
     for d in (64, 128, 256):
         units.append((f"kvc_decode_tc_d{d}", "kvc_decode_tc_inst.cu", [f"-DKVC_INST_D={d}"]))

@@ -24,6 +24,8 @@ struct kvc_cache {
     std::vector<CUtensorMap> tmaps;  // per layer: K, V (32-row boxes), K, V (128-row boxes; 3-D
                                      // maps of whole tiles for a contiguous D = 128 cache);
                                      // paged: K, V, K, V with min(bs, 128)-row boxes
+    std::vector<CUtensorMap> rmaps;  // paged bf16 pools with D = 64: per layer K, V (2-D boxes of
+                                     // min(bs, 128) rows) for the ragged attention kernel
     bool paged;                      // K / V of a layer are pools [num_blocks, H_kv, bs, D]
     bool rolling;                    // T_max = window slots, position p in slot p mod T_max
     bool quant;                      // 8-bit codes + fp32 row scales (q, out, new rows in dtype)

@@ -389,9 +389,11 @@ __device__ __forceinline__ void ragged_dst(const RaggedParams& p, const S& g, in
 
 #endif  // __CUDACC__
 
-// Launchers (kvc_ragged.cu and its tcgen05 counterpart); each returns a cudaError_t.  joint: the
-// call has groups.
+// Launchers (kvc_ragged.cu, kvc_ragged_tc5.cu, kvc_rope.cu); each returns a cudaError_t.
 int launch_ragged_cc(int dtype, const RaggedParams& p, cudaStream_t s);
+// bf16, D = 64 or 128; q: make_q_tensor_map, k / v: the pool's maps with min(bs, 128)-row boxes.
+int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                      cudaStream_t s);
 struct RopeTable {
     uint64_t freq[128];  // inv_freq in 2^-64 turns per position
     uint8_t axis[128];

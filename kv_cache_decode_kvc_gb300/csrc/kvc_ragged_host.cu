@@ -27,7 +27,12 @@ int on_device(const kvc_cache* h) {
     return dev == h->device ? KVC_OK : KVC_EINVAL;
 }
 
-// CTAs of the attention kernels at most: two per SM suit the CUDA-core kernel.
+// The tensor-core kernel takes bf16 pools with D = 64 or 128 unless CUDA cores are asked for.
+bool ragged_tc5(const kvc_cache* h) {
+    return h->dtype == KVC_BF16 && h->math != 1 && (h->D == 128 ? h->tc_ok : !h->rmaps.empty());
+}
+// CTAs of the attention kernels at most: the tensor-core kernel fills an SM, two blocks of the
+// CUDA-core kernel fit.
 int ragged_p(const kvc_cache* h) { return h->ctas > 0 ? h->ctas : 2 * h->sms; }
 
 int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* table,
@@ -73,9 +78,15 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.max_blocks = h->max_blocks;
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;
-    p.P = P;
+    p.P = ragged_tc5(h) && h->ctas <= 0 ? h->sms : P;
     p.min_units = h->ctas > 0 ? 1 : kvc::RAGGED_MIN_UNITS;
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
+    if (ragged_tc5(h)) {
+        CUtensorMap mq;
+        if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G)) return KVC_ECUDA;
+        const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
+        return kvc::launch_ragged_tc5(p, mq, kv[0], kv[1], static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
+    }
     return kvc::launch_ragged_cc(h->dtype, p, static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
