@@ -75,14 +75,14 @@ bool make_kv3_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int box_ro
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, int64_t ts, int G) {
+bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, int64_t ts, int G, int tokens) {
     EncodeTiledFn fn = encode_fn();
     if (!fn || (reinterpret_cast<uintptr_t>(q) & 15)) return false;
-    const cuuint64_t dims[4] = {64, (cuuint64_t)H_q, (cuuint64_t)N, (cuuint64_t)(D / 64)};
-    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)ts * 2, 128};
-    const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G), (cuuint32_t)(D / 64)};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H_q, (cuuint64_t)N};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ts * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

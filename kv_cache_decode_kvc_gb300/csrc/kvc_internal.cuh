@@ -187,8 +187,8 @@ constexpr int TC_FULL_ROWS = 128;
 bool make_kv_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int D, int box_rows);
 bool make_kv3_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int box_rows);
 // Packed bf16 query rows [N, H_q, D] (tokens ts elements apart): boxes of 64 columns x G heads x
-// 128 / G tokens x D / 64 column blocks, 128-byte swizzle; tokens from N on read as zero.
-bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, int64_t ts, int G);
+// `tokens` tokens, 128-byte swizzle; tokens from N on read as zero.
+bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, int64_t ts, int G, int tokens);
 int launch_combine(int dtype, int D, int G, const DecodeParams& p, cudaStream_t s);
 
 // cudaFuncSetAttribute applies to the current device only: a launcher sets a kernel's

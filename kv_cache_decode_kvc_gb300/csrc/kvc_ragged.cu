@@ -14,13 +14,15 @@ namespace kvc {
 template <int D_>
 struct CcCfg {
     static constexpr int D = D_;
+    static constexpr int LKT = D > 64 ? 5 : 6;
     static constexpr int RT = 64;
-    static constexpr int KT = D > 64 ? 32 : 64;
+    static constexpr int KT = 1 << LKT;
+    using R = Ragged<6, LKT, false>;
     static constexpr int NC = KT / 16;           // score columns of a thread
     static constexpr int NV = D < 64 ? 1 : D / 64;  // float4 output columns of a thread
     static constexpr int QS = D + 4, KS = D + 4, PS = KT + 4;  // row strides (floats)
     static constexpr int TILES = (RT * QS + KT * KS + KT * D + RT * PS) * 4;
-    static constexpr int PLAN = 2 * (MAX_B + 1) * 8;  // the prefix sums lie under the tiles
+    static constexpr int PLAN = 2 * (2 * MAX_B + 1) * 4;  // the prefix sums lie under the tiles
     static constexpr int SMEM = TILES > PLAN ? TILES : PLAN;
 };
 
@@ -38,10 +40,10 @@ __device__ __forceinline__ void store_row16(float* dst, const uint4& v, float sc
 template <typename T, int D>
 __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
     using C = CcCfg<D>;
-    using R = Ragged<C::RT, C::KT>;
+    using R = typename C::R;
     extern __shared__ __align__(16) char smem[];
     __shared__ typename R::Seg seg_s;
-    __shared__ int64_t tmp[32];
+    __shared__ typename R::Split split_s;
     float* qs = reinterpret_cast<float*>(smem);
     float* ks = qs + C::RT * C::QS;
     float* vs = ks + C::KT * C::KS;
@@ -49,38 +51,28 @@ __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int64_t* gc = reinterpret_cast<int64_t*>(smem);
-    int64_t* sc = gc + p.NG + 1;
-    if (!ragged_valid(p, tid, 256)) {
-        if (blockIdx.x == 0 && tid == 0) {
-            atomicOr(p.err, DEV_BAD_SEQ);
-            p.plan[p.NG] = 0;
-            p.plan[p.NG + 1 + p.B] = 0;
-        }
-        return;
+    int* c = reinterpret_cast<int*>(smem);
+    if (tid < 32) {
+        const typename R::Split sp = R::scan(p, c, tid);
+        if (tid == 0) split_s = sp;
     }
-    const int64_t U = ragged_scan<C::RT, C::KT>(p, gc, sc, tmp, tid, 256);
-    if (blockIdx.x == 0)
-        for (int i = tid; i < p.NG + p.B + 2; i += 256) p.plan[i] = gc[i];
-    ragged_zero_rows<T>(p, tid, 256);
-    const int64_t P = ragged_ctas(U, p.P, p.min_units);
-    if (blockIdx.x >= P) return;
-    int64_t x = cta_begin(blockIdx.x, U, P);
-    const int64_t x1 = cta_begin(blockIdx.x + 1, U, P);
-    typename R::Stream st;
-    if (tid == 0) st = R::locate(p, gc, sc, x);
+    __syncthreads();
+    const typename R::Split sp = split_s;
+    if (blockIdx.x == 0) {
+        const int n = 2 * (p.NG + p.B + 1);
+        for (int i = tid; i < n; i += 256) p.plan[i] = sp.valid ? c[i] : 0;
+        if (!sp.valid && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
+    }
+    if (tid < 6) p.cuts[6 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
+    if (sp.valid) ragged_zero_rows<T>(p, tid, 256);
+    typename R::Walk wk;
+    if (tid == 0) wk = R::walk(p, sp, c, blockIdx.x, 1);
 
     while (true) {
         __syncthreads();  // the prefix sums (or the last segment's tiles) are read
         if (tid == 0) {
-            typename R::Seg g;
-            g.n = 0;
-            while (g.n == 0 && x < x1) {
-                g = R::segment(p, st, x, x1);
-                x = st.u0 + RAGGED_C0 + st.n;
-                if (x < x1 && !R::next(p, st)) x = x1;
-            }
-            seg_s = g;
+            seg_s = R::next_seg(p, wk);
+            if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, 1, seg_s);
         }
         __syncthreads();
         const typename R::Seg g = seg_s;
@@ -215,7 +207,7 @@ __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
             if (r >= nrow || (D < 64 && tx > 0)) continue;
             const int64_t row = g.row0 + (r >> p.lgG);
             const int head = g.h * G + (r & (G - 1));
-            if (g.dst == 0) {
+            if (g.dst == -1) {
                 const float inv = 1.f / l[i];
                 T* out = static_cast<T*>(p.out) + row * p.out_ts + (int64_t)head * D;
 #pragma unroll
@@ -232,7 +224,7 @@ __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
                 }
             } else {
                 float *o, *ml;
-                ragged_dst(p, g, blockIdx.x, r, row, head, o, ml);
+                ragged_dst(p, g.dst, R::SLOT_ROWS, r, row, head, o, ml);
 #pragma unroll
                 for (int v = 0; v < C::NV; ++v) *reinterpret_cast<float4*>(o + v * 64 + tx * 4) = acc[i][v];
                 if (tx == 0) *reinterpret_cast<float2*>(ml) = make_float2(m[i], l[i]);
@@ -261,7 +253,7 @@ static int launch_cc(const RaggedParams& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_cc_kernel<T, D>, p);
     if (e != cudaSuccess) return (int)e;
-    return launch_merge<T, C::RT, C::KT>(p, s);
+    return launch_merge<T, typename C::R>(p, s);
 }
 
 int launch_ragged_cc(int dtype, const RaggedParams& p, cudaStream_t s) {

@@ -11,17 +11,22 @@
 //     tiles of KT;
 //   - a group of sequences with a common prefix of P positions has streams over [0, P) whose
 //     rows come from all of its sequences (packed consecutively), no mask; each of its
-//     sequences has streams over [P, L_b) as any sequence has over [0, L_b);
+//     sequences has streams over [P, L_b) as any sequence has over [0, L_b).  Groups and
+//     sequences are the entries e in [0, NG + B) of the batch;
 //   - all streams are laid end to end, each costing its tiles and C0 more for its start, and CTA
 //     i of P takes the cost units [i U / P, (i + 1) U / P): equal work whatever the lengths, no
-//     CTA waits for another, the same split on every run (results are reproducible).
+//     CTA waits for another, the same split on every run (results are reproducible);
+//   - streams of class 0 come first, then those of class 1.  The tensor-core kernel has two
+//     softmax sets per CTA: they share the streams of entries with more than PAIR_ROWS query
+//     rows per head (class 0: each K / V tile feeds both), and halve the CTA's range of the
+//     others (class 1) between them, each walking streams of its own.  Elsewhere all
+//     streams are class 1 and a CTA is one worker.
 // Everything is computed on the device from cu_seqlens, lens and the groups.
 //
-// A stream that one CTA holds whole and that no other stream shares rows with is written to out.
-// Otherwise its pieces go to scratch and combine_ragged_kernel merges them: the first piece of a
-// stream of a sequence with a shared prefix to a row buffer (one for prefix streams, one for
-// the sequences' own), of other streams to slot 1 of its CTA; later pieces, which open their
-// CTA's range, to slot 0.
+// A stream that one worker holds whole and that no other stream shares rows with is written to
+// out.  Otherwise its pieces go to scratch and are merged (kvc_ragged_merge.cuh): the first piece of
+// a stream of a sequence with a shared prefix to a row buffer (one for prefix streams, one for
+// the sequences' own); of other streams, and all later pieces, to slots of their worker.
 #pragma once
 
 #include "kvc_internal.cuh"
@@ -30,7 +35,7 @@ namespace kvc {
 
 constexpr int RAGGED_C0 = 1;         // cost of a stream's start, in tiles
 constexpr int RAGGED_MIN_UNITS = 4;  // fewer CTAs when a CTA's share would drop below this
-constexpr int RAGGED_SLOT_ROWS = 256;
+constexpr int PAIR_ROWS = 64;
 
 struct RaggedParams {
     const void* K;  // layer base, pools [num_blocks, H_kv, bs, D]
@@ -44,49 +49,71 @@ struct RaggedParams {
     const int32_t* groups; // [NG + 1], nullptr: no shared prefixes
     const int32_t* prefix; // [NG]
     uint32_t* err;
-    int64_t* plan;   // [NG + 1] + [B + 1] per-head cost prefix sums, for the merge
+    int* plan;       // [2][NG + B + 1] per-head cost prefix sums of the classes, for the merge
+    int4* cuts;      // [3 P][2] streams cut between workers (no groups), for the merge
     float* row_o;    // [2][N H_q][D] unnormalised outputs of first pieces (groups only)
     float* row_ml;   // [2][N H_q][2] (max in log2 units, denominator)
-    float* slot_o;   // [P][2][RAGGED_SLOT_ROWS][D]
-    float* slot_ml;  // [P][2][RAGGED_SLOT_ROWS][2]
+    float* slot_o;   // [P][slots][slot rows][D]
+    float* slot_ml;  // [P][slots][slot rows][2]
     int B, N, H_q, H_kv, lgG, NG, D;
     int bs, max_blocks, num_blocks, T_max;
     int P;          // CTAs at most
-    int min_units;  // 1: use all P CTAs down to one unit each
+    int min_units;  // cost units per CTA at least (2 or more: no worker between two pieces is empty)
     float qscale;   // log2(e) / sqrt(D)
 };
 
-// Scratch layout (bytes, 256-byte aligned parts), host side.
+// Scratch layout (bytes, 256-byte aligned parts), host side: P CTAs with `slots` slots of `rows` rows.
 struct RaggedScratch {
-    uint64_t plan, row_o, row_ml, slot_o, slot_ml, total;
+    uint64_t plan, cuts, row_o, row_ml, slot_o, slot_ml, total;
 };
-inline RaggedScratch ragged_scratch(int B, int N, int NG, int H_q, int D, int P) {
+inline RaggedScratch ragged_scratch(int B, int N, int NG, int H_q, int D, int P, int slots, int rows) {
     auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };
     RaggedScratch s;
     uint64_t at = 0;
     s.plan = at;
-    at += up((uint64_t)(B + NG + 2) * 8);
-    const uint64_t rows = NG > 0 ? 2ull * (uint64_t)N * (uint64_t)H_q : 0;
+    at += up(2 * (uint64_t)(B + NG + 1) * 4);
+    s.cuts = at;
+    at += up(3 * (uint64_t)P * 32);
+    const uint64_t joint = NG > 0 ? 2ull * (uint64_t)N * (uint64_t)H_q : 0;
     s.row_o = at;
-    at += up(rows * (uint64_t)D * 4);
+    at += up(joint * (uint64_t)D * 4);
     s.row_ml = at;
-    at += up(rows * 8);
-    const uint64_t slots = 2ull * (uint64_t)P * RAGGED_SLOT_ROWS;
+    at += up(joint * 8);
+    const uint64_t held = (uint64_t)P * slots * rows;
     s.slot_o = at;
-    at += up(slots * (uint64_t)D * 4);
+    at += up(held * (uint64_t)D * 4);
     s.slot_ml = at;
-    at += up(slots * 8);
+    at += up(held * 8);
     s.total = at;
     return s;
 }
 
 #ifdef __CUDACC__
 
-// ------------------------------------------------------------------ sequences and streams
-struct SeqInfo {
+// ------------------------------------------------------------------ entries and streams
+// Cost units are 32-bit (a call with 2^31 of them, hours of work, is refused): CTA i of P takes
+// U / P units, the first U % P one more.
+__device__ __forceinline__ int rg_begin(int i, int U, int P) {
+    const int each = (int)((unsigned)U / (unsigned)P), more = U - each * P;
+    return i * each + min(i, more);
+}
+__device__ __forceinline__ int rg_cta(int x, int U, int P) {
+    const int each = (int)((unsigned)U / (unsigned)P), more = U - each * P;
+    const int y = x - more * (each + 1);
+    return y < 0 ? (int)((unsigned)x / (unsigned)(each + 1)) : more + (int)((unsigned)y / (unsigned)each);
+}
+__device__ __forceinline__ int ragged_ctas(int U, int P, int min_units) {
+    const int want = (int)((unsigned)U / (unsigned)min_units);
+    return want < 1 ? 1 : min(want, P);
+}
+
+struct Entry {
     int row0, T;  // packed rows [row0, row0 + T)
     int L, pfx;   // positions; shared prefix in effect (whole blocks, 0: none)
-    bool ok;      // false: has rows but cannot be attended (its outputs are zero)
+    int seq;      // table row
+    bool group;   // a group's prefix: positions [0, pfx); else a sequence: [pfx, L)
+    bool ok;      // has streams
+    bool bad;     // a sequence with rows that cannot be attended (its outputs are zero)
 };
 
 // Shared prefix of sequence b: in effect (whole blocks; a group of one shares nothing) and as
@@ -103,158 +130,267 @@ __device__ __forceinline__ int2 seq_prefix(const RaggedParams& p, int b) {
     const bool one = __ldg(p.groups + lo + 1) - __ldg(p.groups + lo) < 2;
     return make_int2(one ? 0 : P / p.bs * p.bs, P);
 }
-
-__device__ __forceinline__ SeqInfo seq_info(const RaggedParams& p, int b) {
-    SeqInfo s;
+__device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b) {
+    Entry s;
     s.row0 = __ldg(p.cu + b);
-    s.T = __ldg(p.cu + b + 1) - s.row0;
+    const int r1 = __ldg(p.cu + b + 1);
     s.L = __ldg(p.lens + b);
+    s.T = r1 - s.row0;
     const int2 pf = seq_prefix(p, b);
     s.pfx = pf.x;
+    s.seq = b;
+    s.group = false;
     s.ok = s.T > 0 && s.L >= s.T && s.L <= p.T_max && pf.y >= 0 && s.L - s.T >= pf.y;
+    s.bad = s.T > 0 && !s.ok;
     return s;
 }
-
-// Rows of group g and its prefix in effect (0: no streams).
-__device__ __forceinline__ SeqInfo group_info(const RaggedParams& p, int g) {
-    const int b0 = __ldg(p.groups + g), b1 = __ldg(p.groups + g + 1);
-    SeqInfo s;
+__device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
+    const int b0 = __ldg(p.groups + g), b1 = __ldg(p.groups + g + 1), P = __ldg(p.prefix + g);
+    Entry s;
     s.row0 = __ldg(p.cu + b0);
     s.T = __ldg(p.cu + b1) - s.row0;
-    const int P = __ldg(p.prefix + g);
     s.pfx = (b1 - b0 < 2 || P < 0 || P > p.T_max) ? 0 : P / p.bs * p.bs;
     s.L = s.pfx;
+    s.seq = b0;
+    s.group = true;
     s.ok = s.T > 0 && s.pfx > 0;
+    s.bad = false;
     return s;
 }
-
-// sum of ceil(x / R) for x = 1 .. X
-__device__ __forceinline__ int64_t ceil_sum(int64_t X, int R) {
-    const int64_t n = X / R, r = X - n * R;
-    return (int64_t)R * (n * (n + 1) / 2) + r * (n + 1);
+__device__ __forceinline__ Entry entry_of(const RaggedParams& p, int e) {
+    return e < p.NG ? group_entry(p, e) : seq_entry(p, e - p.NG);
 }
 
-template <int RT, int KT>
+// sum of ceil(x / 2^lg) for x = 1 .. X
+__device__ __forceinline__ int64_t ceil_sum(int64_t X, int lg) {
+    const int64_t n = X >> lg, r = X & ((1 << lg) - 1);
+    return ((n * (n + 1) / 2) << lg) + r * (n + 1);
+}
+
+// Work split.  LRT, LKT: log2 of a stream's rows and of a key tile; PAIRS: classes as the
+// tensor-core kernel has them, and two workers per CTA for class 1.
+template <int LRT, int LKT, bool PAIRS>
 struct Ragged {
-    // Key tiles of a stream of a sequence with S0 keys of its own before its new tokens, whose
+    static constexpr int RT = 1 << LRT, KT = 1 << LKT;
+    // scratch slots of a CTA: with PAIRS five of 128 rows (a shared stream's later piece takes 0-1,
+    // its first piece 2-3 and then ends the range; set 0: 0 and 2, set 1: 3 and 4)
+    static constexpr int SLOTS = PAIRS ? 5 : 2, SLOT_ROWS = PAIRS ? RT / 2 : RT;
+
+    __device__ static int cls(const RaggedParams& p, const Entry& s) {
+        return PAIRS && ((int64_t)s.T << p.lgG) > PAIR_ROWS ? 0 : 1;
+    }
+    // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
-    __device__ static int tiles(int S0, int t1) { return (int)(((int64_t)S0 + t1 + KT - 1) / KT); }
-    // Cost of its first k streams, all full (TQ tokens each):
+    __device__ static int tiles(int S0, int t1) { return (int)(((int64_t)S0 + t1 + KT - 1) >> LKT); }
+    // Cost of its first k streams, all full (TQ = 2^lq tokens each):
     // sum over i = 1 .. k of ceil((S0 + i TQ) / KT), and the starts.
-    __device__ static int64_t cost_full(int S0, int64_t k, int TQ) {
-        if (TQ >= KT) return k * ((S0 + KT - 1) / KT) + (int64_t)(TQ / KT) * (k * (k + 1) / 2) + k * RAGGED_C0;
-        const int R = KT / TQ;  // ceil((S0 + i TQ) / KT) = ceil((ceil(S0 / TQ) + i) / R)
-        const int64_t s = (S0 + TQ - 1) / TQ;
-        return ceil_sum(s + k, R) - ceil_sum(s, R) + k * RAGGED_C0;
+    __device__ static int64_t cost_full(int S0, int64_t k, int lq) {
+        if (lq >= LKT)
+            return k * ((S0 + KT - 1) >> LKT) + ((k * (k + 1) / 2) << (lq - LKT)) + k * RAGGED_C0;
+        // ceil((S0 + i TQ) / KT) = ceil((ceil(S0 / TQ) + i) / (KT / TQ))
+        const int64_t s = (S0 + (1 << lq) - 1) >> lq;
+        return ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq) + k * RAGGED_C0;
     }
-    __device__ static int64_t seq_cost(const SeqInfo& s, int TQ) {
+    __device__ static int64_t cost(const RaggedParams& p, const Entry& s) {
         if (!s.ok) return 0;
-        const int nk = (s.T + TQ - 1) / TQ, S0 = s.L - s.T - s.pfx;
-        return cost_full(S0, nk - 1, TQ) + tiles(S0, s.T) + RAGGED_C0;
-    }
-    __device__ static int64_t group_cost(const SeqInfo& s, int TQ) {
-        if (!s.ok) return 0;
-        return (int64_t)((s.T + TQ - 1) / TQ) * ((s.pfx + KT - 1) / KT + RAGGED_C0);
+        const int lq = LRT - p.lgG, nk = (s.T + (1 << lq) - 1) >> lq;
+        if (s.group) return (int64_t)nk * (((s.pfx + KT - 1) >> LKT) + RAGGED_C0);
+        const int S0 = s.L - s.T - s.pfx;
+        return cost_full(S0, nk - 1, lq) + tiles(S0, s.T) + RAGGED_C0;
     }
 
-    // A stream: type 0 = a group's prefix, 1 = a sequence's own keys; idx = group or sequence.
-    struct Stream {
-        int type, idx, h, k;
-        SeqInfo s;
-        int64_t u0;  // its first cost unit
-        int n;       // key tiles
+    // The batch's split: total cost U, class 0's part W0, CTAs P.
+    struct Split {
+        int U, W0, P;
+        bool valid;
     };
-    __device__ static void fill(Stream& st, int TQ) {
-        if (st.type == 0) {
-            st.n = (st.s.pfx + KT - 1) / KT;
-        } else {
-            const int t1 = min(st.s.T, (st.k + 1) * TQ);
-            st.n = tiles(st.s.L - st.s.T - st.s.pfx, t1);
+    // One warp computes the per-head cost prefix sums c[0 .. NE], c[NE + 1 .. 2 NE + 1] of the two
+    // classes (NE = NG + B) and checks that cu and the groups ascend within their bounds.
+    __device__ static Split scan(const RaggedParams& p, int* c, int lane) {
+        const int NE = p.NG + p.B;
+        int carry[2] = {0, 0};
+        float sum = 0.f;  // the cost in fp32: 32-bit sums that would wrap are refused
+        bool bad = false;
+        if (lane < 2) c[lane * (NE + 1)] = 0;
+        for (int e0 = 0; e0 < NE; e0 += 32) {
+            const int e = e0 + lane;
+            int64_t v0 = 0;
+            int cl = 1;
+            bool fine = false;
+            if (e < p.NG) {
+                const int b0 = __ldg(p.groups + e), b1 = __ldg(p.groups + e + 1);
+                fine = b0 >= 0 && b1 >= b0 && b1 <= p.B && (e > 0 || b0 == 0) && (e < p.NG - 1 || b1 == p.B);
+            } else if (e < NE) {
+                const int c0 = __ldg(p.cu + e - p.NG), c1 = __ldg(p.cu + e - p.NG + 1);
+                fine = c0 >= 0 && c1 >= c0 && c1 <= p.N && (e > p.NG || c0 == 0);
+            }
+            if (fine) {
+                const Entry s = entry_of(p, e);
+                v0 = cost(p, s);
+                cl = cls(p, s);
+            }
+            bad |= !fine && e < NE;
+            sum += (float)v0;
+            const int v = (int)v0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (!PAIRS && k == 0) {
+                    if (e < NE) c[e + 1] = 0;
+                    continue;
+                }
+                int x = cl == k ? v : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                    if (lane >= o) x += t;
+                }
+                if (e < NE) c[k * (NE + 1) + e + 1] = carry[k] + x;
+                carry[k] += __shfl_sync(0xFFFFFFFFu, x, 31);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        bad |= sum * (float)p.H_kv > 2.1e9f;
+        Split sp;
+        sp.valid = !__any_sync(0xFFFFFFFFu, bad);
+        sp.W0 = sp.valid ? carry[0] * p.H_kv : 0;
+        sp.U = sp.valid ? sp.W0 + carry[1] * p.H_kv : 0;
+        sp.P = sp.U > 0 ? ragged_ctas(sp.U, p.P, p.min_units) : 0;
+        __syncwarp();
+        return sp;
+    }
+    // The split as the attention kernel left it in p.plan.
+    __device__ static Split planned(const RaggedParams& p) {
+        const int NE = p.NG + p.B;
+        Split sp;
+        sp.W0 = p.plan[NE] * p.H_kv;
+        sp.U = sp.W0 + p.plan[2 * NE + 1] * p.H_kv;
+        sp.P = sp.U > 0 ? ragged_ctas(sp.U, p.P, p.min_units) : 0;
+        sp.valid = sp.U > 0;
+        return sp;
+    }
+
+    // Worker w of CTA i: 0 the CTA as a whole (class 0), 1 and 2 its sets (class 1; without
+    // PAIRS only 1).  Cost units [a, b).
+    __device__ static void range(const Split& sp, int i, int w, int& a, int& b) {
+        a = b = 0;
+        if (i >= sp.P) return;
+        const int x0 = rg_begin(i, sp.U, sp.P), x1 = rg_begin(i + 1, sp.U, sp.P);
+        if (w == 0) {
+            a = x0;
+            b = x1 < sp.W0 ? x1 : sp.W0;
+            return;
+        }
+        a = x0 > sp.W0 ? x0 : sp.W0;
+        b = x1;
+        if (PAIRS && b > a) {
+            const int mid = a + (b - a + 1) / 2;
+            if (w == 1) b = mid; else a = mid;
         }
     }
-    // The stream holding cost unit x, from the prefix sums gc[NG + 1], sc[B + 1] (per head).
-    __device__ static Stream locate(const RaggedParams& p, const int64_t* gc, const int64_t* sc, int64_t x) {
-        const int TQ = RT >> p.lgG;
+    // The worker that owns unit x, as a position in the order of its class: CTA for class 0,
+    // 2 CTA + set (CTA without PAIRS) for class 1.
+    __device__ static int owner(const Split& sp, int x) {
+        const int i = rg_cta(x, sp.U, sp.P);
+        if (!PAIRS || x < sp.W0) return i;
+        int a, b;
+        range(sp, i, 2, a, b);
+        return 2 * i + (x >= a ? 1 : 0);
+    }
+    // Slot of a worker's piece: `later` piece of a stream (it opens the worker's range) or its first.
+    __device__ static int slot(int cl, int own, bool later) {
+        if (!PAIRS) return own * 2 + (later ? 0 : 1);
+        if (cl == 0) return own * 5 + (later ? 0 : 2);
+        return (own >> 1) * 5 + ((own & 1) ? (later ? 3 : 4) : (later ? 0 : 2));
+    }
+
+    struct Stream {
+        Entry s;
+        int e, h, k;
+        int u0;  // its first cost unit
+        int n;   // key tiles
+    };
+    __device__ static void fill(const RaggedParams& p, Stream& st) {
+        const int lq = LRT - p.lgG;
+        if (st.s.group) {
+            st.n = (st.s.pfx + KT - 1) >> LKT;
+        } else {
+            const int64_t t1 = (int64_t)(st.k + 1) << lq;
+            st.n = tiles(st.s.L - st.s.T - st.s.pfx, t1 < st.s.T ? (int)t1 : st.s.T);
+        }
+    }
+    // The stream holding cost unit x.
+    __device__ static Stream locate(const RaggedParams& p, const Split& sp, const int* c, int x) {
+        const int NE = p.NG + p.B, lq = LRT - p.lgG;
         Stream st;
-        const int64_t W0 = p.NG > 0 ? gc[p.NG] * p.H_kv : 0;
-        st.type = x < W0 ? 0 : 1;
-        const int64_t* c = st.type == 0 ? gc : sc;
-        const int64_t base = st.type == 0 ? 0 : W0;
-        int lo = 0, hi = (st.type == 0 ? p.NG : p.B) - 1;  // largest i with H_kv c[i] <= x - base
+        const int base = x < sp.W0 ? 0 : sp.W0;
+        if (x >= sp.W0) c += NE + 1;
+        int lo = 0, hi = NE - 1;  // largest e with H_kv c[e] <= x - base
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (c[mid] * p.H_kv <= x - base) lo = mid; else hi = mid - 1;
         }
-        st.idx = lo;
-        const int64_t per = c[lo + 1] - c[lo];
-        int64_t r = x - base - c[lo] * p.H_kv;
-        st.h = (int)(r / per);
+        st.e = lo;
+        st.s = entry_of(p, lo);
+        const int per = c[lo + 1] - c[lo];
+        int r = x - base - c[lo] * p.H_kv;
+        st.h = (int)((unsigned)r / (unsigned)per);
         r -= st.h * per;
         st.u0 = base + c[lo] * p.H_kv + st.h * per;
-        st.s = st.type == 0 ? group_info(p, lo) : seq_info(p, lo);
-        const int nk = (st.s.T + TQ - 1) / TQ;
-        if (st.type == 0) {
-            const int64_t one = (st.s.pfx + KT - 1) / KT + RAGGED_C0;
-            st.k = (int)(r / one);
+        if (st.s.group) {
+            const int one = ((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0;
+            st.k = (int)((unsigned)r / (unsigned)one);
             st.u0 += st.k * one;
         } else {
             const int S0 = st.s.L - st.s.T - st.s.pfx;
-            int a = 0, b = nk - 1;
+            int a = 0, b = ((st.s.T + (1 << lq) - 1) >> lq) - 1;
             while (a < b) {  // largest k with cost_full(k) <= r
                 const int mid = (a + b + 1) >> 1;
-                if (cost_full(S0, mid, TQ) <= r) a = mid; else b = mid - 1;
+                if (cost_full(S0, mid, lq) <= r) a = mid; else b = mid - 1;
             }
             st.k = a;
-            st.u0 += cost_full(S0, a, TQ);
+            st.u0 += (int)cost_full(S0, a, lq);
         }
-        fill(st, TQ);
+        fill(p, st);
         return st;
     }
-    // The stream of packed row `row` (a token of sequence idx, type 1, or of group idx, type 0).
-    __device__ static Stream of_row(const RaggedParams& p, const int64_t* gc, const int64_t* sc, int type, int idx,
-                                    int h, int row) {
-        const int TQ = RT >> p.lgG;
+    // The stream of packed row `row` of entry e.
+    __device__ static Stream of_row(const RaggedParams& p, const Split& sp, const int* c, int e, int h, int row) {
+        const int NE = p.NG + p.B, lq = LRT - p.lgG;
         Stream st;
-        st.type = type;
-        st.idx = idx;
+        st.e = e;
         st.h = h;
-        st.s = type == 0 ? group_info(p, idx) : seq_info(p, idx);
-        st.k = (row - st.s.row0) / TQ;
-        const int64_t* c = type == 0 ? gc : sc;
-        st.u0 = (type == 0 || p.NG == 0 ? 0 : gc[p.NG] * p.H_kv) + c[idx] * p.H_kv + h * (c[idx + 1] - c[idx]);
-        if (type == 0)
-            st.u0 += st.k * (int64_t)((st.s.pfx + KT - 1) / KT + RAGGED_C0);
-        else
-            st.u0 += cost_full(st.s.L - st.s.T - st.s.pfx, st.k, TQ);
-        fill(st, TQ);
+        st.s = entry_of(p, e);
+        st.k = (row - st.s.row0) >> lq;
+        const int cl = cls(p, st.s);
+        c += cl * (NE + 1);
+        st.u0 = (cl == 0 ? 0 : sp.W0) + c[e] * p.H_kv + h * (c[e + 1] - c[e]);
+        if (st.s.group) st.u0 += st.k * (((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0);
+        else st.u0 += (int)cost_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
+        fill(p, st);
         return st;
     }
-    // The next stream with keys after st; false if there is none.
-    __device__ static bool next(const RaggedParams& p, Stream& st) {
-        const int TQ = RT >> p.lgG;
+    // The next stream of class cl after st; false if there is none.
+    __device__ static bool next(const RaggedParams& p, Stream& st, int cl) {
+        const int lq = LRT - p.lgG;
         st.u0 += st.n + RAGGED_C0;
-        if ((int64_t)(st.k + 1) * TQ < st.s.T) {
+        if (((int64_t)(st.k + 1) << lq) < st.s.T) {
             ++st.k;
         } else {
             st.k = 0;
             if (++st.h == p.H_kv) {
                 st.h = 0;
-                while (true) {
-                    if (++st.idx == (st.type == 0 ? p.NG : p.B)) {
-                        if (st.type == 1) return false;
-                        st.type = 1;
-                        st.idx = 0;
-                    }
-                    st.s = st.type == 0 ? group_info(p, st.idx) : seq_info(p, st.idx);
-                    if (st.s.ok) break;
-                }
+                do {
+                    if (++st.e == p.NG + p.B) return false;
+                    st.s = entry_of(p, st.e);
+                } while (!st.s.ok || cls(p, st.s) != cl);
             }
         }
-        fill(st, TQ);
+        fill(p, st);
         return true;
     }
 
-    // A CTA's piece of a stream.
+    // A worker's piece of a stream.
     struct Seg {
         int n;           // key tiles (0: no more segments)
         int seq, h;      // table row, KV head
@@ -262,108 +398,84 @@ struct Ragged {
         int kv0;         // position of its first key tile
         int kv_end;      // positions [kv0, kv_end) exist for the stream
         int lim0, causal;  // row of token i sees positions below min(kv_end, lim0 + i * causal)
-        int dst;         // 0 out, 1 / 2 row buffer 0 / 1, 3 / 4 slot 0 / 1 of the CTA
+        int dst;         // -1 out, -2 / -3 row buffer 0 / 1, else the slot
+        int cl;          // class
     };
-    // The part [x, x1) of stream st as a segment (n = 0 if it holds no tile).
-    __device__ static Seg segment(const RaggedParams& p, const Stream& st, int64_t x, int64_t x1) {
-        const int TQ = RT >> p.lgG;
+    // The part [x, x1) of stream st as a segment (n = 0 if it holds no tile).  own: the worker
+    // (as `owner` counts).
+    __device__ static Seg segment(const RaggedParams& p, const Stream& st, int cl, int own, int x, int x1) {
+        const int lq = LRT - p.lgG;
         Seg g;
-        const int64_t a = x - st.u0 - RAGGED_C0, b = x1 - st.u0 - RAGGED_C0;
-        const int j0 = a < 0 ? 0 : (int)a, j1 = b < 0 ? 0 : (b > st.n ? st.n : (int)b);
+        const int j0 = max(x - st.u0 - RAGGED_C0, 0), j1 = min(max(x1 - st.u0 - RAGGED_C0, 0), st.n);
         g.n = j1 - j0;
-        g.seq = st.type == 0 ? __ldg(p.groups + st.idx) : st.idx;
+        g.cl = cl;
+        g.seq = st.s.seq;
         g.h = st.h;
-        g.row0 = st.s.row0 + st.k * TQ;
-        g.ntok = min(TQ, st.s.T - st.k * TQ);
-        const int first = st.type == 0 ? 0 : st.s.pfx;
-        g.kv0 = first + j0 * KT;
-        if (st.type == 0) {
+        g.row0 = st.s.row0 + (st.k << lq);
+        g.ntok = min(1 << lq, st.s.T - (st.k << lq));
+        g.kv0 = (st.s.group ? 0 : st.s.pfx) + (j0 << LKT);
+        if (st.s.group) {
             g.kv_end = st.s.pfx;
             g.lim0 = st.s.pfx;
             g.causal = 0;
         } else {
-            const int S = st.s.L - st.s.T + st.k * TQ;  // position of the tile's first token
+            const int S = st.s.L - st.s.T + (st.k << lq);  // position of the tile's first token
             g.kv_end = S + g.ntok;
             g.lim0 = S + 1;
             g.causal = 1;
         }
-        const bool joint = st.s.pfx > 0;  // (a prefix stream always is)
-        if (j0 > 0) g.dst = 3;
-        else if (joint) g.dst = 1 + st.type;
-        else g.dst = j1 == st.n ? 0 : 4;
+        if (j0 > 0) g.dst = slot(cl, own, true);
+        else if (st.s.pfx > 0) g.dst = st.s.group ? -2 : -3;  // rows shared with another stream
+        else g.dst = j1 == st.n ? -1 : slot(cl, own, false);
         return g;
+    }
+
+    // A worker's segments, in order.
+    struct Walk {
+        Stream st;
+        int x, x1, own, cl;
+        bool cut;  // the last segment is the first piece of a stream that others share no rows with
+    };
+    __device__ static Walk walk(const RaggedParams& p, const Split& sp, const int* c, int i, int w) {
+        Walk k;
+        range(sp, i, w, k.x, k.x1);
+        k.cl = w == 0 ? 0 : 1;
+        k.own = PAIRS && w > 0 ? 2 * i + (w - 1) : i;
+        k.cut = false;
+        if (k.x < k.x1) k.st = locate(p, sp, c, k.x);
+        return k;
+    }
+    __device__ static Seg next_seg(const RaggedParams& p, Walk& k) {
+        Seg g;
+        g.n = 0;
+        g.cl = k.cl;
+        while (g.n == 0 && k.x < k.x1) {
+            g = segment(p, k.st, k.cl, k.own, k.x, k.x1);
+            k.cut = g.n > 0 && k.st.s.pfx == 0 && g.dst >= 0 && g.kv0 == 0;
+            k.x = k.st.u0 + RAGGED_C0 + k.st.n;
+            if (k.x < k.x1 && !next(p, k.st, k.cl)) k.x = k.x1;
+        }
+        return g;
+    }
+    // Leaves the cut stream that ends worker w's range (k.cut, g its last segment) for the merge:
+    // entry 3 i + w is (pieces, first owner, class, packed row), (rows of the tile, KV head).
+    __device__ static void leave_cut(const RaggedParams& p, const Split& sp, const Walk& k, int i, int w, const Seg& g) {
+        const int last = owner(sp, k.st.u0 + RAGGED_C0 + k.st.n - 1);
+        p.cuts[2 * (3 * i + w)] = make_int4(last - k.own + 1, k.own, k.cl, g.row0);
+        p.cuts[2 * (3 * i + w) + 1] = make_int4(g.ntok << p.lgG, g.h, 0, 0);
     }
 };
 
-__device__ __forceinline__ int64_t ragged_ctas(int64_t U, int P, int min_units) {
-    const int64_t want = (U + min_units - 1) / min_units;
-    return want < P ? want : P;
-}
-
-// cu and groups ascend within their bounds?  Every thread of the block takes part.
-__device__ __forceinline__ bool ragged_valid(const RaggedParams& p, int tid, int nthreads) {
-    bool bad = false;
-    for (int b = tid; b <= p.B; b += nthreads) {
-        const int c = __ldg(p.cu + b);
-        bad |= b == 0 ? c != 0 : c < __ldg(p.cu + b - 1);
-        bad |= c > p.N;
-    }
-    for (int g = tid; g <= p.NG && p.NG > 0; g += nthreads) {
-        const int c = __ldg(p.groups + g);
-        bad |= g == 0 ? c != 0 : c < __ldg(p.groups + g - 1);
-        bad |= g == p.NG ? c != p.B : c > p.B;
-    }
-    return __syncthreads_or(bad) == 0;
-}
-
-// Per-head cost prefix sums gc[NG + 1], sc[B + 1] in shared memory (every thread of the block;
-// tmp: 32 int64).  Returns the total cost U.
-template <int RT, int KT>
-__device__ __forceinline__ int64_t ragged_scan(const RaggedParams& p, int64_t* gc, int64_t* sc, int64_t* tmp, int tid,
-                                               int nthreads) {
-    using R = Ragged<RT, KT>;
-    const int TQ = RT >> p.lgG, lane = tid & 31, warp = tid >> 5, nw = nthreads >> 5;
-    int64_t total[2] = {0, 0};
-#pragma unroll 1
-    for (int ty = 0; ty < 2; ++ty) {
-        const int n = ty == 0 ? p.NG : p.B;
-        int64_t* c = ty == 0 ? gc : sc;
-        int64_t carry = 0;
-        if (tid == 0) c[0] = 0;
-        for (int i0 = 0; i0 < n; i0 += nthreads) {
-            const int i = i0 + tid;
-            int64_t v = 0;
-            if (i < n) v = ty == 0 ? R::group_cost(group_info(p, i), TQ) : R::seq_cost(seq_info(p, i), TQ);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
-                if (lane >= o) v += t;
-            }
-            if (lane == 31) tmp[warp] = v;
-            __syncthreads();
-            int64_t before = carry, all = carry;
-            for (int w = 0; w < nw; ++w) {
-                if (w < warp) before += tmp[w];
-                all += tmp[w];
-            }
-            if (i < n) c[i + 1] = before + v;
-            carry = all;
-            __syncthreads();
-        }
-        total[ty] = carry;
-    }
-    return (total[0] + total[1]) * p.H_kv;
-}
-
-// Zero output rows of the sequences that cannot be attended (CTA-strided over sequences).
+// Zero output rows of the sequences that cannot be attended (CTA-strided over sequences, thread tid
+// of n).
 template <typename T>
-__device__ __forceinline__ void ragged_zero_rows(const RaggedParams& p, int tid, int nthreads) {
+__device__ __forceinline__ void ragged_zero_rows(const RaggedParams& p, int tid, int n) {
     const int vecs = p.H_q * p.D * Elem<T>::BYTES / 16;
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const SeqInfo s = seq_info(p, b);
-        if (s.T <= 0 || s.ok) continue;
+        const Entry s = seq_entry(p, b);
+        if (!s.bad) continue;
         if (tid == 0) atomicOr(p.err, DEV_BAD_LENS);
-        for (int64_t i = tid; i < (int64_t)s.T * vecs; i += nthreads) {
+        for (int64_t i = tid; i < (int64_t)s.T * vecs; i += n) {
             const int64_t r = i / vecs;
             char* row = static_cast<char*>(p.out) + (s.row0 + r) * p.out_ts * Elem<T>::BYTES;
             reinterpret_cast<uint4*>(row)[i - r * vecs] = make_uint4(0, 0, 0, 0);
@@ -371,17 +483,16 @@ __device__ __forceinline__ void ragged_zero_rows(const RaggedParams& p, int tid,
     }
 }
 
-// Where the state of packed row `row`, head j (query-row r of its tile) of a segment with dst > 0
+// Where the state of packed row `row`, head j (query row r of its tile) of a segment with dst != -1
 // goes.
-template <typename S>
-__device__ __forceinline__ void ragged_dst(const RaggedParams& p, const S& g, int cta, int r, int64_t row, int j,
+__device__ __forceinline__ void ragged_dst(const RaggedParams& p, int dst, int slot_rows, int r, int64_t row, int j,
                                            float*& o, float*& ml) {
-    if (g.dst <= 2) {
-        const int64_t at = ((int64_t)(g.dst - 1) * p.N + row) * p.H_q + j;
+    if (dst < 0) {
+        const int64_t at = ((int64_t)(-2 - dst) * p.N + row) * p.H_q + j;
         o = p.row_o + at * p.D;
         ml = p.row_ml + at * 2;
     } else {
-        const int64_t at = ((int64_t)cta * 2 + (g.dst - 3)) * RAGGED_SLOT_ROWS + r;
+        const int64_t at = (int64_t)dst * slot_rows + r;
         o = p.slot_o + at * p.D;
         ml = p.slot_ml + at * 2;
     }
@@ -391,9 +502,10 @@ __device__ __forceinline__ void ragged_dst(const RaggedParams& p, const S& g, in
 
 // Launchers (kvc_ragged.cu, kvc_ragged_tc5.cu, kvc_rope.cu); each returns a cudaError_t.
 int launch_ragged_cc(int dtype, const RaggedParams& p, cudaStream_t s);
-// bf16, D = 64 or 128; q: make_q_tensor_map, k / v: the pool's maps with min(bs, 128)-row boxes.
-int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                      cudaStream_t s);
+// bf16, D = 64 or 128; q, q1: make_q_tensor_map with boxes of 64 rows and of max(16, G); k / v: the
+// pool's maps with min(bs, 128)-row boxes.
+int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& q1, const CUtensorMap& k,
+                      const CUtensorMap& v, cudaStream_t s);
 struct RopeTable {
     uint64_t freq[128];  // inv_freq in 2^-64 turns per position
     uint8_t axis[128];

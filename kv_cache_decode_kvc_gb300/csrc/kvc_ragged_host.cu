@@ -33,7 +33,11 @@ bool ragged_tc5(const kvc_cache* h) {
 }
 // CTAs of the attention kernels at most: the tensor-core kernel fills an SM, two blocks of the
 // CUDA-core kernel fit.
-int ragged_p(const kvc_cache* h) { return h->ctas > 0 ? h->ctas : 2 * h->sms; }
+int ragged_p(const kvc_cache* h, bool tc5) { return h->ctas > 0 ? h->ctas : (tc5 ? 1 : 2) * h->sms; }
+// Scratch of a path: the tensor-core kernel's CTAs hold five slots of 128 rows, the others' two of 64.
+kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, bool tc5) {
+    return kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h, tc5), tc5 ? 5 : 2, tc5 ? 128 : 64);
+}
 
 int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* table,
                 const int32_t* cu, const int32_t* lens, int N, const int32_t* groups, const int32_t* prefix, int NG,
@@ -43,8 +47,8 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     const int64_t row = (int64_t)h->H_q * h->D;
     if (!packed_ok(q, q_stride, row, h->es) || !packed_ok(out, out_stride, row, h->es)) return KVC_EINVAL;
     if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(ws, 256)) return KVC_EINVAL;
-    const int P = ragged_p(h);
-    const kvc::RaggedScratch sc = kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, P);
+    const bool tc5 = ragged_tc5(h);
+    const kvc::RaggedScratch sc = ragged_ws(h, N, NG, tc5);
     if (ws_bytes < sc.total) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;
@@ -62,7 +66,8 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.prefix = NG > 0 ? prefix : nullptr;
     p.err = h->err;
     char* w = static_cast<char*>(ws);
-    p.plan = reinterpret_cast<int64_t*>(w + sc.plan);
+    p.plan = reinterpret_cast<int*>(w + sc.plan);
+    p.cuts = reinterpret_cast<int4*>(w + sc.cuts);
     p.row_o = reinterpret_cast<float*>(w + sc.row_o);
     p.row_ml = reinterpret_cast<float*>(w + sc.row_ml);
     p.slot_o = reinterpret_cast<float*>(w + sc.slot_o);
@@ -78,14 +83,18 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.max_blocks = h->max_blocks;
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;
-    p.P = ragged_tc5(h) && h->ctas <= 0 ? h->sms : P;
-    p.min_units = h->ctas > 0 ? 1 : kvc::RAGGED_MIN_UNITS;
+    p.P = ragged_p(h, tc5);
+    p.min_units = h->ctas > 0 ? 2 : kvc::RAGGED_MIN_UNITS;
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
-    if (ragged_tc5(h)) {
-        CUtensorMap mq;
-        if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G)) return KVC_ECUDA;
+    if (tc5) {
+        // boxes of 64 query rows, and of as few as one token's
+        CUtensorMap mq, m1;
+        const int few = h->G > 16 ? h->G : 16;
+        if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G, 64 / h->G) ||
+            !kvc::make_q_tensor_map(&m1, q, N, h->H_q, h->D, q_stride, h->G, few / h->G))
+            return KVC_ECUDA;
         const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
-        return kvc::launch_ragged_tc5(p, mq, kv[0], kv[1], static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
+        return kvc::launch_ragged_tc5(p, mq, m1, kv[0], kv[1], static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
     }
     return kvc::launch_ragged_cc(h->dtype, p, static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
 }
@@ -176,7 +185,9 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
 
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes) {
     if (!h || !bytes || !h->paged || N < 1 || NG < 0 || NG > h->B) return KVC_EINVAL;
-    *bytes = kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h)).total;
+    // enough for either path, whatever kvc_set_math does in between
+    const uint64_t a = ragged_ws(h, N, NG, true).total, b = ragged_ws(h, N, NG, false).total;
+    *bytes = a > b ? a : b;
     return KVC_OK;
 }
 

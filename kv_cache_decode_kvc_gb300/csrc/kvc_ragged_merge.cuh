@@ -1,5 +1,5 @@
 // kvc_ragged_merge.cuh -- merge of the pieces of split streams (see kvc_ragged.cuh), launched
-// behind an attention kernel with tiles of RT rows and KT keys.
+// behind an attention kernel with the split R.
 #pragma once
 
 #include "kvc_ragged.cuh"
@@ -59,76 +59,64 @@ __device__ __forceinline__ void merge_row(const RaggedParams& p, int np, T* out,
     }
 }
 
-constexpr int MERGE_WARPS = 8;
+constexpr int MERGE_WARPS = 8, MERGE_SLICES = 8;
 
-// Without groups: block (i, s) takes the cut between CTAs i and i + 1; if that is the first cut
-// of a stream, its warps merge rows [MERGE_WARPS s, MERGE_WARPS (s + 1)) of the stream's tile.
-template <typename T, int RT, int KT>
+// Without groups: block (c, s) takes the c-th possible cut; if a stream was cut there first, its
+// warps merge every MERGE_SLICES-th eight rows of the stream's tile.
+template <typename T, class R>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const RaggedParams p) {
-    using R = Ragged<RT, KT>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t* sc = p.plan + p.NG + 1;
-    const int64_t U = sc[p.B] * p.H_kv;
-    if (U == 0) return;
-    const int64_t P = ragged_ctas(U, p.P, p.min_units);
-    const int64_t i = blockIdx.x;
-    if (i + 1 >= P) return;
-    const int64_t x = cta_begin(i + 1, U, P);
-    const typename R::Stream st = R::locate(p, p.plan, sc, x);
-    const int64_t t0 = st.u0 + RAGGED_C0;
-    if (x <= t0 || cta_of(t0, U, P) != i) return;
-    const int np = (int)(cta_of(t0 + st.n - 1, U, P) - i) + 1;
-    const int TQ = RT >> p.lgG, G = 1 << p.lgG;
-    const int r = blockIdx.y * MERGE_WARPS + warp;
-    if (r >= min(TQ, st.s.T - st.k * TQ) * G) return;
-    const int64_t row = st.s.row0 + st.k * TQ + (r >> p.lgG);
-    T* out = static_cast<T*>(p.out) + row * p.out_ts + (int64_t)(st.h * G + (r & (G - 1))) * p.D;
-    merge_row<T>(p, np, out, lane, [&](int q, const float*& o, const float*& ml) {
-        const int64_t at = ((i + q) * 2 + (q == 0 ? 1 : 0)) * RAGGED_SLOT_ROWS + r;
-        o = p.slot_o + at * p.D;
-        ml = p.slot_ml + at * 2;
-    });
+    const int4 a = __ldcg(p.cuts + 2 * blockIdx.x), b = __ldcg(p.cuts + 2 * blockIdx.x + 1);
+    if (a.x == 0) return;
+    const int G = 1 << p.lgG;
+    for (int r = blockIdx.y * MERGE_WARPS + warp; r < b.x; r += MERGE_SLICES * MERGE_WARPS) {
+        const int64_t row = a.w + (r >> p.lgG);
+        T* out = static_cast<T*>(p.out) + row * p.out_ts + (int64_t)(b.y * G + (r & (G - 1))) * p.D;
+        merge_row<T>(p, a.x, out, lane, [&](int q, const float*& o, const float*& ml) {
+            const int64_t at = (int64_t)R::slot(a.z, a.y + q, q > 0) * R::SLOT_ROWS + r;
+            o = p.slot_o + at * p.D;
+            ml = p.slot_ml + at * 2;
+        });
+    }
 }
 
 // With groups: block (row, KV head), a warp per query head of the group in turn; the row's
 // pieces are those of its prefix stream and of its sequence's own stream.
-template <typename T, int RT, int KT>
+template <typename T, class R>
 __global__ void __launch_bounds__(128) merge_rows_kernel(const RaggedParams p) {
-    using R = Ragged<RT, KT>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t *gc = p.plan, *sc = p.plan + p.NG + 1;
-    const int64_t U = (gc[p.NG] + sc[p.B]) * p.H_kv;
-    if (U == 0) return;
-    const int64_t P = ragged_ctas(U, p.P, p.min_units);
-    const int row = blockIdx.x, h = blockIdx.y, TQ = RT >> p.lgG, G = 1 << p.lgG;
+    const typename R::Split sp = R::planned(p);
+    if (!sp.valid) return;
+    const int row = blockIdx.x, h = blockIdx.y, G = 1 << p.lgG;
     if (row >= __ldg(p.cu + p.B)) return;
     int lo = 0, hi = p.B - 1;  // the sequence: largest b with cu[b] <= row
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (__ldg(p.cu + mid) <= row) lo = mid; else hi = mid - 1;
     }
-    const typename R::Stream own = R::of_row(p, gc, sc, 1, lo, h, row);
+    const typename R::Stream own = R::of_row(p, sp, p.plan, p.NG + lo, h, row);
     if (!own.s.ok) return;
-    const int64_t of = cta_of(own.u0 + RAGGED_C0, U, P), ol = cta_of(own.u0 + RAGGED_C0 + own.n - 1, U, P);
+    const int of = R::owner(sp, own.u0 + RAGGED_C0), ol = R::owner(sp, own.u0 + RAGGED_C0 + own.n - 1);
     const bool joint = own.s.pfx > 0;
-    if (!joint && of == ol) return;  // written by its CTA
-    int64_t pf = 0, pl = -1;
-    int pr = 0;
+    if (!joint && of == ol) return;  // written by its worker
+    int pf = 0, pl = -1, pr = 0, pc = 0;
+    const int oc = R::cls(p, own.s);
     if (joint) {
         int a = 0, b = p.NG - 1;
         while (a < b) {
             const int mid = (a + b + 1) >> 1;
             if (__ldg(p.groups + mid) <= lo) a = mid; else b = mid - 1;
         }
-        const typename R::Stream pre = R::of_row(p, gc, sc, 0, a, h, row);
-        pf = cta_of(pre.u0 + RAGGED_C0, U, P);
-        pl = cta_of(pre.u0 + RAGGED_C0 + pre.n - 1, U, P);
-        pr = (row - pre.s.row0 - pre.k * TQ) * G;
+        const typename R::Stream pre = R::of_row(p, sp, p.plan, a, h, row);
+        pf = R::owner(sp, pre.u0 + RAGGED_C0);
+        pl = R::owner(sp, pre.u0 + RAGGED_C0 + pre.n - 1);
+        pr = ((row - pre.s.row0) << p.lgG) & (R::RT - 1);
+        pc = R::cls(p, pre.s);
     }
-    const int orow = (row - own.s.row0 - own.k * TQ) * G;
-    const int n0 = (int)(pl - pf + 1), np = n0 + (int)(ol - of + 1);
+    const int orow = ((row - own.s.row0) << p.lgG) & (R::RT - 1);
+    const int n0 = pl - pf + 1, np = n0 + ol - of + 1;
     for (int g = warp; g < G; g += 4) {
         const int j = h * G + g;
         T* out = static_cast<T*>(p.out) + row * p.out_ts + (int64_t)j * p.D;
@@ -141,7 +129,7 @@ __global__ void __launch_bounds__(128) merge_rows_kernel(const RaggedParams p) {
                 o = p.row_o + at * p.D;
                 ml = p.row_ml + at * 2;
             } else {
-                at = (((pre ? pf : of) + c) * 2 + (c == 0 ? 1 : 0)) * RAGGED_SLOT_ROWS + (pre ? pr : orow) + g;
+                at = (int64_t)R::slot(pre ? pc : oc, (pre ? pf : of) + c, c > 0) * R::SLOT_ROWS + (pre ? pr : orow) + g;
                 o = p.slot_o + at * p.D;
                 ml = p.slot_ml + at * 2;
             }
@@ -150,7 +138,7 @@ __global__ void __launch_bounds__(128) merge_rows_kernel(const RaggedParams p) {
 }
 
 // Launch behind the attention kernel; starts as that one ends.
-template <typename T, int RT, int KT>
+template <typename T, class R>
 inline int launch_merge(const RaggedParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -161,14 +149,13 @@ inline int launch_merge(const RaggedParams& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e;
     if (p.NG == 0) {
-        if (p.P < 2) return 0;
-        cfg.gridDim = dim3((unsigned)(p.P - 1), RT / MERGE_WARPS);
+        cfg.gridDim = dim3((unsigned)(3 * p.P), MERGE_SLICES);
         cfg.blockDim = dim3(MERGE_WARPS * 32);
-        e = cudaLaunchKernelEx(&cfg, merge_cuts_kernel<T, RT, KT>, p);
+        e = cudaLaunchKernelEx(&cfg, merge_cuts_kernel<T, R>, p);
     } else {
         cfg.gridDim = dim3((unsigned)p.N, (unsigned)p.H_kv);
         cfg.blockDim = dim3(128);
-        e = cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, RT, KT>, p);
+        e = cudaLaunchKernelEx(&cfg, merge_rows_kernel<T, R>, p);
     }
     return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
