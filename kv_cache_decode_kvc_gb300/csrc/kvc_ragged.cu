@@ -11,18 +11,18 @@
 
 namespace kvc {
 
-template <int D_>
+template <int D_, bool JOINT>
 struct CcCfg {
     static constexpr int D = D_;
     static constexpr int LKT = D > 64 ? 5 : 6;
     static constexpr int RT = 64;
     static constexpr int KT = 1 << LKT;
-    using R = Ragged<6, LKT, false>;
+    using R = Ragged<6, LKT, false, JOINT>;
     static constexpr int NC = KT / 16;           // score columns of a thread
     static constexpr int NV = D < 64 ? 1 : D / 64;  // float4 output columns of a thread
     static constexpr int QS = D + 4, KS = D + 4, PS = KT + 4;  // row strides (floats)
     static constexpr int TILES = (RT * QS + KT * KS + KT * D + RT * PS) * 4;
-    static constexpr int PLAN = 2 * (2 * MAX_B + 1) * 4;  // the prefix sums lie under the tiles
+    static constexpr int PLAN = R::work_ints(MAX_B, MAX_B) * 4;  // the split's arrays lie under the tiles
     static constexpr int SMEM = TILES > PLAN ? TILES : PLAN;
 };
 
@@ -37,9 +37,9 @@ __device__ __forceinline__ void store_row16(float* dst, const uint4& v, float sc
             make_float4(f[i] * scale, f[i + 1] * scale, f[i + 2] * scale, f[i + 3] * scale);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool JOINT>
 __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
-    using C = CcCfg<D>;
+    using C = CcCfg<D, JOINT>;
     using R = typename C::R;
     extern __shared__ __align__(16) char smem[];
     __shared__ typename R::Seg seg_s;
@@ -51,22 +51,22 @@ __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int* c = reinterpret_cast<int*>(smem);
+    const typename R::Work work = R::work(p, smem);
     if (tid < 32) {
-        const typename R::Split sp = R::scan(p, c, tid);
+        const typename R::Split sp = R::scan(p, work, tid);
         if (tid == 0) split_s = sp;
     }
     __syncthreads();
     const typename R::Split sp = split_s;
     if (blockIdx.x == 0) {
-        const int n = 2 * (p.NG + p.B + 1);
-        for (int i = tid; i < n; i += 256) p.plan[i] = sp.valid ? c[i] : 0;
+        const int n = 2 * (R::groups(p) + p.B + 1);
+        for (int i = tid; i < n; i += 256) p.plan[i] = sp.valid ? work.c[i] : 0;
         if (!sp.valid && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
     }
     if (tid < 6) p.cuts[6 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
-    if (sp.valid) ragged_zero_rows<T>(p, tid, 256);
+    if (sp.valid) ragged_zero_rows<T, JOINT>(p, tid, 256);
     typename R::Walk wk;
-    if (tid == 0) wk = R::walk(p, sp, c, blockIdx.x, 1);
+    if (tid == 0) wk = R::walk(p, sp, work, blockIdx.x, 1);
 
     while (true) {
         __syncthreads();  // the prefix sums (or the last segment's tiles) are read
@@ -233,12 +233,12 @@ __global__ void __launch_bounds__(256) ragged_cc_kernel(const RaggedParams p) {
     }
 }
 
-template <typename T, int D>
-static int launch_cc(const RaggedParams& p, cudaStream_t s) {
-    using C = CcCfg<D>;
+template <typename T, int D, bool JOINT>
+static int launch_cc_as(const RaggedParams& p, cudaStream_t s) {
+    using C = CcCfg<D, JOINT>;
     static PerDeviceOnce once;
     const int e0 = once.run([] {
-        return (int)cudaFuncSetAttribute(ragged_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return (int)cudaFuncSetAttribute(ragged_cc_kernel<T, D, JOINT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e0 != 0) return e0;
     cudaLaunchConfig_t cfg = {};
@@ -251,9 +251,13 @@ static int launch_cc(const RaggedParams& p, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_cc_kernel<T, D>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_cc_kernel<T, D, JOINT>, p);
     if (e != cudaSuccess) return (int)e;
-    return launch_merge<T, typename C::R>(p, s);
+    return launch_merge<T, typename C::R, JOINT>(p, s);
+}
+template <typename T, int D>
+static int launch_cc(const RaggedParams& p, cudaStream_t s) {
+    return p.NG > 0 ? launch_cc_as<T, D, true>(p, s) : launch_cc_as<T, D, false>(p, s);
 }
 
 int launch_ragged_cc(int dtype, const RaggedParams& p, cudaStream_t s) {

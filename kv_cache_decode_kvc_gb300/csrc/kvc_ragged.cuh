@@ -34,7 +34,7 @@
 namespace kvc {
 
 constexpr int RAGGED_C0 = 1;         // cost of a stream's start, in tiles
-constexpr int RAGGED_MIN_UNITS = 4;  // fewer CTAs when a CTA's share would drop below this
+constexpr int RAGGED_LG_MIN = 2;     // fewer CTAs when a CTA's share would drop below 4 units
 constexpr int PAIR_ROWS = 64;
 
 struct RaggedParams {
@@ -58,7 +58,8 @@ struct RaggedParams {
     int B, N, H_q, H_kv, lgG, NG, D;
     int bs, max_blocks, num_blocks, T_max;
     int P;          // CTAs at most
-    int min_units;  // cost units per CTA at least (2 or more: no worker between two pieces is empty)
+    int lg_min;     // log2 of the cost units per CTA at least (1 or more: no worker between two pieces is
+                    // empty)
     float qscale;   // log2(e) / sqrt(D)
 };
 
@@ -91,22 +92,6 @@ inline RaggedScratch ragged_scratch(int B, int N, int NG, int H_q, int D, int P,
 #ifdef __CUDACC__
 
 // ------------------------------------------------------------------ entries and streams
-// Cost units are 32-bit (a call with 2^31 of them, hours of work, is refused): CTA i of P takes
-// U / P units, the first U % P one more.
-__device__ __forceinline__ int rg_begin(int i, int U, int P) {
-    const int each = (int)((unsigned)U / (unsigned)P), more = U - each * P;
-    return i * each + min(i, more);
-}
-__device__ __forceinline__ int rg_cta(int x, int U, int P) {
-    const int each = (int)((unsigned)U / (unsigned)P), more = U - each * P;
-    const int y = x - more * (each + 1);
-    return y < 0 ? (int)((unsigned)x / (unsigned)(each + 1)) : more + (int)((unsigned)y / (unsigned)each);
-}
-__device__ __forceinline__ int ragged_ctas(int U, int P, int min_units) {
-    const int want = (int)((unsigned)U / (unsigned)min_units);
-    return want < 1 ? 1 : min(want, P);
-}
-
 struct Entry {
     int row0, T;  // packed rows [row0, row0 + T)
     int L, pfx;   // positions; shared prefix in effect (whole blocks, 0: none)
@@ -116,157 +101,223 @@ struct Entry {
     bool bad;     // a sequence with rows that cannot be attended (its outputs are zero)
 };
 
-// Shared prefix of sequence b: in effect (whole blocks; a group of one shares nothing) and as
-// given (-1 if out of range).
-__device__ __forceinline__ int2 seq_prefix(const RaggedParams& p, int b) {
-    if (p.groups == nullptr) return make_int2(0, 0);
-    int lo = 0, hi = p.NG - 1;  // largest g with groups[g] <= b
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.groups + mid) <= b) lo = mid; else hi = mid - 1;
-    }
-    const int P = __ldg(p.prefix + lo);
-    if (P < 0 || P > p.T_max) return make_int2(0, -1);
-    const bool one = __ldg(p.groups + lo + 1) - __ldg(p.groups + lo) < 2;
-    return make_int2(one ? 0 : P / p.bs * p.bs, P);
+// Shared prefix of group g of sequences [b0, b1): in effect (whole blocks; a group of one shares
+// nothing); P as given may be out of range.
+__device__ __forceinline__ int prefix_used(const RaggedParams& p, int b0, int b1, int P) {
+    return (b1 - b0 < 2 || P < 0 || P > p.T_max) ? 0 : P / p.bs * p.bs;
 }
-__device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b) {
+__device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b, int row0, int row1, int L, int P, int used) {
     Entry s;
-    s.row0 = __ldg(p.cu + b);
-    const int r1 = __ldg(p.cu + b + 1);
-    s.L = __ldg(p.lens + b);
-    s.T = r1 - s.row0;
-    const int2 pf = seq_prefix(p, b);
-    s.pfx = pf.x;
+    s.row0 = row0;
+    s.T = row1 - row0;
+    s.L = L;
+    s.pfx = used;
     s.seq = b;
     s.group = false;
-    s.ok = s.T > 0 && s.L >= s.T && s.L <= p.T_max && pf.y >= 0 && s.L - s.T >= pf.y;
+    s.ok = s.T > 0 && L >= s.T && L <= p.T_max && P >= 0 && P <= p.T_max && L - s.T >= P;
     s.bad = s.T > 0 && !s.ok;
     return s;
 }
-__device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
-    const int b0 = __ldg(p.groups + g), b1 = __ldg(p.groups + g + 1), P = __ldg(p.prefix + g);
+__device__ __forceinline__ Entry group_entry(int b0, int row0, int row1, int used) {
     Entry s;
-    s.row0 = __ldg(p.cu + b0);
-    s.T = __ldg(p.cu + b1) - s.row0;
-    s.pfx = (b1 - b0 < 2 || P < 0 || P > p.T_max) ? 0 : P / p.bs * p.bs;
-    s.L = s.pfx;
+    s.row0 = row0;
+    s.T = row1 - row0;
+    s.L = s.pfx = used;
     s.seq = b0;
     s.group = true;
-    s.ok = s.T > 0 && s.pfx > 0;
+    s.ok = s.T > 0 && used > 0;
     s.bad = false;
     return s;
 }
-__device__ __forceinline__ Entry entry_of(const RaggedParams& p, int e) {
-    return e < p.NG ? group_entry(p, e) : seq_entry(p, e - p.NG);
+// The same from the arrays in memory.
+template <bool JOINT>
+__device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b) {
+    const int row0 = __ldg(p.cu + b), row1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
+    int P = 0, used = 0;
+    if (JOINT) {
+        int lo = 0, hi = p.NG - 1;  // largest g with groups[g] <= b
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldg(p.groups + mid) <= b) lo = mid; else hi = mid - 1;
+        }
+        P = __ldg(p.prefix + lo);
+        used = prefix_used(p, __ldg(p.groups + lo), __ldg(p.groups + lo + 1), P);
+    }
+    return seq_entry(p, b, row0, row1, L, P, used);
+}
+__device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
+    const int b0 = __ldg(p.groups + g), b1 = __ldg(p.groups + g + 1), P = __ldg(p.prefix + g);
+    return group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), prefix_used(p, b0, b1, P));
 }
 
 // sum of ceil(x / 2^lg) for x = 1 .. X
-__device__ __forceinline__ int64_t ceil_sum(int64_t X, int lg) {
-    const int64_t n = X >> lg, r = X & ((1 << lg) - 1);
-    return ((n * (n + 1) / 2) << lg) + r * (n + 1);
+__device__ __forceinline__ int triangle(int n) { return ((n + 1) >> 1) * (n | 1); }  // 1 + .. + n
+__device__ __forceinline__ int ceil_sum(int X, int lg) {
+    const int n = X >> lg;
+    return (triangle(n) << lg) + (X & ((1 << lg) - 1)) * (n + 1);
 }
 
 // Work split.  LRT, LKT: log2 of a stream's rows and of a key tile; PAIRS: classes as the
-// tensor-core kernel has them, and two workers per CTA for class 1.
-template <int LRT, int LKT, bool PAIRS>
+// tensor-core kernel has them, and two workers per CTA for class 1; JOINT: the call has groups.
+// (A CTA starts with a cold instruction cache, where code costs several times its warm time:
+// the split's is kept short, and without groups their part is compiled out.)
+template <int LRT, int LKT, bool PAIRS, bool JOINT>
 struct Ragged {
     static constexpr int RT = 1 << LRT, KT = 1 << LKT;
     // scratch slots of a CTA: with PAIRS five of 128 rows (a shared stream's later piece takes 0-1,
     // its first piece 2-3 and then ends the range; set 0: 0 and 2, set 1: 3 and 4)
     static constexpr int SLOTS = PAIRS ? 5 : 2, SLOT_ROWS = PAIRS ? RT / 2 : RT;
 
+    __device__ static int groups(const RaggedParams& p) { return JOINT ? p.NG : 0; }
+    __device__ static Entry entry_of(const RaggedParams& p, int e) {
+        if (JOINT && e < p.NG) return group_entry(p, e);
+        return seq_entry<JOINT>(p, e - groups(p));
+    }
     __device__ static int cls(const RaggedParams& p, const Entry& s) {
         return PAIRS && ((int64_t)s.T << p.lgG) > PAIR_ROWS ? 0 : 1;
     }
     // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
-    __device__ static int tiles(int S0, int t1) { return (int)(((int64_t)S0 + t1 + KT - 1) >> LKT); }
-    // Cost of its first k streams, all full (TQ = 2^lq tokens each):
-    // sum over i = 1 .. k of ceil((S0 + i TQ) / KT), and the starts.
-    __device__ static int64_t cost_full(int S0, int64_t k, int lq) {
-        if (lq >= LKT)
-            return k * ((S0 + KT - 1) >> LKT) + ((k * (k + 1) / 2) << (lq - LKT)) + k * RAGGED_C0;
+    __device__ static int tiles(int S0, int t1) { return (int)(((unsigned)S0 + (unsigned)t1 + KT - 1) >> LKT); }
+    // Costs are 32-bit (a call of 2^31 units, hours of work, is refused: scan).  Cost of an entry's first k
+    // streams, all full (TQ = 2^lq tokens each): sum over i = 1 .. k of ceil((S0 + i TQ) / KT),
+    // and the starts.
+    __device__ static int cost_full(int S0, int k, int lq) {
+        if (lq >= LKT) return k * ((int)((unsigned)(S0 + KT - 1) >> LKT) + RAGGED_C0) + (triangle(k) << (lq - LKT));
         // ceil((S0 + i TQ) / KT) = ceil((ceil(S0 / TQ) + i) / (KT / TQ))
-        const int64_t s = (S0 + (1 << lq) - 1) >> lq;
+        const int s = (int)((unsigned)(S0 + (1 << lq) - 1) >> lq);
         return ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq) + k * RAGGED_C0;
     }
-    __device__ static int64_t cost(const RaggedParams& p, const Entry& s) {
+    __device__ static int cost(const RaggedParams& p, const Entry& s) {
         if (!s.ok) return 0;
-        const int lq = LRT - p.lgG, nk = (s.T + (1 << lq) - 1) >> lq;
-        if (s.group) return (int64_t)nk * (((s.pfx + KT - 1) >> LKT) + RAGGED_C0);
+        const int lq = LRT - p.lgG, nk = (int)((unsigned)(s.T + (1 << lq) - 1) >> lq);
+        if (JOINT && s.group) return nk * (((s.pfx + KT - 1) >> LKT) + RAGGED_C0);
         const int S0 = s.L - s.T - s.pfx;
         return cost_full(S0, nk - 1, lq) + tiles(S0, s.T) + RAGGED_C0;
     }
+    // The same to a few parts in a million, without wrapping.
+    __device__ static float cost_about(const RaggedParams& p, const Entry& s) {
+        if (!s.ok) return 0.f;
+        const float nk = (float)s.T / (float)(RT >> p.lgG) + 1.f, own = (float)(JOINT && s.group ? s.pfx : s.L - s.pfx);
+        return nk * (own / KT + 1.f + RAGGED_C0);
+    }
 
     // The batch's split: total cost U, class 0's part W0, CTAs P.
+    // CTA i of P takes `each` units, the first `more` of them one more.
     struct Split {
-        int U, W0, P;
+        int U, W0, P, each, more;
         bool valid;
     };
-    // One warp computes the per-head cost prefix sums c[0 .. NE], c[NE + 1 .. 2 NE + 1] of the two
-    // classes (NE = NG + B) and checks that cu and the groups ascend within their bounds.
-    __device__ static Split scan(const RaggedParams& p, int* c, int lane) {
-        const int NE = p.NG + p.B;
+    __device__ static void divide(const RaggedParams& p, Split& sp) {
+        const int want = sp.U >> p.lg_min;
+        sp.P = sp.U == 0 ? 0 : max(1, min(want, p.P));
+        sp.each = sp.U == 0 ? 0 : (int)((unsigned)sp.U / (unsigned)sp.P);
+        sp.more = sp.U - sp.each * sp.P;
+    }
+    __device__ static int begin(const Split& sp, int i) { return i * sp.each + min(i, sp.more); }
+    __device__ static int cta(const Split& sp, int x) {
+        const int y = x - sp.more * (sp.each + 1);
+        return y < 0 ? (int)((unsigned)x / (unsigned)(sp.each + 1)) : sp.more + (int)((unsigned)y / (unsigned)sp.each);
+    }
+    // What one warp computes in shared memory (work_ints of it): the per-head cost prefix sums
+    // c[0 .. NE], c[NE + 1 .. 2 NE + 1] of the two classes (NE = NG + B), the entries, a copy of the
+    // groups.
+    struct Work {
+        int4* ent;  // (row0, T, L, pfx and flags: sequence ok 1)
+        int *c, *groups, *prefix;
+    };
+    static constexpr int work_ints(int B, int NG) { return 4 * (B + NG) + 2 * (B + NG + 1) + 2 * NG + 1; }
+    __device__ static Work work(const RaggedParams& p, void* smem) {
+        const int NE = groups(p) + p.B;
+        Work k;
+        k.ent = static_cast<int4*>(smem);
+        k.c = reinterpret_cast<int*>(k.ent + NE);
+        k.groups = k.c + 2 * (NE + 1);
+        k.prefix = k.groups + p.NG + 1;
+        return k;
+    }
+    // ... and whether cu and the groups ascend within their bounds.
+    __device__ static Split scan(const RaggedParams& p, const Work& k, int lane) {
+        const int NE = groups(p) + p.B;
+        int* c = k.c;
         int carry[2] = {0, 0};
-        float sum = 0.f;  // the cost in fp32: 32-bit sums that would wrap are refused
+        float about = 0.f;  // the total cost: sums that 32 bits do not hold are refused
         bool bad = false;
         if (lane < 2) c[lane * (NE + 1)] = 0;
-        for (int e0 = 0; e0 < NE; e0 += 32) {
+        for (int g = lane; JOINT && g <= p.NG; g += 32) {
+            const int b0 = __ldg(p.groups + g);
+            bad |= b0 < 0 || b0 > p.B || (g == 0 && b0 != 0) || (g == p.NG && b0 != p.B);
+            k.groups[g] = b0;
+            if (g < p.NG) k.prefix[g] = __ldg(p.prefix + g);
+        }
+        if (JOINT) bad = __any_sync(0xFFFFFFFFu, bad);
+        for (int e0 = 0; e0 < NE && !bad; e0 += 32) {
             const int e = e0 + lane;
-            int64_t v0 = 0;
-            int cl = 1;
-            bool fine = false;
-            if (e < p.NG) {
-                const int b0 = __ldg(p.groups + e), b1 = __ldg(p.groups + e + 1);
-                fine = b0 >= 0 && b1 >= b0 && b1 <= p.B && (e > 0 || b0 == 0) && (e < p.NG - 1 || b1 == p.B);
+            Entry s;
+            s.ok = false;
+            bool fine = e >= NE;
+            if (JOINT && e < p.NG) {
+                const int b0 = k.groups[e], b1 = k.groups[e + 1];
+                fine = b1 >= b0;
+                if (fine) s = group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), prefix_used(p, b0, b1, k.prefix[e]));
             } else if (e < NE) {
-                const int c0 = __ldg(p.cu + e - p.NG), c1 = __ldg(p.cu + e - p.NG + 1);
-                fine = c0 >= 0 && c1 >= c0 && c1 <= p.N && (e > p.NG || c0 == 0);
-            }
-            if (fine) {
-                const Entry s = entry_of(p, e);
-                v0 = cost(p, s);
-                cl = cls(p, s);
-            }
-            bad |= !fine && e < NE;
-            sum += (float)v0;
-            const int v = (int)v0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (!PAIRS && k == 0) {
-                    if (e < NE) c[e + 1] = 0;
-                    continue;
+                const int b = e - groups(p), c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
+                fine = c0 >= 0 && c1 >= c0 && c1 <= p.N && (b > 0 || c0 == 0);
+                int P = 0, used = 0;
+                if (JOINT) {
+                    int lo = 0, hi = p.NG - 1;  // largest g with groups[g] <= b
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (k.groups[mid] <= b) lo = mid; else hi = mid - 1;
+                    }
+                    P = k.prefix[lo];
+                    used = prefix_used(p, k.groups[lo], k.groups[lo + 1], P);
                 }
-                int x = cl == k ? v : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int t = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                    if (lane >= o) x += t;
-                }
-                if (e < NE) c[k * (NE + 1) + e + 1] = carry[k] + x;
-                carry[k] += __shfl_sync(0xFFFFFFFFu, x, 31);
+                s = seq_entry(p, b, c0, c1, L, P, used);
             }
+            bad |= !fine;
+            int x[2] = {0, 0};
+            if (fine && e < NE) {
+                x[cls(p, s)] = cost(p, s);
+                about += cost_about(p, s);
+                k.ent[e] = make_int4(s.row0, s.T, s.L, s.pfx);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t1 = __shfl_up_sync(0xFFFFFFFFu, x[1], o);
+                const int t0 = PAIRS ? __shfl_up_sync(0xFFFFFFFFu, x[0], o) : 0;
+                if (lane >= o) {
+                    x[0] += t0;
+                    x[1] += t1;
+                }
+            }
+            if (e < NE) {
+                c[e + 1] = carry[0] + x[0];
+                c[NE + 1 + e + 1] = carry[1] + x[1];
+            }
+            carry[0] += PAIRS ? __shfl_sync(0xFFFFFFFFu, x[0], 31) : 0;
+            carry[1] += __shfl_sync(0xFFFFFFFFu, x[1], 31);
+            bad = __any_sync(0xFFFFFFFFu, bad);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        bad |= sum * (float)p.H_kv > 2.1e9f;
+        for (int o = 16; o > 0; o >>= 1) about += __shfl_xor_sync(0xFFFFFFFFu, about, o);
+        bad |= about * (float)p.H_kv > 2.1e9f;
         Split sp;
-        sp.valid = !__any_sync(0xFFFFFFFFu, bad);
+        sp.valid = !bad;
         sp.W0 = sp.valid ? carry[0] * p.H_kv : 0;
         sp.U = sp.valid ? sp.W0 + carry[1] * p.H_kv : 0;
-        sp.P = sp.U > 0 ? ragged_ctas(sp.U, p.P, p.min_units) : 0;
+        divide(p, sp);
         __syncwarp();
         return sp;
     }
     // The split as the attention kernel left it in p.plan.
     __device__ static Split planned(const RaggedParams& p) {
-        const int NE = p.NG + p.B;
+        const int NE = groups(p) + p.B;
         Split sp;
         sp.W0 = p.plan[NE] * p.H_kv;
         sp.U = sp.W0 + p.plan[2 * NE + 1] * p.H_kv;
-        sp.P = sp.U > 0 ? ragged_ctas(sp.U, p.P, p.min_units) : 0;
         sp.valid = sp.U > 0;
+        divide(p, sp);
         return sp;
     }
 
@@ -275,7 +326,7 @@ struct Ragged {
     __device__ static void range(const Split& sp, int i, int w, int& a, int& b) {
         a = b = 0;
         if (i >= sp.P) return;
-        const int x0 = rg_begin(i, sp.U, sp.P), x1 = rg_begin(i + 1, sp.U, sp.P);
+        const int x0 = begin(sp, i), x1 = begin(sp, i + 1);
         if (w == 0) {
             a = x0;
             b = x1 < sp.W0 ? x1 : sp.W0;
@@ -291,7 +342,7 @@ struct Ragged {
     // The worker that owns unit x, as a position in the order of its class: CTA for class 0,
     // 2 CTA + set (CTA without PAIRS) for class 1.
     __device__ static int owner(const Split& sp, int x) {
-        const int i = rg_cta(x, sp.U, sp.P);
+        const int i = cta(sp, x);
         if (!PAIRS || x < sp.W0) return i;
         int a, b;
         range(sp, i, 2, a, b);
@@ -312,7 +363,7 @@ struct Ragged {
     };
     __device__ static void fill(const RaggedParams& p, Stream& st) {
         const int lq = LRT - p.lgG;
-        if (st.s.group) {
+        if (JOINT && st.s.group) {
             st.n = (st.s.pfx + KT - 1) >> LKT;
         } else {
             const int64_t t1 = (int64_t)(st.k + 1) << lq;
@@ -320,8 +371,9 @@ struct Ragged {
         }
     }
     // The stream holding cost unit x.
-    __device__ static Stream locate(const RaggedParams& p, const Split& sp, const int* c, int x) {
-        const int NE = p.NG + p.B, lq = LRT - p.lgG;
+    __device__ static Stream locate(const RaggedParams& p, const Split& sp, const Work& k, int x) {
+        const int NE = groups(p) + p.B, lq = LRT - p.lgG;
+        const int* c = k.c;
         Stream st;
         const int base = x < sp.W0 ? 0 : sp.W0;
         if (x >= sp.W0) c += NE + 1;
@@ -331,32 +383,45 @@ struct Ragged {
             if (c[mid] * p.H_kv <= x - base) lo = mid; else hi = mid - 1;
         }
         st.e = lo;
-        st.s = entry_of(p, lo);
+        const int4 w = k.ent[lo];
+        st.s.row0 = w.x;
+        st.s.T = w.y;
+        st.s.L = w.z;
+        st.s.pfx = w.w;
+        st.s.group = JOINT && lo < p.NG;
+        st.s.seq = JOINT && st.s.group ? k.groups[lo] : lo - groups(p);
+        st.s.ok = true;
+        st.s.bad = false;
         const int per = c[lo + 1] - c[lo];
         int r = x - base - c[lo] * p.H_kv;
         st.h = (int)((unsigned)r / (unsigned)per);
         r -= st.h * per;
         st.u0 = base + c[lo] * p.H_kv + st.h * per;
-        if (st.s.group) {
+        if (JOINT && st.s.group) {
             const int one = ((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0;
             st.k = (int)((unsigned)r / (unsigned)one);
             st.u0 += st.k * one;
         } else {
-            const int S0 = st.s.L - st.s.T - st.s.pfx;
-            int a = 0, b = ((st.s.T + (1 << lq) - 1) >> lq) - 1;
-            while (a < b) {  // largest k with cost_full(k) <= r
-                const int mid = (a + b + 1) >> 1;
-                if (cost_full(S0, mid, lq) <= r) a = mid; else b = mid - 1;
+            // largest k with cost_full(k) <= r: by the real root of k^2 TQ / 2 + k (S0 + KT (C0 + 1/2)) = r KT,
+            // then steps (the ceilings differ from the half-tile by less than one stream's cost)
+            const int S0 = st.s.L - st.s.T - st.s.pfx, last = (int)((unsigned)(st.s.T + (1 << lq) - 1) >> lq) - 1;
+            int a = 0;
+            if (last > 0) {
+                const float TQ = (float)(1 << lq), b1 = (float)S0 + 0.5f * TQ + KT * (RAGGED_C0 + 0.5f);
+                const float root = (sqrtf(b1 * b1 + 2.f * TQ * KT * (float)r) - b1) / TQ;
+                a = min(max((int)root, 0), last);
+                while (a > 0 && cost_full(S0, a, lq) > r) --a;
+                while (a < last && cost_full(S0, a + 1, lq) <= r) ++a;
             }
             st.k = a;
-            st.u0 += (int)cost_full(S0, a, lq);
+            st.u0 += cost_full(S0, a, lq);
         }
         fill(p, st);
         return st;
     }
     // The stream of packed row `row` of entry e.
     __device__ static Stream of_row(const RaggedParams& p, const Split& sp, const int* c, int e, int h, int row) {
-        const int NE = p.NG + p.B, lq = LRT - p.lgG;
+        const int NE = groups(p) + p.B, lq = LRT - p.lgG;
         Stream st;
         st.e = e;
         st.h = h;
@@ -365,8 +430,8 @@ struct Ragged {
         const int cl = cls(p, st.s);
         c += cl * (NE + 1);
         st.u0 = (cl == 0 ? 0 : sp.W0) + c[e] * p.H_kv + h * (c[e + 1] - c[e]);
-        if (st.s.group) st.u0 += st.k * (((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0);
-        else st.u0 += (int)cost_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
+        if (JOINT && st.s.group) st.u0 += st.k * (((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0);
+        else st.u0 += cost_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
         fill(p, st);
         return st;
     }
@@ -381,7 +446,7 @@ struct Ragged {
             if (++st.h == p.H_kv) {
                 st.h = 0;
                 do {
-                    if (++st.e == p.NG + p.B) return false;
+                    if (++st.e == groups(p) + p.B) return false;
                     st.s = entry_of(p, st.e);
                 } while (!st.s.ok || cls(p, st.s) != cl);
             }
@@ -413,8 +478,8 @@ struct Ragged {
         g.h = st.h;
         g.row0 = st.s.row0 + (st.k << lq);
         g.ntok = min(1 << lq, st.s.T - (st.k << lq));
-        g.kv0 = (st.s.group ? 0 : st.s.pfx) + (j0 << LKT);
-        if (st.s.group) {
+        g.kv0 = (JOINT && st.s.group ? 0 : st.s.pfx) + (j0 << LKT);
+        if (JOINT && st.s.group) {
             g.kv_end = st.s.pfx;
             g.lim0 = st.s.pfx;
             g.causal = 0;
@@ -425,7 +490,7 @@ struct Ragged {
             g.causal = 1;
         }
         if (j0 > 0) g.dst = slot(cl, own, true);
-        else if (st.s.pfx > 0) g.dst = st.s.group ? -2 : -3;  // rows shared with another stream
+        else if (JOINT && st.s.pfx > 0) g.dst = st.s.group ? -2 : -3;  // rows shared with another stream
         else g.dst = j1 == st.n ? -1 : slot(cl, own, false);
         return g;
     }
@@ -434,26 +499,29 @@ struct Ragged {
     struct Walk {
         Stream st;
         int x, x1, own, cl;
-        bool cut;  // the last segment is the first piece of a stream that others share no rows with
+        bool cut;   // the last segment is the first piece of a stream that others share no rows with
+        bool step;  // st is done: the next segment is in the stream after it
     };
-    __device__ static Walk walk(const RaggedParams& p, const Split& sp, const int* c, int i, int w) {
+    __device__ static Walk walk(const RaggedParams& p, const Split& sp, const Work& wk, int i, int w) {
         Walk k;
         range(sp, i, w, k.x, k.x1);
         k.cl = w == 0 ? 0 : 1;
         k.own = PAIRS && w > 0 ? 2 * i + (w - 1) : i;
-        k.cut = false;
-        if (k.x < k.x1) k.st = locate(p, sp, c, k.x);
+        k.cut = k.step = false;
+        if (k.x < k.x1) k.st = locate(p, sp, wk, k.x);
         return k;
     }
     __device__ static Seg next_seg(const RaggedParams& p, Walk& k) {
         Seg g;
         g.n = 0;
         g.cl = k.cl;
+        k.cut = false;
         while (g.n == 0 && k.x < k.x1) {
+            if (k.step && !next(p, k.st, k.cl)) break;
             g = segment(p, k.st, k.cl, k.own, k.x, k.x1);
-            k.cut = g.n > 0 && k.st.s.pfx == 0 && g.dst >= 0 && g.kv0 == 0;
+            k.cut = k.st.s.pfx == 0 && g.dst >= 0 && g.n > 0 && g.kv0 == 0;
             k.x = k.st.u0 + RAGGED_C0 + k.st.n;
-            if (k.x < k.x1 && !next(p, k.st, k.cl)) k.x = k.x1;
+            k.step = true;
         }
         return g;
     }
@@ -468,11 +536,11 @@ struct Ragged {
 
 // Zero output rows of the sequences that cannot be attended (CTA-strided over sequences, thread tid
 // of n).
-template <typename T>
+template <typename T, bool JOINT>
 __device__ __forceinline__ void ragged_zero_rows(const RaggedParams& p, int tid, int n) {
     const int vecs = p.H_q * p.D * Elem<T>::BYTES / 16;
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const Entry s = seq_entry(p, b);
+        const Entry s = seq_entry<JOINT>(p, b);
         if (!s.bad) continue;
         if (tid == 0) atomicOr(p.err, DEV_BAD_LENS);
         for (int64_t i = tid; i < (int64_t)s.T * vecs; i += n) {

@@ -30,11 +30,11 @@
 
 namespace kvc {
 
-template <int D_>
+template <int D_, bool JOINT>
 struct RtCfg {
     static constexpr int D = D_;
-    using R = Ragged<8, 7, true>;
-    using Seg = R::Seg;
+    using R = Ragged<8, 7, true, JOINT>;
+    using Seg = typename R::Seg;
     static constexpr int KT = R::KT;
     static constexpr int CB = D / 64;                // 128-byte column blocks of a row
     static constexpr int QSET = 128 * D * 2;         // a set's query bytes: 128 rows, or two tiles of 64
@@ -50,7 +50,7 @@ struct RtCfg {
     // tensor memory columns: S of set s at 128 s, O of set s at 256 + D s
     static constexpr int TMEM_COLS = 512;
     static_assert(NSLOT >= 4, "ring too shallow");
-    static_assert(NSLOT * TILE >= 2 * (2 * MAX_B + 1) * 4, "the prefix sums lie under the ring");
+    static_assert(NSLOT * TILE >= R::work_ints(MAX_B, MAX_B) * 4, "the split's arrays lie under the ring");
     struct Misc {
         uint64_t full[10], empty[10], vfix[10];
         uint64_t qpair, qfree;      // class 0: query rows landed; last product with them done
@@ -226,11 +226,11 @@ __device__ __forceinline__ void replay(Fetch&& fetch, Pair&& pair, K&& k, V&& v)
     }
 }
 
-template <int D>
+template <int D, bool JOINT>
 __global__ void __launch_bounds__(640, 1)
 ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
-    using C = RtCfg<D>;
+    using C = RtCfg<D, JOINT>;
     using R = typename C::R;
     using Seg = typename C::Seg;
     using Misc = typename C::Misc;
@@ -298,50 +298,48 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
 
     if (warp == 2) {
         // ====================================================== split and streams
-        int* c = reinterpret_cast<int*>(ring);
-        const typename R::Split sp = R::scan(p, c, lane);
+        const typename R::Work work = R::work(p, ring);
+        if (lane < 6) p.cuts[6 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+        const typename R::Split sp = R::scan(p, work, lane);
+        if (lane == 0) M.valid = sp.valid;
         if (blockIdx.x == 0) {
-            const int n = 2 * (p.NG + p.B + 1);
-            for (int i = lane; i < n; i += 32) p.plan[i] = sp.valid ? c[i] : 0;
+            const int n = 2 * (R::groups(p) + p.B + 1);
+            for (int i = lane; i < n; i += 32) p.plan[i] = sp.valid ? work.c[i] : 0;
             if (!sp.valid && lane == 0) atomicOr(p.err, DEV_BAD_SEQ);
         }
-        if (lane < 6) p.cuts[6 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
-        if (lane == 0) M.valid = sp.valid;
         typename R::Walk wk;
-        if (lane < 3) wk = R::walk(p, sp, c, blockIdx.x, lane);
+        if (lane < 3) wk = R::walk(p, sp, work, blockIdx.x, lane);
         fence_async_smem();
-        __syncwarp();  // the prefix sums are read: the ring may be filled by copies
+        __syncwarp();  // the split's arrays are read: the ring may be filled by copies
+        // Lane 0 leaves the segments of class 0 to both sets, then lanes 1 and 2 those of class 1 to
+        // theirs and the end.
         int s = 0;
-        if (lane == 0) {
-            for (bool ok = true; ok;) {
-                const Seg g = R::next_seg(p, wk);
-                if (g.n == 0) break;
-                if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, 0, g);
-                for (int q = 0; q < 2 && ok; ++q) {
-                    if (s >= 2) ok = mbar_wait(&M.segempty[q][s & 1], ((s - 2) >> 1) & 1, ab, p.err);
-                    if (ok) {
-                        M.seg[q][s & 1] = g;
-                        mbar_arrive(&M.segfull[q][s & 1]);
-                    }
-                }
-                ++s;
-            }
-        }
-        s = __shfl_sync(ALL, s, 0);
-        const int q = lane - 1;
-        bool done = lane != 1 && lane != 2, have = false;
+        bool done = lane > 2, have = false;
         Seg g;
+        g.n = 0;
         uint64_t t0 = global_ns();
         while (__any_sync(ALL, !done)) {
+            const bool pairs = (__ballot_sync(ALL, !done) & 1) != 0;
+            const int s0 = __shfl_sync(ALL, s, 0);
             if (done) continue;
             if (!have) {
                 g = R::next_seg(p, wk);
-                if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, lane, g);
                 have = true;
             }
-            if (s < 2 || mbar_try_wait(&M.segempty[q][s & 1], ((s - 2) >> 1) & 1)) {
-                M.seg[q][s & 1] = g;
-                mbar_arrive(&M.segfull[q][s & 1]);
+            if (lane == 0 && g.n == 0) {
+                done = true;
+                continue;
+            }
+            if (lane > 0 && pairs) continue;
+            if (lane > 0 && s < s0) s = s0;
+            const int q0 = lane == 2 ? 1 : 0, q1 = lane == 1 ? 0 : 1;
+            const uint32_t ph = ((s - 2) >> 1) & 1;
+            if (s < 2 || (mbar_try_wait(&M.segempty[q0][s & 1], ph) && mbar_try_wait(&M.segempty[q1][s & 1], ph))) {
+                for (int q = q0; q <= q1; ++q) {
+                    M.seg[q][s & 1] = g;
+                    mbar_arrive(&M.segfull[q][s & 1]);
+                }
+                if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, lane, g);
                 done = g.n == 0;
                 have = false;
                 ++s;
@@ -647,10 +645,24 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         // Both warps of a row's halves run the same loops to the end (a wait that gave up only skips the
         // stores), so the barrier between them always completes.
         const int bar = 1 + set * 4 + quad;
-        for (int s = 0;; ++s) {
+        // The first pass (s = -1) is dry: one made-up tile, nothing waited for, stored or signalled.  It brings
+        // the loop's code into the instruction cache while warp 2 computes the split (10 us less on
+        // small batches).
+        for (int s = -1;; ++s) {
             Seg g;
-            if (!pair_all(bar, fetch_seg(set, s, g, false))) break;
-            if (s == 0 && M.valid) ragged_zero_rows<__nv_bfloat16>(p, tid - 128, C::THREADS - 128);
+            const bool dry = s < 0;
+            if (dry) {
+                g.n = 1;
+                g.seq = g.h = g.row0 = g.kv0 = g.cl = 0;
+                g.ntok = 256 >> p.lgG;
+                g.kv_end = 100;
+                g.lim0 = 1;
+                g.causal = 1;
+                g.dst = -1;
+            } else if (!pair_all(bar, fetch_seg(set, s, g, false))) {
+                break;
+            }
+            if (s == 0 && M.valid) ragged_zero_rows<__nv_bfloat16, JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG, r0 = g.cl == 0 ? set * 128 : 0;  // the set's rows from r0
             const int r = r0 + r128, rw = r - lane;                            // the warp's first row sees least
@@ -676,7 +688,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     }
                 } else {
                     for (int j = 0; j < g.n; ++j) {
-                        ok = mbar_wait(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
+                        if (!dry) ok = mbar_wait(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
                         __syncwarp();
                         tc5_fence_after();
                         const int t0 = g.kv0 + j * C::KT + half * 64;
@@ -731,21 +743,21 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                             w[i] = bf16x2_rn(e.x, e.y);
                         }
-                        tc5_st32(tS + half * 32, w);
+                        if (!dry) tc5_st32(tS + half * 32, w);
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         tc5_wait_st();
                         tc5_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_n(&M.pfull[set], count);
+                        if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], count);
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                ok = mbar_wait(&M.ofull[set], no++ & 1, ab, p.err) && ok;
+                if (!dry) ok = mbar_wait(&M.ofull[set], no++ & 1, ab, p.err) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
                     *mine = l;
-                    ok = pair_all(bar, ok);
+                    ok = pair_all(bar, ok && !dry);
                     l += *other;
                     named_bar_sync(bar, 64);  // read on both sides before the next segment's maxima
                     const bool nonfin = *(volatile int*)&M.nonfinite[set][s & 1] != 0;
@@ -802,7 +814,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&M.segempty[set][s & 1]);
+            if (lane == 0 && !dry) mbar_arrive(&M.segempty[set][s & 1]);
         }
     }
     __syncwarp();
@@ -835,13 +847,13 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     }
 }
 
-template <int D>
+template <int D, bool JOINT>
 static int launch_rt(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& q1, const CUtensorMap& k,
                      const CUtensorMap& v, cudaStream_t s) {
-    using C = RtCfg<D>;
+    using C = RtCfg<D, JOINT>;
     static PerDeviceOnce once;
     const int e0 = once.run([] {
-        return (int)cudaFuncSetAttribute(ragged_tc5_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return (int)cudaFuncSetAttribute(ragged_tc5_kernel<D, JOINT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e0 != 0) return e0;
     cudaLaunchConfig_t cfg = {};
@@ -854,14 +866,15 @@ static int launch_rt(const RaggedParams& p, const CUtensorMap& q, const CUtensor
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_tc5_kernel<D>, p, q, q1, k, v);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_tc5_kernel<D, JOINT>, p, q, q1, k, v);
     if (e != cudaSuccess) return (int)e;
-    return launch_merge<__nv_bfloat16, typename C::R>(p, s);
+    return launch_merge<__nv_bfloat16, typename C::R, JOINT>(p, s);
 }
 
 int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& q1, const CUtensorMap& k,
                       const CUtensorMap& v, cudaStream_t s) {
-    return p.D == 128 ? launch_rt<128>(p, q, q1, k, v, s) : launch_rt<64>(p, q, q1, k, v, s);
+    if (p.NG > 0) return p.D == 128 ? launch_rt<128, true>(p, q, q1, k, v, s) : launch_rt<64, true>(p, q, q1, k, v, s);
+    return p.D == 128 ? launch_rt<128, false>(p, q, q1, k, v, s) : launch_rt<64, false>(p, q, q1, k, v, s);
 }
 
 }  // namespace kvc
