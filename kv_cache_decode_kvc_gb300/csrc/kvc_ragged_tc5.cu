@@ -194,34 +194,84 @@ __device__ __forceinline__ void tc5_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo
         : "memory");
 }
 
-// The order of the ring's items, replayed by the copy, product and guard warps.  fetch(q, s, g) waits
-// for segment s of set q; pair(g) handles a segment of class 0 (K0 V0 K1 V1 ..); k(q, g, j) and
-// v(q, g, j) the key tile j of set q's segment of class 1 for the scores and for the output: the sets
-// take turns, V of a set's tile and then K of its next.  Each returns false to stop (a wait gave up).
-template <class Seg, class Fetch, class Pair, class K, class V>
-__device__ __forceinline__ void replay(Fetch&& fetch, Pair&& pair, K&& k, V&& v) {
-    Seg g[2];
-    int s = 0;
-    while (true) {  // class 0: the same segments for both sets
-        if (!fetch(0, s, g[0]) || !fetch(1, s, g[1])) return;
-        if (g[0].n == 0 || g[0].cl != 0) break;
-        if (!pair(g[0])) return;
-        ++s;
+// The kernel's roles and their unrolled tiles together exceed the instruction cache if each use of a
+// helper is its own copy: the waits' polling, the rare paths and the roles' bodies are kept in one
+// place each.
+__device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err) {
+    return mbar_wait(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err) {
+    return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort_flag, err);
+}
+template <bool JOINT>
+__device__ __noinline__ void zero_rows(const RaggedParams& p, int tid, int n) {
+    ragged_zero_rows<__nv_bfloat16, JOINT>(p, tid, n);
+}
+// Adds the non-finite V values of positions [a, b) to a row's stored columns [col, col + n): out (bf16,
+// already divided; the sum is the value or NaN either way) or a piece.
+__device__ __noinline__ void add_nonfinite(const RaggedParams& p, int seq, int h, int a, int b, int col, int n,
+                                           __nv_bfloat16* out, float* po) {
+    for (int t = a; t < b; ++t) {
+        const int64_t vr = cache_row_rd(p.table, p.bs, p.max_blocks, p.num_blocks, p.H_kv, p.T_max, seq, h, t, p.err);
+        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.V) + vr * p.D;
+        for (int d = col; d < col + n; ++d) {
+            const float x = __bfloat162float(v[d]);
+            if (isfinite(x)) continue;
+            if (po) po[d] += x;
+            else out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
+        }
     }
-    int sq[2] = {s, s}, j[2] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        if (g[q].n > 0 && !k(q, g[q], 0)) return;
-    while (g[0].n > 0 || g[1].n > 0) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (g[q].n == 0) continue;
-            if (!v(q, g[q], j[q])) return;
-            if (++j[q] == g[q].n) {
-                j[q] = 0;
-                if (!fetch(q, ++sq[q], g[q])) return;
+}
+
+// The order of the ring's items, replayed by the copy, product and guard warps.  fetch(l) loads the next
+// segment of lane l.  A segment of class 0, which both sets walk together, is handled by whole(l): K of
+// its tiles 0 ..  each followed by V (K0 V0 K1 V1 ..).  In class 1 each set is a lane and the lanes
+// alternate: turn(l, v, k) handles V of tile l.j if v and K of the tile after it (0 if not v) if k; a
+// segment's last V and the next segment's first K are turns of their own, one behind the other.
+// All return false to stop (a wait gave up).
+template <class Seg>
+struct Lane {
+    Seg g;
+    int q, s, j;
+    bool begun;      // K of tile j has been handled
+    int ent, next;   // (copies) this CUDA lane's block of tile j and of the tile after it
+};
+template <class Seg, class Fetch, class Turn, class Whole>
+__device__ __forceinline__ void replay(Fetch&& fetch, Turn&& turn, Whole&& whole) {
+    Lane<Seg> a, b;
+    a.q = a.s = a.j = b.s = b.j = 0;
+    b.q = 1;
+    a.begun = b.begun = false;
+    bool both = true, more = true;  // class 0; lane a needs its next segment
+    while (true) {
+        if (more) {
+            if (!fetch(a)) return;
+            if (both) {
+                if (!fetch(b)) return;  // (class 0: the same segment)
+                ++b.s;
+                both = a.g.n > 0 && a.g.cl == 0;
             }
-            if (g[q].n > 0 && !k(q, g[q], j[q])) return;
+            ++a.s;
+        }
+        more = false;
+        if (both) {
+            if (!whole(a)) return;
+            more = true;
+            continue;
+        }
+        if (a.g.n > 0) {
+            const bool last = a.begun && a.j + 1 == a.g.n;
+            if (!turn(a, a.begun, !last)) return;
+            more = last;
+            a.j = last || !a.begun ? 0 : a.j + 1;
+            a.begun = !last;
+            if (more) continue;
+        }
+        if (!both) {
+            if (a.g.n == 0 && b.g.n == 0) return;
+            const Lane<Seg> t = a;
+            a = b;
+            b = t;
         }
     }
 }
@@ -241,7 +291,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     Misc& M = *reinterpret_cast<Misc*>(ring + C::NSLOT * C::TILE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = 1 << p.lgG;
-    volatile int* ab = &M.abort_flag;
+    int* ab = &M.abort_flag;
     if (smem_addr(rt_smem) & 1023) {  // (the swizzled tiles need it; the declaration asks for it)
         if (tid == 0) atomicOr(p.err, DEV_WAIT_TIMEOUT);
         return;
@@ -287,13 +337,17 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     uint32_t issued = 0;  // copies / products begun (copy and product threads)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // A role's segment s of set q, as soon as it is known; `release`: nothing more is read of it.
-    auto fetch_seg = [&](int q, int s, Seg& g, bool release) {
-        bool ok = mbar_wait(&M.segfull[q][s & 1], (s >> 1) & 1, ab, p.err);
-        if (!ok) return false;
-        g = M.seg[q][s & 1];
-        if (release) mbar_arrive(&M.segempty[q][s & 1]);
-        return true;
+    // A role's segment s of set q, as soon as it is known (the caller releases the place).
+    auto fetch_seg = [&](int q, int s, Seg& g) {
+        const bool ok = wait_on(&M.segfull[q][s & 1], (s >> 1) & 1, ab, p.err);
+        if (ok) g = M.seg[q][s & 1];
+        return ok;
+    };
+    // ... by a whole warp that keeps its own copy and needs the place no longer.
+    auto take_seg = [&](Lane<Seg>& l) {
+        const bool ok = __all_sync(ALL, fetch_seg(l.q, l.s, l.g)) != 0;
+        if (ok && lane == 0) mbar_arrive(&M.segempty[l.q][l.s & 1]);
+        return ok;
     };
 
     if (warp == 2) {
@@ -357,17 +411,18 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const int lrows = p.bs < C::KT ? p.bs : C::KT;  // rows of a copied box
         const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qbuf);
         uint32_t item = 0;
-        int npair = 0, sc[2] = {0, 0}, ent[2] = {0, 0}, nxt[2] = {0, 0};
+        int npair = 0, sc0 = 0, sc1 = 0;  // segments begun: of class 0, of class 1 by set
         auto entry = [&](const Seg& g, int j) {  // this lane's block of key tile j
             const int t = g.kv0 + j * C::KT + lane * lrows;
             return j < g.n && lane * lrows < C::KT && t < g.kv_end
                        ? __ldg(p.table + (size_t)g.seq * p.max_blocks + t / p.bs)
                        : 0;
         };
-        auto copy = [&](const Seg& g, int j, int e, const CUtensorMap* map) {
+        // K (isv false) or V of key tile j, whose block this CUDA lane knows
+        auto copy = [&](const Seg& g, int j, int e, bool isv) {
             const uint32_t slot = item % C::NSLOT, use = item / C::NSLOT;
             bool ok = true;
-            if (lane == 0 && use > 0) ok = mbar_wait(&M.empty[slot], (use - 1) & 1, ab, p.err);
+            if (lane == 0 && use > 0) ok = wait_on(&M.empty[slot], (use - 1) & 1, ab, p.err);
             if (!__all_sync(ALL, ok)) return false;
             const int t0 = g.kv0 + j * C::KT, left = g.kv_end - t0;
             const int nbox = left >= C::KT ? C::KT / lrows : (left + lrows - 1) / lrows;
@@ -381,68 +436,79 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 }
                 const int row = (int)(((int64_t)e * p.H_kv + g.h) * p.bs + (t0 + lane * lrows) % p.bs);
                 const uint32_t dst = ring_s + slot * C::TILE + lane * lrows * D * 2;
+                const CUtensorMap* map = isv ? &tmV : &tmK;
                 if constexpr (D == 128) tma_load_4d(dst, map, row >> 3, lrows >> 3, &M.full[slot], pol);
                 else tma_load_2d(dst, map, 0, row, &M.full[slot], pol);
             }
             return true;
         };
-        auto fetch = [&](int q, int s, Seg& g) {
-            bool ok = fetch_seg(q, s, g, false);
-            ok = __all_sync(ALL, ok);
-            if (ok && lane == 0) mbar_arrive(&M.segempty[q][s & 1]);
-            if (ok && g.n > 0) nxt[q] = entry(g, 0);
-            return ok;
-        };
         replay<Seg>(
-            fetch,
-            [&](const Seg& g) {
-                const int boxes = ((g.ntok << p.lgG) + 63) / 64;  // of 64 rows: set q's are 2 q, 2 q + 1
-                bool ok = true;
-                if (lane == 0) {
-                    if (npair > 0) ok = mbar_wait(&M.qfree, (npair - 1) & 1, ab, p.err);
-                    if (ok) {
-                        M.nq[0] = npair + 1;
-                        mbar_arrive_expect_tx(&M.qpair, boxes * C::CB * 8192);
-                        for (int b = 0; b < boxes; ++b)
-                            for (int cb = 0; cb < C::CB; ++cb)
-                                tma_load_q(q_s + (b >> 1) * C::QSET + cb * 16384 + (b & 1) * 8192, &tmQ, cb * 64, g.h * G,
-                                           g.row0 + (b * 64 >> p.lgG), &M.qpair);
+            [&](Lane<Seg>& l) {
+                const bool ok = take_seg(l);
+                if (ok && l.g.n > 0) l.next = entry(l.g, 0);
+                return ok;
+            },
+            [&](Lane<Seg>& l, bool v, bool k) {  // class 1
+                const Seg& g = l.g;
+                if (!v) {
+                    // the segment's query rows, into the set's places in turn: a place comes free with the
+                    // segment before the last, the first ones with class 0's last products
+                    const int rows = g.ntok << p.lgG, few = G > 16 ? G : 16, sc = l.q ? sc1 : sc0, place = sc & 1;
+                    const bool small = rows <= few;
+                    bool ok = true;
+                    if (lane == 0 && npair > 0 && sc == 0) ok = wait_on(&M.qfree, (npair - 1) & 1, ab, p.err);
+                    if (lane == 0 && ok) {
+                        M.nq[1 + 2 * l.q + place] = (sc >> 1) + 1;
+                        mbar_arrive_expect_tx(&M.qfull[l.q][place], C::CB * (small ? few * 128 : 8192));
+                        for (int cb = 0; cb < C::CB; ++cb)
+                            tma_load_q(q_s + l.q * C::QSET + place * (C::QSET / 2) + cb * 8192, small ? &tmQ1 : &tmQ, cb * 64,
+                                       g.h * G, g.row0, &M.qfull[l.q][place]);
                     }
+                    if (l.q) ++sc1;
+                    else ++sc0;
+                    if (!__all_sync(ALL, ok)) return false;
                 }
-                ++npair;
-                if (!__all_sync(ALL, ok)) return false;
-                for (int j = 0; j < g.n; ++j) {
-                    ent[0] = nxt[0];
-                    nxt[0] = entry(g, j + 1);
-                    if (!copy(g, j, ent[0], &tmK) || !copy(g, j, ent[0], &tmV)) return false;
+#pragma unroll 1
+                for (int i = v ? 0 : 1; i < (k ? 2 : 1); ++i) {
+                    const int j = l.j + (i && v ? 1 : 0);
+                    if (i) {
+                        l.ent = l.next;
+                        l.next = entry(g, j + 1);
+                    }
+                    if (!copy(g, j, l.ent, i == 0)) return false;
                 }
                 return true;
             },
-            [&](int q, const Seg& g, int j) {
-                if (j == 0) {
-                    const int place = sc[q] & 1, few = G > 16 ? G : 16;
-                    const bool small = (g.ntok << p.lgG) <= few;
-                    bool ok = true;
-                    if (lane == 0) {
-                        // places come free with the segment before the last; the shared tiles first with their
-                        // last product
-                        if (npair > 0 && sc[q] == 0) ok = mbar_wait(&M.qfree, (npair - 1) & 1, ab, p.err);
-                        if (ok) {
-                            M.nq[1 + 2 * q + place] = (sc[q] >> 1) + 1;
-                            mbar_arrive_expect_tx(&M.qfull[q][place], C::CB * (small ? few * 128 : 8192));
-                            for (int cb = 0; cb < C::CB; ++cb)
-                                tma_load_q(q_s + q * C::QSET + place * (C::QSET / 2) + cb * 8192, small ? &tmQ1 : &tmQ,
-                                           cb * 64, g.h * G, g.row0, &M.qfull[q][place]);
-                        }
+            [&](Lane<Seg>& l) {  // class 0
+                const Seg& g = l.g;
+                // query rows in boxes of 64 (set q's are 2 q, 2 q + 1), once the products with the last ones are
+                // done
+                const int boxes = ((g.ntok << p.lgG) + 63) / 64;
+                bool ok = true;
+                if (lane == 0 && npair > 0) ok = wait_on(&M.qfree, (npair - 1) & 1, ab, p.err);
+                ++npair;
+                if (lane == 0 && ok) {
+                    M.nq[0] = npair;
+                    mbar_arrive_expect_tx(&M.qpair, boxes * C::CB * 8192);
+#pragma unroll 1
+                    for (int i = 0; i < boxes * C::CB; ++i) {
+                        const int b = i / C::CB, cb = i - b * C::CB;
+                        tma_load_q(q_s + (b >> 1) * C::QSET + (b & 1) * 8192 + cb * 16384, &tmQ, cb * 64, g.h * G,
+                                   g.row0 + (b * 64 >> p.lgG), &M.qpair);
                     }
-                    ++sc[q];
-                    if (!__all_sync(ALL, ok)) return false;
                 }
-                ent[q] = nxt[q];
-                nxt[q] = entry(g, j + 1);
-                return copy(g, j, ent[q], &tmK);
-            },
-            [&](int q, const Seg& g, int j) { return copy(g, j, ent[q], &tmV); });
+                if (!__all_sync(ALL, ok)) return false;
+                int e = 0;
+#pragma unroll 1
+                for (int i = 0; i < 2 * g.n; ++i) {
+                    if ((i & 1) == 0) {
+                        e = l.next;
+                        l.next = entry(g, (i >> 1) + 1);
+                    }
+                    if (!copy(g, i >> 1, e, i & 1)) return false;
+                }
+                return true;
+            });
     } else if (warp == 1) {
         // ====================================================== products
         // (the whole warp runs this, one elected thread issues)
@@ -452,139 +518,143 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const uint64_t dK = smem_desc_sw128(smem_addr(ring), 16u, C::GSTR);
         const uint64_t dV = smem_desc_sw128(smem_addr(ring), 1024u, C::GSTR);
         const uint32_t tm = __shfl_sync(ALL, tmem, 0);
-        uint32_t item = 0, fix = 0;  // fix: parity of each slot's next guarded use
-        uint32_t np[2] = {0, 0};
-        int npair = 0, sc[2] = {0, 0};
-        auto wait_item = [&](uint32_t it) {
-            return mbar_wait(&M.full[it % C::NSLOT], (it / C::NSLOT) & 1, ab, p.err);
-        };
+        uint32_t item = 0, fix = 0, np = 0;  // parities: each slot's next guarded use, each set's weights
+        int npair = 0, sc0 = 0, sc1 = 0;
+        auto wait_item = [&](uint32_t it) { return wait_on(&M.full[it % C::NSLOT], (it / C::NSLOT) & 1, ab, p.err); };
         // a V tile that some row does not see all of has passed warp 3
-        auto wait_v = [&](const Seg& g, int j, uint32_t it) {
-            if (!wait_item(it)) return false;
-            if (g.kv0 + (j + 1) * C::KT > g.lim0) {
-                const uint32_t sl = it % C::NSLOT;
-                if (!mbar_wait(&M.vfix[sl], (fix >> sl) & 1, ab, p.err)) return false;
+        auto wait_v = [&](const Seg& g, int j) {
+            bool ok = wait_item(item);
+            if (ok && g.kv0 + (j + 1) * C::KT > g.lim0) {
+                const uint32_t sl = item % C::NSLOT;
+                ok = wait_on(&M.vfix[sl], (fix >> sl) & 1, ab, p.err);
                 fix ^= 1u << sl;
             }
-            return true;
+            return ok;
         };
-        auto wait_p = [&](int q) { return mbar_wait(&M.pfull[q], np[q]++ & 1, ab, p.err); };
-        // S[q] = Q K(slot)^T; the query tile at byte qo, its column blocks qcb apart; then the slot is
-        // free if `last`
-        auto score = [&](int q, uint32_t qo, uint32_t qcb, uint32_t slot_, bool last) {
-            const uint32_t slot = __shfl_sync(ALL, slot_, 0);
-            const uint32_t a0 = (uint32_t)dQ + (__shfl_sync(ALL, qo, 0) >> 4), b0 = (uint32_t)dK + slot * (C::TILE >> 4);
-            const uint32_t ah = (uint32_t)(dQ >> 32), bh = (uint32_t)(dK >> 32);
-            __syncwarp();
-            tc5_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc5_mma_ss(tm + q * 128, a0 + (((kk >> 2) * qcb + (kk & 3) * 32) >> 4), ah,
-                               b0 + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), bh, ID1, kk > 0);
-                tc5_commit(&M.sfull[q]);
-                if (last) tc5_commit(&M.empty[slot]);
-            }
-            __syncwarp();
-        };
-        // O[q] (+)= P[q] V(slot); then the set's segment is done if `end`, the slot free if `last`
-        auto apply = [&](int q, uint32_t slot_, bool acc_, bool end, bool last) {
-            const uint32_t slot = __shfl_sync(ALL, slot_, 0), acc = __shfl_sync(ALL, acc_ ? 1u : 0u, 0);
-            const uint32_t b0 = (uint32_t)dV + slot * (C::TILE >> 4), bh = (uint32_t)(dV >> 32);
-            __syncwarp();
+        auto uni = [&](uint32_t x) { return __shfl_sync(ALL, x, 0); };
+        // O[q] (+)= P[q] V, V's descriptor vb; its commits.  (one elected thread issues)
+        auto apply = [&](uint32_t q, uint32_t vb, uint32_t acc, uint64_t* done, uint64_t* freed) {
             tc5_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < C::KT / 16; ++kk)
-                    tc5_mma_ts(tm + 256 + q * D, tm + q * 128 + kk * 8, b0 + ((kk * 2 * C::GSTR) >> 4), bh, ID2,
+                    tc5_mma_ts(tm + 256 + q * D, tm + q * 128 + kk * 8, vb + ((kk * 2 * C::GSTR) >> 4), (uint32_t)(dV >> 32), ID2,
                                kk > 0 ? 1u : acc);
-                if (end) tc5_commit(&M.ofull[q]);
-                if (last) tc5_commit(&M.empty[slot]);
+                if (done) tc5_commit(done);
+                if (freed) tc5_commit(freed);
             }
             __syncwarp();
         };
-        auto free_q = [&] {
-            if (elect_one()) tc5_commit(&M.qfree);
+        // S[q] = Q K^T, descriptors qb (column blocks qcb apart) and kb
+        auto score = [&](uint32_t q, uint32_t qb, uint32_t qcb, uint32_t kb, uint64_t* freed, uint64_t* qfreed) {
+            tc5_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc5_mma_ss(tm + q * 128, qb + (kk >> 2) * qcb + (((kk & 3) * 32) >> 4), (uint32_t)(dQ >> 32),
+                               kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), (uint32_t)(dK >> 32), ID1, kk > 0);
+                tc5_commit(&M.sfull[q]);
+                if (freed) tc5_commit(freed);
+                if (qfreed) tc5_commit(qfreed);
+            }
             __syncwarp();
         };
-        auto go = [&](bool ok) { return __all_sync(ALL, ok) != 0; };
         replay<Seg>(
-            [&](int q, int s, Seg& g) {
-                const bool ok = go(fetch_seg(q, s, g, false));
-                if (ok && lane == 0) mbar_arrive(&M.segempty[q][s & 1]);
-                return ok;
-            },
-            [&](const Seg& g) {
-                const int sets = (g.ntok << p.lgG) > 128 ? 2 : 1, n = g.n;
-                if (!go(mbar_wait(&M.qpair, npair++ & 1, ab, p.err) && wait_item(item))) return false;
+            take_seg,
+            [&](Lane<Seg>& l, bool v, bool k) {  // class 1
+                const Seg& g = l.g;
+                const int sc = l.q ? sc1 : sc0, place = sc & 1;
+                const uint32_t vs = item % C::NSLOT, ki = item + (v ? 1 : 0), ks = ki % C::NSLOT;
                 issued = 1;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (q < sets) score(q, q * C::QSET, 16384, item % C::NSLOT, q + 1 == sets);
-                ++item;
-                if (n == 1) free_q();
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t vs = item % C::NSLOT, ks = (item + 1) % C::NSLOT;
-                    if (!go(wait_v(g, j, item))) return false;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (q >= sets) continue;
-                        if (!go(wait_p(q))) return false;
-                        apply(q, vs, j > 0, j + 1 == n, q + 1 == sets);
-                        if (j + 1 < n) {
-                            if (q == 0 && !go(wait_item(item + 1))) return false;
-                            score(q, q * C::QSET, 16384, ks, q + 1 == sets);
-                        }
-                    }
-                    item += j + 1 < n ? 2 : 1;
-                    if (j + 2 == n) free_q();
+                const uint32_t vb = (uint32_t)dV + uni(vs) * (C::TILE >> 4), kb = (uint32_t)dK + uni(ks) * (C::TILE >> 4);
+                const uint32_t q = uni(l.q), acc = uni(l.j > 0 ? 1u : 0u);
+                const uint32_t qb = (uint32_t)dQ + ((q * C::QSET + uni(place * (C::QSET / 2))) >> 4);
+                if (v) {
+                    bool ok = wait_v(g, l.j) && wait_on(&M.pfull[q], (np >> q) & 1, ab, p.err);
+                    np ^= 1u << q;
+                    if (!__all_sync(ALL, ok)) return false;
+                    apply(q, vb, acc, k ? nullptr : &M.ofull[q], &M.empty[vs]);
+                }
+                if (k) {
+                    bool ok = v || wait_on(&M.qfull[q][place], (sc >> 1) & 1, ab, p.err);
+                    ok = ok && wait_item(ki);
+                    if (!__all_sync(ALL, ok)) return false;
+                    score(q, qb, 8192 >> 4, kb, &M.empty[ks], nullptr);
+                }
+                item += (v ? 1 : 0) + (k ? 1 : 0);
+                if (v && !k) {
+                    if (l.q) ++sc1;
+                    else ++sc0;
                 }
                 return true;
             },
-            [&](int q, const Seg& g, int j) {
-                const int place = sc[q] & 1;
-                bool ok = j > 0 || mbar_wait(&M.qfull[q][place], (sc[q] >> 1) & 1, ab, p.err);
-                ok = ok && wait_item(item);
-                if (!go(ok)) return false;
+            [&](Lane<Seg>& l) {  // class 0: V of tile j, K of tile j + 1, set by set
+                const Seg& g = l.g;
+                const int sets = (g.ntok << p.lgG) > 128 ? 2 : 1, n = g.n;
+                const uint32_t qb = (uint32_t)dQ;
+                auto v_desc = [&](uint32_t it) { return (uint32_t)dV + uni(it % C::NSLOT) * (C::TILE >> 4); };
+                auto k_desc = [&](uint32_t it) { return (uint32_t)dK + uni(it % C::NSLOT) * (C::TILE >> 4); };
+                auto ready = [&](int q) {
+                    const bool ok = wait_on(&M.pfull[q], (np >> q) & 1, ab, p.err);
+                    np ^= 1u << q;
+                    return __all_sync(ALL, ok) != 0;
+                };
+                if (!__all_sync(ALL, wait_on(&M.qpair, npair++ & 1, ab, p.err) && wait_item(item))) return false;
                 issued = 1;
-                score(q, q * C::QSET + place * (C::QSET / 2), 8192, item % C::NSLOT, true);
+                const uint32_t k0 = k_desc(item);
+#pragma unroll 1
+                for (int q = 0; q < sets; ++q) {
+                    const bool last = q + 1 == sets;
+                    score(uni(q), qb + ((uni(q) * C::QSET) >> 4), 16384 >> 4, k0, last ? &M.empty[item % C::NSLOT] : nullptr,
+                          last && n == 1 ? &M.qfree : nullptr);
+                }
                 ++item;
-                return true;
-            },
-            [&](int q, const Seg& g, int j) {
-                if (!go(wait_v(g, j, item) && wait_p(q))) return false;
-                apply(q, item % C::NSLOT, j > 0, j + 1 == g.n, true);
-                if (j + 1 == g.n) ++sc[q];
+#pragma unroll 1
+                for (int j = 0; j + 1 < n; ++j) {
+                    const uint32_t vb = v_desc(item), kb = k_desc(item + 1), acc = uni(j > 0 ? 1u : 0u);
+                    uint64_t *ve = &M.empty[item % C::NSLOT], *ke = &M.empty[(item + 1) % C::NSLOT];
+                    uint64_t* qf = j + 2 == n ? &M.qfree : nullptr;
+                    if (!__all_sync(ALL, wait_v(g, j)) || !ready(0)) return false;
+                    apply(0, vb, acc, nullptr, sets == 1 ? ve : nullptr);
+                    if (!__all_sync(ALL, wait_item(item + 1))) return false;
+                    score(0, qb, 16384 >> 4, kb, sets == 1 ? ke : nullptr, sets == 1 ? qf : nullptr);
+                    if (sets == 2) {
+                        if (!ready(1)) return false;
+                        apply(1, vb, acc, nullptr, ve);
+                        score(1, qb + (C::QSET >> 4), 16384 >> 4, kb, ke, qf);
+                    }
+                    item += 2;
+                }
+                if (!__all_sync(ALL, wait_v(g, n - 1))) return false;
+                const uint32_t vb = v_desc(item), acc = uni(n > 1 ? 1u : 0u);
+#pragma unroll 1
+                for (int q = 0; q < sets; ++q) {
+                    if (!ready(q)) return false;
+                    apply(uni(q), vb, acc, &M.ofull[q], q + 1 == sets ? &M.empty[item % C::NSLOT] : nullptr);
+                }
                 ++item;
                 return true;
             });
     } else if (warp == 3) {
         // ====================================================== masked values
         uint32_t item = 0;
-        int cur[2] = {0, 0};
-        // every item is waited for in turn and held until it has been seen: a barrier's parity tells
-        // only neighbouring uses apart
-        auto seen = [&] {
-            const bool ok = mbar_wait(&M.full[item % C::NSLOT], (item / C::NSLOT) & 1, ab, p.err);
-            return __all_sync(ALL, ok) != 0;
-        };
-        auto pass = [&] {
-            if (lane == 0) mbar_arrive(&M.empty[item % C::NSLOT]);
-            ++item;
-        };
-        auto value = [&](int q, const Seg& g, int j) {
-            if (!seen()) return false;
+        // Every item is waited for in turn and held until it has been seen: a barrier's parity tells
+        // only neighbouring uses apart.  j: V of key tile j, -1: K.
+        auto look = [&](const Lane<Seg>& l, int j) {
+            const Seg& g = l.g;
+            const uint32_t slot = item % C::NSLOT;
+            if (!__all_sync(ALL, wait_on(&M.full[slot], (item / C::NSLOT) & 1, ab, p.err))) return false;
             const int t0 = g.kv0 + j * C::KT;
-            if (t0 + C::KT > g.lim0) {
-                char* v = ring + (item % C::NSLOT) * C::TILE;
+            if (j >= 0 && t0 + C::KT > g.lim0) {
+                char* tile = ring + slot * C::TILE;
                 const int end = g.kv_end - t0, first = g.lim0 > t0 ? g.lim0 - t0 : 0;
                 constexpr int W = C::CB * 8;  // 16-byte pieces of a row
                 uint32_t found = 0;
 #pragma unroll 4
-                for (int i = first * W + lane; i < C::KT * W; i += 32) {
-                    const int r = i / W, w = i % W;
-                    uint4* a = reinterpret_cast<uint4*>(v + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16);
-                    uint4 d = r < end ? *a : make_uint4(0, 0, 0, 0);
+                for (int c = first * W + lane; c < C::KT * W; c += 32) {
+                    const int r = c / W, w = c % W;
+                    uint4* a = reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16);
+                    const uint4 d = r < end ? *a : make_uint4(0, 0, 0, 0);
                     // an all-ones exponent in either half of a word
                     auto bad = [](uint32_t u) {
                         return ((u & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((u & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
@@ -595,42 +665,39 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     if (any != 0 || r >= end) *a = make_uint4(d.x & ~b.x, d.y & ~b.y, d.z & ~b.z, d.w & ~b.w);
                 }
                 if (found) {
-                    M.nonfinite[q][cur[q] & 1] = 1;
-                    if (g.cl == 0) M.nonfinite[1][cur[q] & 1] = 1;
+                    M.nonfinite[l.q][(l.s - 1) & 1] = 1;
+                    if (g.cl == 0) M.nonfinite[1][(l.s - 1) & 1] = 1;
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&M.vfix[item % C::NSLOT]);
+                if (lane == 0) mbar_arrive(&M.vfix[slot]);
             }
-            pass();
+            if (lane == 0) mbar_arrive(&M.empty[slot]);
+            ++item;
             return true;
         };
         replay<Seg>(
-            [&](int q, int s, Seg& g) {
-                bool ok = fetch_seg(q, s, g, false);
-                ok = __all_sync(ALL, ok);
-                cur[q] = s;
+            [&](Lane<Seg>& l) {
+                const bool ok = __all_sync(ALL, fetch_seg(l.q, l.s, l.g)) != 0;
                 if (ok && lane == 0) {
-                    M.nonfinite[q][s & 1] = 0;
-                    mbar_arrive(&M.segempty[q][s & 1]);
+                    M.nonfinite[l.q][l.s & 1] = 0;
+                    mbar_arrive(&M.segempty[l.q][l.s & 1]);
                 }
                 __syncwarp();
                 return ok;
             },
-            [&](const Seg& g) {
-                for (int j = 0; j < g.n; ++j) {
-                    if (!seen()) return false;
-                    pass();
-                    if (!value(0, g, j)) return false;
-                }
+            [&](Lane<Seg>& l, bool v, bool k) {
+#pragma unroll 1
+                for (int i = v ? 0 : 1; i < (k ? 2 : 1); ++i)
+                    if (!look(l, i ? -1 : l.j)) return false;
                 return true;
             },
-            [&](int q, const Seg& g, int j) {
-                if (!seen()) return false;
-                pass();
+            [&](Lane<Seg>& l) {
+#pragma unroll 1
+                for (int i = 0; i < 2 * l.g.n; ++i)
+                    if (!look(l, i & 1 ? i >> 1 : -1)) return false;
                 return true;
-            },
-            value);
+            });
     } else {
         // ====================================================== softmax and output
         const int set = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
@@ -659,10 +726,10 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 g.lim0 = 1;
                 g.causal = 1;
                 g.dst = -1;
-            } else if (!pair_all(bar, fetch_seg(set, s, g, false))) {
+            } else if (!pair_all(bar, fetch_seg(set, s, g))) {
                 break;
             }
-            if (s == 0 && M.valid) ragged_zero_rows<__nv_bfloat16, JOINT>(p, tid - 128, C::THREADS - 128);
+            if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG, r0 = g.cl == 0 ? set * 128 : 0;  // the set's rows from r0
             const int r = r0 + r128, rw = r - lane;                            // the warp's first row sees least
@@ -681,14 +748,14 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         ns += g.n;
                     } else {
                         for (int j = 0; j < g.n; ++j) {
-                            ok = mbar_wait(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
+                            ok = wait_on(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&M.pfull[set]);
                         }
                     }
                 } else {
                     for (int j = 0; j < g.n; ++j) {
-                        if (!dry) ok = mbar_wait(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
+                        if (!dry) ok = wait_on(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
                         __syncwarp();
                         tc5_fence_after();
                         const int t0 = g.kv0 + j * C::KT + half * 64;
@@ -752,7 +819,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                if (!dry) ok = mbar_wait(&M.ofull[set], no++ & 1, ab, p.err) && ok;
+                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, ab, p.err) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
@@ -777,20 +844,6 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         __syncwarp();
                         tc5_ld32(tO + d, o);
                         if (r < nrow && ok) {
-                            if (nonfin) {
-                                // the values warp 3 took out of tiles this row sees part of
-                                const int a = max(g.lim0, g.kv0), b = min(limit, g.kv0 + g.n * C::KT);
-                                for (int t = a; t < b; ++t) {
-                                    const int64_t vr = cache_row_rd(p.table, p.bs, p.max_blocks, p.num_blocks, p.H_kv, p.T_max,
-                                                                    g.seq, g.h, t, p.err);
-                                    const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.V) + vr * D + col;
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) {
-                                        const float x = __bfloat162float(vp[i]);
-                                        if (!isfinite(x)) o[i] += x;
-                                    }
-                                }
-                            }
                             if (g.dst == -1) {
 #pragma unroll
                                 for (int i = 0; i < 32; i += 16) {
@@ -810,6 +863,10 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             }
                         }
                     }
+                    if (nonfin && r < nrow && ok)
+                        // the values warp 3 took out of tiles this row sees part of
+                        add_nonfinite(p, g.seq, g.h, max(g.lim0, g.kv0), min(limit, g.kv0 + g.n * C::KT), half * C::HD, C::HD, out,
+                                      g.dst == -1 ? nullptr : po);
                     tc5_fence_before();
                 }
             }
