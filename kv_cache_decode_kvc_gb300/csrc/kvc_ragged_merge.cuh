@@ -177,7 +177,8 @@ __device__ __forceinline__ void merge_two(const RaggedParams& p, int r0, int ste
 
 constexpr int MERGE_SLICES = 8;
 // Without groups: block (c, y) takes the c-th possible cut; if a stream was cut there first, its
-// warps merge the rows of the stream's tile from row 8 y on, every 64th eight of them.
+// warps merge the rows of the stream's tile from row 8 y on, every 64th eight of them (with many
+// pieces: rows y, y + 8, .. one by one).
 template <typename T, class R>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const RaggedParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -202,13 +203,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const Ragg
             merge_two<T>(p, r, STEP, b.x, lane, out_of, at_row);
         return;
     }
-    for (int r0 = blockIdx.y * MERGE_WARPS; r0 < b.x; r0 += MERGE_SLICES * MERGE_WARPS) {
-        if (a.x > MERGE_WIDE) {
-            for (int r = r0; r < min(r0 + MERGE_WARPS, b.x); ++r) merge_row_wide<T>(p, a.x, out_of(r), warp, lane, at_row(r));
-        } else if (r0 + warp < b.x) {
-            merge_store<T>(p, merge_pieces(p, a.x, 0, 1, lane, at_row(r0 + warp)), out_of(r0 + warp), lane);
-        }
+    if (a.x > MERGE_WIDE) {
+        for (int r = blockIdx.y; r < b.x; r += MERGE_SLICES) merge_row_wide<T>(p, a.x, out_of(r), warp, lane, at_row(r));
+        return;
     }
+    for (int r = blockIdx.y * MERGE_WARPS + warp; r < b.x; r += MERGE_SLICES * MERGE_WARPS)
+        merge_store<T>(p, merge_pieces(p, a.x, 0, 1, lane, at_row(r)), out_of(r), lane);
 }
 
 // With groups: block (row, KV head, y), a warp per query head 8 y + warp of the group; the row's

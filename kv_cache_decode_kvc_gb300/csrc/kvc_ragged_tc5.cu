@@ -331,11 +331,13 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const CUtensorMap* m = lane == 0 ? &tmQ : lane == 1 ? &tmQ1 : lane == 2 ? &tmK : &tmV;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
-    __syncthreads();
+    // Warp 2 begins with the split at once and joins the others (barrier 9) before it hands out segments.
+    if (warp != 2) named_bar_sync(10, C::THREADS - 32);
     tc5_fence_after();
-    const uint32_t tmem = M.tmem;
+    const uint32_t tmem = warp != 2 ? M.tmem : 0;
     uint32_t issued = 0;  // copies / products begun (copy and product threads)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp != 2) named_bar_arrive(9, C::THREADS);
+    if (warp < 4) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // A role's segment s of set q, as soon as it is known (the caller releases the place).
     auto fetch_seg = [&](int q, int s, Seg& g) {
@@ -364,7 +366,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         typename R::Walk wk;
         if (lane < 3) wk = R::walk(p, sp, work, blockIdx.x, lane);
         fence_async_smem();
-        __syncwarp();  // the split's arrays are read: the ring may be filled by copies
+        named_bar_sync(9, C::THREADS);  // the split's arrays are read, the barriers set up
         // Lane 0 leaves the segments of class 0 to both sets, then lanes 1 and 2 those of class 1 to
         // theirs and the end.
         int s = 0;
@@ -407,7 +409,9 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         }
     } else if (warp == 0) {
         // ====================================================== copies
-        const uint64_t pol = policy_evict_normal();
+        // tiles of class 1 are read once: they leave L2 first (the kernel's code and the batch's arrays, which
+        // the next call needs from there, stay)
+        const uint64_t pol0 = policy_evict_normal(), pol1 = policy_evict_first();
         const int lrows = p.bs < C::KT ? p.bs : C::KT;  // rows of a copied box
         const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qbuf);
         uint32_t item = 0;
@@ -437,6 +441,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 const int row = (int)(((int64_t)e * p.H_kv + g.h) * p.bs + (t0 + lane * lrows) % p.bs);
                 const uint32_t dst = ring_s + slot * C::TILE + lane * lrows * D * 2;
                 const CUtensorMap* map = isv ? &tmV : &tmK;
+                const uint64_t pol = g.cl == 0 ? pol0 : pol1;
                 if constexpr (D == 128) tma_load_4d(dst, map, row >> 3, lrows >> 3, &M.full[slot], pol);
                 else tma_load_2d(dst, map, 0, row, &M.full[slot], pol);
             }
@@ -729,6 +734,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             } else if (!pair_all(bar, fetch_seg(set, s, g))) {
                 break;
             }
+            if (s == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG, r0 = g.cl == 0 ? set * 128 : 0;  // the set's rows from r0

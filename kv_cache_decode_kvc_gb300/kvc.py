@@ -24,6 +24,7 @@ KVC_CACHE_PLAIN, KVC_CACHE_INT8, KVC_CACHE_FP8 = 0, 1, 2
 KVC_ROPE_HALF, KVC_ROPE_ADJACENT = 0, 1
 
 _lib = None
+_torch = None  # imported with the first cache's tensors
 
 
 class KvcError(RuntimeError):
@@ -119,11 +120,25 @@ def _ptr(x) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """The current torch stream's handle.  torch.cuda.current_stream() spends 4 us on wrapping it;
+    the raw getter, where this torch has it, takes the device's index."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    torch.cuda._lazy_init()
+    return _raw_stream(torch._C._cuda_getDevice())
+
+
+_raw_stream = None
 
 
 def _as_stream(stream):
@@ -388,8 +403,10 @@ class KVCache:
 
     @property
     def torch_dtype(self):
-        import torch
-        return torch.bfloat16 if self.dtype_code == KVC_BF16 else torch.float32
+        global _torch
+        if _torch is None:
+            import torch as _torch
+        return _torch.bfloat16 if self.dtype_code == KVC_BF16 else _torch.float32
 
     def close(self):
         if self.h:
@@ -505,18 +522,17 @@ class Rope:
 
 
 def _packed(t, heads, D, dtype, what):
-    """(tensor, elements between tokens) of a packed [N, heads, D] tensor."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != dtype:
-        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype}, got {tuple(t.shape)} {t.dtype}")
-    s = t.stride()
-    if s[2] != 1 or (s[1] != D and heads > 1):
-        raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {s}")
-    return s[0] if t.shape[0] > 1 else max(s[0], heads * D)
+    """Elements between tokens of a packed [N, heads, D] tensor."""
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype:
+        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype}, got {tuple(sh)} {t.dtype}")
+    if st[2] != 1 or (st[1] != D and heads > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {st}")
+    return st[0] if sh[0] > 1 else max(st[0], heads * D)
 
 
-def _index(t, what, *shape):
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _index(t, what, int32, *shape):
+    if t.dtype != int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: want contiguous int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
@@ -551,10 +567,10 @@ class PagedKVCache(KVCache):
         kvc_paged_decode_step(self.h, layer, q, k_new, v_new, out, block_table, lens, stream)
 
 
-    def _batch(self, block_table, cu_seqlens, lens):
-        _index(block_table, "block_table", self.B, self.max_blocks)
-        _index(cu_seqlens, "cu_seqlens", self.B + 1)
-        _index(lens, "lens", self.B)
+    def _batch(self, block_table, cu_seqlens, lens, int32):
+        _index(block_table, "block_table", int32, self.B, self.max_blocks)
+        _index(cu_seqlens, "cu_seqlens", int32, self.B + 1)
+        _index(lens, "lens", int32, self.B)
 
     def append_rope(self, layer, rope, q, k, v, block_table, cu_seqlens, lens, q_out=None, positions=None,
                     stream=None):
@@ -562,14 +578,19 @@ class PagedKVCache(KVCache):
         [N, H_q, D] rotated into q_out (None: in place; q None: append only).  Sequence b's tokens are
         rows cu_seqlens[b] .. cu_seqlens[b + 1], lens[b] counts its positions with them.  positions
         int32 [n_axes, N] or, for one axis, [N] (None: the slot in the sequence)."""
-        N, D, dt = k.shape[0], self.D, self.torch_dtype
+        dt = self.torch_dtype
+        int32 = _torch.int32
+        N, D = k.shape[0], self.D
         ks, vs = _packed(k, self.H_kv, D, dt, "k"), _packed(v, self.H_kv, D, dt, "v")
         if v.shape[0] != N:
             raise ValueError(f"v: want {N} rows, got {v.shape[0]}")
         qs = qos = 0
         if q is not None:
-            q_out = q if q_out is None else q_out
-            qs, qos = _packed(q, self.H_q, D, dt, "q"), _packed(q_out, self.H_q, D, dt, "q_out")
+            qs = qos = _packed(q, self.H_q, D, dt, "q")
+            if q_out is None:
+                q_out = q
+            else:
+                qos = _packed(q_out, self.H_q, D, dt, "q_out")
             if q.shape[0] != N or q_out.shape[0] != N:
                 raise ValueError(f"q, q_out: want {N} rows, got {q.shape[0]}, {q_out.shape[0]}")
         elif q_out is not None:
@@ -578,13 +599,12 @@ class PagedKVCache(KVCache):
         if positions is not None:
             if positions.dim() == 1 and rope.n_axes == 1:
                 positions = positions[None]
-            import torch
-            if positions.dtype != torch.int32 or tuple(positions.shape) != (rope.n_axes, N) or (
+            if positions.dtype != int32 or tuple(positions.shape) != (rope.n_axes, N) or (
                     N > 1 and positions.stride(1) != 1):
                 raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}], got {positions.dtype} "
                                  f"{list(positions.shape)}")
             ps = max(positions.stride(0), N)
-        self._batch(block_table, cu_seqlens, lens)
+        self._batch(block_table, cu_seqlens, lens, int32)
         kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
                               cu_seqlens, lens, N, stream)
 
@@ -592,38 +612,36 @@ class PagedKVCache(KVCache):
         """Scratch bytes of attn_ragged (groups = 0) or attn_shared for N packed rows."""
         return kvc_paged_attn_workspace(self.h, N, groups)
 
-    def _scratch(self, workspace, N, groups, stream):
-        import torch
+    def _attn_args(self, q, out, block_table, cu_seqlens, lens, NG, workspace, stream):
+        dt = self.torch_dtype
+        N = q.shape[0]
+        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
+        if out.shape[0] != N:
+            raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
+        self._batch(block_table, cu_seqlens, lens, _torch.int32)
         if workspace is None:
             # allocated on the call's stream, so that its next use is ordered behind this call
-            with torch.cuda.stream(_as_stream(stream)):
-                workspace = torch.empty(self.attn_workspace_bytes(N, groups), dtype=torch.uint8, device="cuda")
-        return workspace, workspace.numel() * workspace.element_size()
+            with _torch.cuda.stream(_as_stream(stream)):
+                workspace = _torch.empty(self.attn_workspace_bytes(N, NG), dtype=_torch.uint8, device="cuda")
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: want a contiguous tensor")
+        return N, qs, os_, workspace, workspace.numel() * workspace.element_size()
 
     def attn_ragged(self, layer, q, out, block_table, cu_seqlens, lens, workspace=None, stream=None):
         """Attention of packed new tokens q [N, H_q, D] -> out over the cache: token i of sequence b sees
         positions up to lens[b] - T_b + i (append first).  workspace: a contiguous device tensor of at
         least attn_workspace_bytes(N) bytes (None: allocated for the call)."""
-        N, dt = q.shape[0], self.torch_dtype
-        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
-        if out.shape[0] != N:
-            raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
-        self._batch(block_table, cu_seqlens, lens)
-        ws, nb = self._scratch(workspace, N, 0, stream)
+        N, qs, os_, ws, nb = self._attn_args(q, out, block_table, cu_seqlens, lens, 0, workspace, stream)
         kvc_paged_attn_ragged(self.h, layer, q, qs, out, os_, block_table, cu_seqlens, lens, N, ws, nb, stream)
 
     def attn_shared(self, layer, q, out, block_table, cu_seqlens, lens, groups, prefix_lens, workspace=None,
                     stream=None):
         """attn_ragged for groups of consecutive sequences [groups[g], groups[g + 1]) (int32 [NG + 1])
         whose first prefix_lens[g] (int32 [NG]) positions lie in the same blocks."""
-        N, dt, NG = q.shape[0], self.torch_dtype, prefix_lens.shape[0]
-        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
-        if out.shape[0] != N:
-            raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
-        self._batch(block_table, cu_seqlens, lens)
-        _index(groups, "groups", NG + 1)
-        _index(prefix_lens, "prefix_lens", NG)
-        ws, nb = self._scratch(workspace, N, NG, stream)
+        NG = prefix_lens.shape[0]
+        N, qs, os_, ws, nb = self._attn_args(q, out, block_table, cu_seqlens, lens, NG, workspace, stream)
+        _index(groups, "groups", _torch.int32, NG + 1)
+        _index(prefix_lens, "prefix_lens", _torch.int32, NG)
         kvc_paged_attn_shared(self.h, layer, q, qs, out, os_, block_table, cu_seqlens, lens, N, groups, prefix_lens,
                               NG, ws, nb, stream)
 
