@@ -203,6 +203,20 @@ __device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, int* abor
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err) {
     return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort_flag, err);
 }
+// The softmax warps wait most of the time, up to sixteen of them at once: between polls they sleep, which
+// leaves the issue slots to the warps that work (a guarded tile took warp 3 up to 7 k cycles beside
+// polling warps).
+__device__ __noinline__ bool mbar_doze(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err, uint32_t ns) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        __nanosleep(ns);
+        if (mbar_try_wait(bar, parity)) return true;
+    }
+    return mbar_wait(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool wait_dozing(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err, uint32_t ns) {
+    return mbar_try_wait(bar, parity) || mbar_doze(bar, parity, abort_flag, err, ns);
+}
 template <bool JOINT>
 __device__ __noinline__ void zero_rows(const RaggedParams& p, int tid, int n) {
     ragged_zero_rows<__nv_bfloat16, JOINT>(p, tid, n);
@@ -652,14 +666,14 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             const int t0 = g.kv0 + j * C::KT;
             if (j >= 0 && t0 + C::KT > g.lim0) {
                 char* tile = ring + slot * C::TILE;
-                const int end = g.kv_end - t0, first = g.lim0 > t0 ? g.lim0 - t0 : 0;
+                const int end = min(g.kv_end - t0, C::KT), first = max(g.lim0 - t0, 0);
                 constexpr int W = C::CB * 8;  // 16-byte pieces of a row
                 uint32_t found = 0;
-#pragma unroll 4
-                for (int c = first * W + lane; c < C::KT * W; c += 32) {
+#pragma unroll 2
+                for (int c = first * W + lane; c < end * W; c += 32) {
                     const int r = c / W, w = c % W;
                     uint4* a = reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16);
-                    const uint4 d = r < end ? *a : make_uint4(0, 0, 0, 0);
+                    const uint4 d = *a;
                     // an all-ones exponent in either half of a word
                     auto bad = [](uint32_t u) {
                         return ((u & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((u & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
@@ -667,7 +681,19 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     const uint4 b = make_uint4(bad(d.x), bad(d.y), bad(d.z), bad(d.w));
                     const uint32_t any = b.x | b.y | b.z | b.w;
                     found |= any;
-                    if (any != 0 || r >= end) *a = make_uint4(d.x & ~b.x, d.y & ~b.y, d.z & ~b.z, d.w & ~b.w);
+                    if (any != 0) *a = make_uint4(d.x & ~b.x, d.y & ~b.y, d.z & ~b.z, d.w & ~b.w);
+                }
+                // rows behind the end: those of its 8-row group, then the whole groups
+                if (end < C::KT) {
+                    const int g8 = (end + 7) & ~7;
+                    for (int c = end * W + lane; c < g8 * W; c += 32) {
+                        const int r = c / W, w = c % W;
+                        *reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll 4
+                    for (int at = (g8 >> 3) * C::GSTR + lane * 16; at < C::TILE; at += 512)
+                        *reinterpret_cast<uint4*>(tile + at) = make_uint4(0, 0, 0, 0);
                 }
                 if (found) {
                     M.nonfinite[l.q][(l.s - 1) & 1] = 1;
@@ -717,6 +743,11 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         // Both warps of a row's halves run the same loops to the end (a wait that gave up only skips the
         // stores), so the barrier between them always completes.
         const int bar = 1 + set * 4 + quad;
+        auto fetch_dozing = [&](int q, int s, Seg& g) {
+            const bool ok = wait_dozing(&M.segfull[q][s & 1], (s >> 1) & 1, ab, p.err, 40);
+            if (ok) g = M.seg[q][s & 1];
+            return ok;
+        };
         // The first pass (s = -1) is dry: one made-up tile, nothing waited for, stored or signalled.  It brings
         // the loop's code into the instruction cache while warp 2 computes the split (10 us less on
         // small batches).
@@ -731,7 +762,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 g.lim0 = 1;
                 g.causal = 1;
                 g.dst = -1;
-            } else if (!pair_all(bar, fetch_seg(set, s, g))) {
+            } else if (!pair_all(bar, fetch_dozing(set, s, g))) {
                 break;
             }
             if (s == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -754,14 +785,14 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         ns += g.n;
                     } else {
                         for (int j = 0; j < g.n; ++j) {
-                            ok = wait_on(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
+                            ok = wait_dozing(&M.sfull[set], ns++ & 1, ab, p.err, 20) && ok;
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&M.pfull[set]);
                         }
                     }
                 } else {
                     for (int j = 0; j < g.n; ++j) {
-                        if (!dry) ok = wait_on(&M.sfull[set], ns++ & 1, ab, p.err) && ok;
+                        if (!dry) ok = wait_dozing(&M.sfull[set], ns++ & 1, ab, p.err, 20) && ok;
                         __syncwarp();
                         tc5_fence_after();
                         const int t0 = g.kv0 + j * C::KT + half * 64;
@@ -825,7 +856,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, ab, p.err) && ok;
+                if (!dry) ok = wait_dozing(&M.ofull[set], no++ & 1, ab, p.err, idle ? 400 : 20) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
