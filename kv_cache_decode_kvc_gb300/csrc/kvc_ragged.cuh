@@ -13,7 +13,7 @@
 //     rows come from all of its sequences (packed consecutively), no mask; each of its
 //     sequences has streams over [P, L_b) as any sequence has over [0, L_b).  Groups and
 //     sequences are the entries e in [0, NG + B) of the batch;
-//   - all streams are laid end to end, each costing its tiles and C0 more for its start, and CTA
+//   - all streams are laid end to end, each costing so much per key tile and for its start, and CTA
 //     i of P takes the cost units [i U / P, (i + 1) U / P): equal work whatever the lengths, no
 //     CTA waits for another, the same split on every run (results are reproducible);
 //   - streams of class 0 come first, then those of class 1.  The tensor-core kernel has two
@@ -33,8 +33,6 @@
 
 namespace kvc {
 
-constexpr int RAGGED_C0 = 1;         // cost of a stream's start, in tiles
-constexpr int RAGGED_LG_MIN = 2;     // fewer CTAs when a CTA's share would drop below 4 units
 constexpr int PAIR_ROWS = 64;
 
 struct RaggedParams {
@@ -58,8 +56,6 @@ struct RaggedParams {
     int B, N, H_q, H_kv, lgG, NG, D;
     int bs, max_blocks, num_blocks, T_max;
     int P;          // CTAs at most
-    int lg_min;     // log2 of the cost units per CTA at least (1 or more: no worker between two pieces is
-                    // empty)
     float qscale;   // log2(e) / sqrt(D)
 };
 
@@ -168,6 +164,14 @@ struct Ragged {
     // its first piece 2-3 and then ends the range; set 0: 0 and 2, set 1: 3 and 4)
     static constexpr int SLOTS = PAIRS ? 5 : 2, SLOT_ROWS = PAIRS ? RT / 2 : RT;
 
+    // Cost units of a key tile and of a stream's start, by class.  (Measured with starts of 1, 2 and 4
+    // tiles in class 0: prompts 271, 246, 232 us; tiles of class 1 at 1/2, 1 and 3/2 of class 0's: the mixed
+    // batch 176, 133 and 168 us.)
+    __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
+    __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 8 : 4; }
+    // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
+    // of it (a worker's share, half of that in class 1, is a tile's cost or more).
+    static constexpr int LG_MIN = PAIRS ? 3 : 1;
     __device__ static int groups(const RaggedParams& p) { return JOINT ? p.NG : 0; }
     __device__ static Entry entry_of(const RaggedParams& p, int e) {
         if (JOINT && e < p.NG) return group_entry(p, e);
@@ -179,27 +183,25 @@ struct Ragged {
     // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
     __device__ static int tiles(int S0, int t1) { return (int)(((unsigned)S0 + (unsigned)t1 + KT - 1) >> LKT); }
-    // Costs are 32-bit (a call of 2^31 units, hours of work, is refused: scan).  Cost of an entry's first k
-    // streams, all full (TQ = 2^lq tokens each): sum over i = 1 .. k of ceil((S0 + i TQ) / KT),
-    // and the starts.
-    __device__ static int cost_full(int S0, int k, int lq) {
-        if (lq >= LKT) return k * ((int)((unsigned)(S0 + KT - 1) >> LKT) + RAGGED_C0) + (triangle(k) << (lq - LKT));
+    // Costs are 32-bit (a call of 2^31 units, hours of work, is refused: scan).  Key tiles of an entry's first
+    // k streams, all full (TQ = 2^lq tokens each): sum over i = 1 .. k of ceil((S0 + i TQ) / KT).
+    __device__ static int tiles_full(int S0, int k, int lq) {
+        if (lq >= LKT) return k * (int)((unsigned)(S0 + KT - 1) >> LKT) + (triangle(k) << (lq - LKT));
         // ceil((S0 + i TQ) / KT) = ceil((ceil(S0 / TQ) + i) / (KT / TQ))
         const int s = (int)((unsigned)(S0 + (1 << lq) - 1) >> lq);
-        return ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq) + k * RAGGED_C0;
+        return ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq);
     }
-    __device__ static int cost(const RaggedParams& p, const Entry& s) {
+    __device__ static int cost(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0;
-        const int lq = LRT - p.lgG, nk = (int)((unsigned)(s.T + (1 << lq) - 1) >> lq);
-        if (JOINT && s.group) return nk * (((s.pfx + KT - 1) >> LKT) + RAGGED_C0);
-        const int S0 = s.L - s.T - s.pfx;
-        return cost_full(S0, nk - 1, lq) + tiles(S0, s.T) + RAGGED_C0;
+        const int lq = LRT - p.lgG, nk = (int)((unsigned)(s.T + (1 << lq) - 1) >> lq), S0 = s.L - s.T - s.pfx;
+        const int n = JOINT && s.group ? nk * ((s.pfx + KT - 1) >> LKT) : tiles_full(S0, nk - 1, lq) + tiles(S0, s.T);
+        return n * tile_cost(cl) + nk * start_cost(cl);
     }
     // The same to a few parts in a million, without wrapping.
-    __device__ static float cost_about(const RaggedParams& p, const Entry& s) {
+    __device__ static float cost_about(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0.f;
         const float nk = (float)s.T / (float)(RT >> p.lgG) + 1.f, own = (float)(JOINT && s.group ? s.pfx : s.L - s.pfx);
-        return nk * (own / KT + 1.f + RAGGED_C0);
+        return nk * ((own / KT + 1.f) * tile_cost(cl) + start_cost(cl));
     }
 
     // The batch's split: total cost U, class 0's part W0, CTAs P.
@@ -209,7 +211,7 @@ struct Ragged {
         bool valid;
     };
     __device__ static void divide(const RaggedParams& p, Split& sp) {
-        const int want = sp.U >> p.lg_min;
+        const int want = sp.U >> LG_MIN;
         sp.P = sp.U == 0 ? 0 : max(1, min(want, p.P));
         sp.each = sp.U == 0 ? 0 : (int)((unsigned)sp.U / (unsigned)sp.P);
         sp.more = sp.U - sp.each * sp.P;
@@ -278,8 +280,9 @@ struct Ragged {
             bad |= !fine;
             int x[2] = {0, 0};
             if (fine && e < NE) {
-                x[cls(p, s)] = cost(p, s);
-                about += cost_about(p, s);
+                const int cl = cls(p, s);
+                x[cl] = cost(p, s, cl);
+                about += cost_about(p, s, cl);
                 k.ent[e] = make_int4(s.row0, s.T, s.L, s.pfx);
             }
 #pragma unroll
@@ -348,6 +351,11 @@ struct Ragged {
         range(sp, i, 2, a, b);
         return 2 * i + (x >= a ? 1 : 0);
     }
+    // The worker of key tile j of a stream of class cl.
+    template <class S>
+    __device__ static int owner_of(const Split& sp, const S& st, int cl, int j) {
+        return owner(sp, st.u0 + start_cost(cl) + j * tile_cost(cl));
+    }
     // Slot of a worker's piece: `later` piece of a stream (it opens the worker's range) or its first.
     __device__ static int slot(int cl, int own, bool later) {
         if (!PAIRS) return own * 2 + (later ? 0 : 1);
@@ -375,7 +383,7 @@ struct Ragged {
         const int NE = groups(p) + p.B, lq = LRT - p.lgG;
         const int* c = k.c;
         Stream st;
-        const int base = x < sp.W0 ? 0 : sp.W0;
+        const int base = x < sp.W0 ? 0 : sp.W0, tc = tile_cost(x < sp.W0 ? 0 : 1), sc = start_cost(x < sp.W0 ? 0 : 1);
         if (x >= sp.W0) c += NE + 1;
         int lo = 0, hi = NE - 1;  // largest e with H_kv c[e] <= x - base
         while (lo < hi) {
@@ -398,23 +406,24 @@ struct Ragged {
         r -= st.h * per;
         st.u0 = base + c[lo] * p.H_kv + st.h * per;
         if (JOINT && st.s.group) {
-            const int one = ((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0;
+            const int one = ((st.s.pfx + KT - 1) >> LKT) * tc + sc;
             st.k = (int)((unsigned)r / (unsigned)one);
             st.u0 += st.k * one;
         } else {
-            // largest k with cost_full(k) <= r: by the real root of k^2 TQ / 2 + k (S0 + KT (C0 + 1/2)) = r KT,
-            // then steps (the ceilings differ from the half-tile by less than one stream's cost)
+            // largest k with k streams costing at most r: by the real root of
+            // tc (k^2 TQ / 2 + k (S0 + KT / 2)) + k sc KT = r KT, then steps (the ceilings differ from the half
+            // tile by less than one stream's cost)
             const int S0 = st.s.L - st.s.T - st.s.pfx, last = (int)((unsigned)(st.s.T + (1 << lq) - 1) >> lq) - 1;
             int a = 0;
             if (last > 0) {
-                const float TQ = (float)(1 << lq), b1 = (float)S0 + 0.5f * TQ + KT * (RAGGED_C0 + 0.5f);
-                const float root = (sqrtf(b1 * b1 + 2.f * TQ * KT * (float)r) - b1) / TQ;
+                const float TQ = (float)(1 << lq), b1 = (float)S0 + 0.5f * TQ + KT * ((float)sc / tc + 0.5f);
+                const float root = (sqrtf(b1 * b1 + 2.f * TQ * KT * (float)r / tc) - b1) / TQ;
                 a = min(max((int)root, 0), last);
-                while (a > 0 && cost_full(S0, a, lq) > r) --a;
-                while (a < last && cost_full(S0, a + 1, lq) <= r) ++a;
+                while (a > 0 && tiles_full(S0, a, lq) * tc + a * sc > r) --a;
+                while (a < last && tiles_full(S0, a + 1, lq) * tc + (a + 1) * sc <= r) ++a;
             }
             st.k = a;
-            st.u0 += cost_full(S0, a, lq);
+            st.u0 += tiles_full(S0, a, lq) * tc + a * sc;
         }
         fill(p, st);
         return st;
@@ -430,15 +439,16 @@ struct Ragged {
         const int cl = cls(p, st.s);
         c += cl * (NE + 1);
         st.u0 = (cl == 0 ? 0 : sp.W0) + c[e] * p.H_kv + h * (c[e + 1] - c[e]);
-        if (JOINT && st.s.group) st.u0 += st.k * (((st.s.pfx + KT - 1) >> LKT) + RAGGED_C0);
-        else st.u0 += cost_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
+        const int n = JOINT && st.s.group ? st.k * ((st.s.pfx + KT - 1) >> LKT)
+                                          : tiles_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
+        st.u0 += n * tile_cost(cl) + st.k * start_cost(cl);
         fill(p, st);
         return st;
     }
     // The next stream of class cl after st; false if there is none.
     __device__ static bool next(const RaggedParams& p, Stream& st, int cl) {
         const int lq = LRT - p.lgG;
-        st.u0 += st.n + RAGGED_C0;
+        st.u0 += st.n * tile_cost(cl) + start_cost(cl);
         if (((int64_t)(st.k + 1) << lq) < st.s.T) {
             ++st.k;
         } else {
@@ -471,7 +481,10 @@ struct Ragged {
     __device__ static Seg segment(const RaggedParams& p, const Stream& st, int cl, int own, int x, int x1) {
         const int lq = LRT - p.lgG;
         Seg g;
-        const int j0 = max(x - st.u0 - RAGGED_C0, 0), j1 = min(max(x1 - st.u0 - RAGGED_C0, 0), st.n);
+        // a tile belongs to the worker that owns its first unit
+        const int tc = tile_cost(cl), first = st.u0 + start_cost(cl);
+        const int j0 = (int)((unsigned)max(x - first + tc - 1, 0) / (unsigned)tc);
+        const int j1 = min((int)((unsigned)max(x1 - first + tc - 1, 0) / (unsigned)tc), st.n);
         g.n = j1 - j0;
         g.cl = cl;
         g.seq = st.s.seq;
@@ -520,7 +533,7 @@ struct Ragged {
             if (k.step && !next(p, k.st, k.cl)) break;
             g = segment(p, k.st, k.cl, k.own, k.x, k.x1);
             k.cut = k.st.s.pfx == 0 && g.dst >= 0 && g.n > 0 && g.kv0 == 0;
-            k.x = k.st.u0 + RAGGED_C0 + k.st.n;
+            k.x = k.st.u0 + start_cost(k.cl) + k.st.n * tile_cost(k.cl);
             k.step = true;
         }
         return g;
@@ -528,7 +541,7 @@ struct Ragged {
     // Leaves the cut stream that ends worker w's range (k.cut, g its last segment) for the merge:
     // entry 3 i + w is (pieces, first owner, class, packed row), (rows of the tile, KV head).
     __device__ static void leave_cut(const RaggedParams& p, const Split& sp, const Walk& k, int i, int w, const Seg& g) {
-        const int last = owner(sp, k.st.u0 + RAGGED_C0 + k.st.n - 1);
+        const int last = owner_of(sp, k.st, k.cl, k.st.n - 1);
         p.cuts[2 * (3 * i + w)] = make_int4(last - k.own + 1, k.own, k.cl, g.row0);
         p.cuts[2 * (3 * i + w) + 1] = make_int4(g.ntok << p.lgG, g.h, 0, 0);
     }

@@ -84,7 +84,6 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;
     p.P = ragged_p(h, tc5);
-    p.lg_min = h->ctas > 0 ? 1 : kvc::RAGGED_LG_MIN;
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
     if (tc5) {
         // boxes of 64 query rows, and of as few as one token's

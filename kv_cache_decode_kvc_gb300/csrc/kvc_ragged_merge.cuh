@@ -228,11 +228,11 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
     }
     const typename R::Stream own = R::of_row(p, sp, p.plan, p.NG + lo, h, row);
     if (!own.s.ok) return;
-    const int of = R::owner(sp, own.u0 + RAGGED_C0), ol = R::owner(sp, own.u0 + RAGGED_C0 + own.n - 1);
+    const int oc = R::cls(p, own.s);
+    const int of = R::owner_of(sp, own, oc, 0), ol = R::owner_of(sp, own, oc, own.n - 1);
     const bool joint = own.s.pfx > 0;
     if (!joint && of == ol) return;  // written by its worker
     int pf = 0, pl = -1, pr = 0, pc = 0;
-    const int oc = R::cls(p, own.s);
     if (joint) {
         int a = 0, b = p.NG - 1;
         while (a < b) {
@@ -240,10 +240,10 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
             if (__ldg(p.groups + mid) <= lo) a = mid; else b = mid - 1;
         }
         const typename R::Stream pre = R::of_row(p, sp, p.plan, a, h, row);
-        pf = R::owner(sp, pre.u0 + RAGGED_C0);
-        pl = R::owner(sp, pre.u0 + RAGGED_C0 + pre.n - 1);
-        pr = ((row - pre.s.row0) << p.lgG) & (R::RT - 1);
         pc = R::cls(p, pre.s);
+        pf = R::owner_of(sp, pre, pc, 0);
+        pl = R::owner_of(sp, pre, pc, pre.n - 1);
+        pr = ((row - pre.s.row0) << p.lgG) & (R::RT - 1);
     }
     const int orow = ((row - own.s.row0) << p.lgG) & (R::RT - 1);
     const int n0 = pl - pf + 1, np = n0 + ol - of + 1;

@@ -37,7 +37,7 @@ struct RtCfg {
     using Seg = typename R::Seg;
     static constexpr int KT = R::KT;
     static constexpr int CB = D / 64;                // 128-byte column blocks of a row
-    static constexpr int QSET = 128 * D * 2;         // a set's query bytes: 128 rows, or two tiles of 64
+    static constexpr int QSET = 128 * D * 2;         // a set's query bytes: 128 rows
     static constexpr int TILE = KT * D * 2;          // bytes of a K or V tile
     static constexpr int GSTR = 1024 * CB;           // 8-row group stride of a K / V tile
     static constexpr int MISC = 3072;                // barriers, segments, exchanged maxima
@@ -120,6 +120,11 @@ __device__ __forceinline__ void tc5_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+// First row, of the set's 128, of its sc-th segment of class 1: its places are rows 0-63 and 64-127 in
+// turn.  A warp reads the tensor-memory lanes of its quarter and a quarter's warps sit on one
+// sub-partition of the SM, so up to 32 rows of set 1 take the places' upper halves: the sets work on
+// sub-partitions of their own.
+__device__ __forceinline__ int class1_row(int q, int sc, int rows) { return (sc & 1) * 64 + (rows <= 32 ? q * 32 : 0); }
 // 3-D copy of query rows: box (64 columns, G heads, tokens).
 __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, int col, int head, int token,
                                            uint64_t* bar) {
@@ -480,8 +485,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         M.nq[1 + 2 * l.q + place] = (sc >> 1) + 1;
                         mbar_arrive_expect_tx(&M.qfull[l.q][place], C::CB * (small ? few * 128 : 8192));
                         for (int cb = 0; cb < C::CB; ++cb)
-                            tma_load_q(q_s + l.q * C::QSET + place * (C::QSET / 2) + cb * 8192, small ? &tmQ1 : &tmQ, cb * 64,
-                                       g.h * G, g.row0, &M.qfull[l.q][place]);
+                            tma_load_q(q_s + l.q * C::QSET + cb * 16384 + class1_row(l.q, sc, rows) * 128, small ? &tmQ1 : &tmQ,
+                                       cb * 64, g.h * G, g.row0, &M.qfull[l.q][place]);
                     }
                     if (l.q) ++sc1;
                     else ++sc0;
@@ -564,13 +569,13 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             }
             __syncwarp();
         };
-        // S[q] = Q K^T, descriptors qb (column blocks qcb apart) and kb
-        auto score = [&](uint32_t q, uint32_t qb, uint32_t qcb, uint32_t kb, uint64_t* freed, uint64_t* qfreed) {
+        // S[q] = Q K^T, descriptors qb and kb.  (In class 1 the rows of the other place come along unused.)
+        auto score = [&](uint32_t q, uint32_t qb, uint32_t kb, uint64_t* freed, uint64_t* qfreed) {
             tc5_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc5_mma_ss(tm + q * 128, qb + (kk >> 2) * qcb + (((kk & 3) * 32) >> 4), (uint32_t)(dQ >> 32),
+                    tc5_mma_ss(tm + q * 128, qb + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), (uint32_t)(dQ >> 32),
                                kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), (uint32_t)(dK >> 32), ID1, kk > 0);
                 tc5_commit(&M.sfull[q]);
                 if (freed) tc5_commit(freed);
@@ -587,7 +592,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 issued = 1;
                 const uint32_t vb = (uint32_t)dV + uni(vs) * (C::TILE >> 4), kb = (uint32_t)dK + uni(ks) * (C::TILE >> 4);
                 const uint32_t q = uni(l.q), acc = uni(l.j > 0 ? 1u : 0u);
-                const uint32_t qb = (uint32_t)dQ + ((q * C::QSET + uni(place * (C::QSET / 2))) >> 4);
+                const uint32_t qb = (uint32_t)dQ + ((q * C::QSET) >> 4);
                 if (v) {
                     bool ok = wait_v(g, l.j) && wait_on(&M.pfull[q], (np >> q) & 1, ab, p.err);
                     np ^= 1u << q;
@@ -598,7 +603,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     bool ok = v || wait_on(&M.qfull[q][place], (sc >> 1) & 1, ab, p.err);
                     ok = ok && wait_item(ki);
                     if (!__all_sync(ALL, ok)) return false;
-                    score(q, qb, 8192 >> 4, kb, &M.empty[ks], nullptr);
+                    score(q, qb, kb, &M.empty[ks], nullptr);
                 }
                 item += (v ? 1 : 0) + (k ? 1 : 0);
                 if (v && !k) {
@@ -624,7 +629,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll 1
                 for (int q = 0; q < sets; ++q) {
                     const bool last = q + 1 == sets;
-                    score(uni(q), qb + ((uni(q) * C::QSET) >> 4), 16384 >> 4, k0, last ? &M.empty[item % C::NSLOT] : nullptr,
+                    score(uni(q), qb + ((uni(q) * C::QSET) >> 4), k0, last ? &M.empty[item % C::NSLOT] : nullptr,
                           last && n == 1 ? &M.qfree : nullptr);
                 }
                 ++item;
@@ -636,11 +641,11 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     if (!__all_sync(ALL, wait_v(g, j)) || !ready(0)) return false;
                     apply(0, vb, acc, nullptr, sets == 1 ? ve : nullptr);
                     if (!__all_sync(ALL, wait_item(item + 1))) return false;
-                    score(0, qb, 16384 >> 4, kb, sets == 1 ? ke : nullptr, sets == 1 ? qf : nullptr);
+                    score(0, qb, kb, sets == 1 ? ke : nullptr, sets == 1 ? qf : nullptr);
                     if (sets == 2) {
                         if (!ready(1)) return false;
                         apply(1, vb, acc, nullptr, ve);
-                        score(1, qb + (C::QSET >> 4), 16384 >> 4, kb, ke, qf);
+                        score(1, qb + (C::QSET >> 4), kb, ke, qf);
                     }
                     item += 2;
                 }
@@ -738,6 +743,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const float c = p.qscale;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_ts * 2)) & 31) == 0;
         uint32_t ns = 0, no = 0;
+        int sc = 0;  // segments of class 1 begun
         float* mine = &M.xm[set][half][r128];
         const float* other = &M.xm[set][half ^ 1][r128];
         // Both warps of a row's halves run the same loops to the end (a wait that gave up only skips the
@@ -768,14 +774,16 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (s == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
-            const int nrow = g.ntok << p.lgG, r0 = g.cl == 0 ? set * 128 : 0;  // the set's rows from r0
-            const int r = r0 + r128, rw = r - lane;                            // the warp's first row sees least
-            const bool idle = rw >= nrow;
+            const int nrow = g.ntok << p.lgG;
+            const int r0 = g.cl == 0 ? set * 128 : -class1_row(set, sc, nrow);  // the set's lane 0 is row r0
+            if (g.cl != 0) ++sc;
+            const int r = r0 + r128, rw = r - lane;                             // the warp's first row sees least
+            const bool idle = rw < 0 || rw >= nrow;
             bool ok = true;
             if (r0 < nrow) {
                 // Warps without rows: with at most 64 rows the others arrive for them, else they keep
                 // the protocol.
-                const int quads = (min(nrow - r0, 128) + 31) >> 5;
+                const int quads = (min(nrow - max(r0, 0), 128) + 31) >> 5;
                 const uint32_t count = quads == 1 ? 4 : quads == 2 ? 2 : 1;
                 const int limit = min(g.kv_end, g.lim0 + g.causal * (r >> p.lgG));
                 const int limit_w = min(g.kv_end, g.lim0 + g.causal * (rw >> p.lgG));
