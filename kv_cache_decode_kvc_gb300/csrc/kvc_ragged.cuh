@@ -54,7 +54,7 @@ struct RaggedParams {
     float* slot_o;   // [P][slots][slot rows][D]
     float* slot_ml;  // [P][slots][slot rows][2]
     int B, N, H_q, H_kv, lgG, NG, D;
-    int bs, max_blocks, num_blocks, T_max;
+    int bs, lgbs, max_blocks, num_blocks, T_max;
     int P;          // CTAs at most
     float qscale;   // log2(e) / sqrt(D)
 };
@@ -100,7 +100,7 @@ struct Entry {
 // Shared prefix of group g of sequences [b0, b1): in effect (whole blocks; a group of one shares
 // nothing); P as given may be out of range.
 __device__ __forceinline__ int prefix_used(const RaggedParams& p, int b0, int b1, int P) {
-    return (b1 - b0 < 2 || P < 0 || P > p.T_max) ? 0 : P / p.bs * p.bs;
+    return (b1 - b0 < 2 || P < 0 || P > p.T_max) ? 0 : P >> p.lgbs << p.lgbs;
 }
 __device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b, int row0, int row1, int L, int P, int used) {
     Entry s;

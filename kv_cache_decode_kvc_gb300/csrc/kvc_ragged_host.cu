@@ -80,6 +80,7 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.D = h->D;
     for (p.lgG = 0; (1 << p.lgG) < h->G; ++p.lgG) {}
     p.bs = h->bs;
+    for (p.lgbs = 0; (1 << p.lgbs) < h->bs; ++p.lgbs) {}
     p.max_blocks = h->max_blocks;
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;

@@ -254,13 +254,14 @@ struct Lane {
     int q, s, j;
     bool begun;      // K of tile j has been handled
     int ent, next;   // (copies) this CUDA lane's block of tile j and of the tile after it
+    bool peeked;     // .. which is the next segment's first
 };
 template <class Seg, class Fetch, class Turn, class Whole>
 __device__ __forceinline__ void replay(Fetch&& fetch, Turn&& turn, Whole&& whole) {
     Lane<Seg> a, b;
     a.q = a.s = a.j = b.s = b.j = 0;
     b.q = 1;
-    a.begun = b.begun = false;
+    a.begun = b.begun = a.peeked = b.peeked = false;
     bool both = true, more = true;  // class 0; lane a needs its next segment
     while (true) {
         if (more) {
@@ -431,45 +432,48 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         // tiles of class 1 are read once: they leave L2 first (the kernel's code and the batch's arrays, which
         // the next call needs from there, stay)
         const uint64_t pol0 = policy_evict_normal(), pol1 = policy_evict_first();
-        const int lrows = p.bs < C::KT ? p.bs : C::KT;  // rows of a copied box
-        const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qbuf);
-        uint32_t item = 0;
+        const int lgr = min(p.lgbs, 7);  // log2 of the rows of a copied box
+        const int bt = lane << lgr;      // this lane's box of a tile begins at this row
+        const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qbuf), to = bt * D * 2;
+        uint32_t slot = 0, filled = 0;    // the next item's slot; parity of the slots' uses
         int npair = 0, sc0 = 0, sc1 = 0;  // segments begun: of class 0, of class 1 by set
         auto entry = [&](const Seg& g, int j) {  // this lane's block of key tile j
-            const int t = g.kv0 + j * C::KT + lane * lrows;
-            return j < g.n && lane * lrows < C::KT && t < g.kv_end
-                       ? __ldg(p.table + (size_t)g.seq * p.max_blocks + t / p.bs)
-                       : 0;
+            const int t = g.kv0 + j * C::KT + bt;
+            return bt < C::KT && t < g.kv_end ? __ldg(p.table + (size_t)g.seq * p.max_blocks + (t >> p.lgbs)) : 0;
         };
         // K (isv false) or V of key tile j, whose block this CUDA lane knows
         auto copy = [&](const Seg& g, int j, int e, bool isv) {
-            const uint32_t slot = item % C::NSLOT, use = item / C::NSLOT;
+            const int t0 = g.kv0 + j * C::KT, rows = min(g.kv_end - t0, C::KT), nbox = (rows + (1 << lgr) - 1) >> lgr;
             bool ok = true;
-            if (lane == 0 && use > 0) ok = wait_on(&M.empty[slot], (use - 1) & 1, ab, p.err);
+            if (lane == 0) {
+                if (issued >= C::NSLOT) ok = wait_on(&M.empty[slot], filled & 1 ^ 1, ab, p.err);
+                if (ok) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)((nbox << lgr) * D * 2));
+            }
             if (!__all_sync(ALL, ok)) return false;
-            const int t0 = g.kv0 + j * C::KT, left = g.kv_end - t0;
-            const int nbox = left >= C::KT ? C::KT / lrows : (left + lrows - 1) / lrows;
-            if (lane == 0) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)(nbox * lrows * D * 2));
-            issued = ++item;
-            __syncwarp();
+            ++issued;
             if (lane < nbox) {
                 if ((unsigned)e >= (unsigned)p.num_blocks) {
                     atomicOr(p.err, DEV_BAD_BLOCK);
                     e = 0;
                 }
-                const int row = (int)(((int64_t)e * p.H_kv + g.h) * p.bs + (t0 + lane * lrows) % p.bs);
-                const uint32_t dst = ring_s + slot * C::TILE + lane * lrows * D * 2;
+                const int row = (int)((((int64_t)e * p.H_kv + g.h) << p.lgbs) + ((t0 + bt) & (p.bs - 1)));
+                const uint32_t dst = ring_s + slot * C::TILE + to;
                 const CUtensorMap* map = isv ? &tmV : &tmK;
                 const uint64_t pol = g.cl == 0 ? pol0 : pol1;
-                if constexpr (D == 128) tma_load_4d(dst, map, row >> 3, lrows >> 3, &M.full[slot], pol);
+                if constexpr (D == 128) tma_load_4d(dst, map, row >> 3, 0, &M.full[slot], pol);
                 else tma_load_2d(dst, map, 0, row, &M.full[slot], pol);
+            }
+            if (++slot == C::NSLOT) {
+                slot = 0;
+                ++filled;
             }
             return true;
         };
         replay<Seg>(
             [&](Lane<Seg>& l) {
                 const bool ok = take_seg(l);
-                if (ok && l.g.n > 0) l.next = entry(l.g, 0);
+                if (ok && !l.peeked && l.g.n > 0) l.next = entry(l.g, 0);
+                l.peeked = false;
                 return ok;
             },
             [&](Lane<Seg>& l, bool v, bool k) {  // class 1
@@ -497,9 +501,16 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     const int j = l.j + (i && v ? 1 : 0);
                     if (i) {
                         l.ent = l.next;
-                        l.next = entry(g, j + 1);
+                        if (j + 1 < g.n) l.next = entry(g, j + 1);
                     }
                     if (!copy(g, j, l.ent, i == 0)) return false;
+                }
+                // the segment after this one may be known: its first blocks are looked up ahead
+                if (k && (v ? l.j + 2 : 1) == g.n &&
+                    __all_sync(ALL, mbar_try_wait(&M.segfull[l.q][l.s & 1], (l.s >> 1) & 1))) {
+                    const Seg& n = M.seg[l.q][l.s & 1];
+                    l.next = n.n > 0 ? entry(n, 0) : 0;
+                    l.peeked = true;
                 }
                 return true;
             },
