@@ -452,8 +452,10 @@ struct Ragged {
         if (((int64_t)(st.k + 1) << lq) < st.s.T) {
             ++st.k;
         } else {
+            const bool one = st.k == 0;
             st.k = 0;
-            if (++st.h == p.H_kv) {
+            if (++st.h < p.H_kv && one) return true;  // the same keys of the next head
+            if (st.h == p.H_kv) {
                 st.h = 0;
                 do {
                     if (++st.e == groups(p) + p.B) return false;

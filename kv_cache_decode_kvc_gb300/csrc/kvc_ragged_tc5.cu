@@ -12,7 +12,7 @@
 // S = Q K^T (A = Q, B = K, both K-major); two threads per row load 64 scores each and agree on
 // the row's maximum through shared memory; the reference maximum is raised only if it grew by more
 // than 2^8 (then O is rescaled in place); the weights are written as bf16 over the scores'
-// columns; O += P V (A = P from tensor memory, B = V read MN-major).  Weights as bf16: a rounding
+// columns (each half over its own); O += P V (A = P from tensor memory, B = V read MN-major).  Weights as bf16: a rounding
 // of 2^-9 per weight, at most the output's own rounding after the division; fp32-like weights
 // would need a second product per tile.  The denominator sums the unrounded weights in fp32.
 //
@@ -29,6 +29,13 @@
 #include "kvc_ragged_merge.cuh"
 
 namespace kvc {
+
+// What the polling loops need beside the barrier: at a fixed place of shared memory.
+struct Give {
+    int abort;  // a wait gave up: the others follow
+    int pad;
+    uint32_t* err;
+};
 
 template <int D_, bool JOINT>
 struct RtCfg {
@@ -59,8 +66,9 @@ struct RtCfg {
         Seg seg[2][2];              // [set][place]
         float xm[2][2][128];        // [set][column half][row] maxima, then denominators
         int nonfinite[2][2];        // [set][place]: warp 3 took non-finite values out of V
-        int valid, abort_flag;
+        int valid;
         uint32_t tmem, nq[5];       // nq: copies of query rows begun per barrier (qpair, qfull)
+        Give give;
     };
     static_assert(sizeof(Misc) <= MISC, "misc area");
 };
@@ -120,6 +128,11 @@ __device__ __forceinline__ void tc5_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tc5_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // First row, of the set's 128, of its sc-th segment of class 1: its places are rows 0-63 and 64-127 in
 // turn.  A warp reads the tensor-memory lanes of its quarter and a quarter's warps sit on one
 // sub-partition of the SM, so up to 32 rows of set 1 take the places' upper halves: the sets work on
@@ -202,25 +215,35 @@ __device__ __forceinline__ void tc5_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo
 // The kernel's roles and their unrolled tiles together exceed the instruction cache if each use of a
 // helper is its own copy: the waits' polling, the rare paths and the roles' bodies are kept in one
 // place each.
-__device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err) {
-    return mbar_wait(bar, parity, abort_flag, err);
+__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err) {
-    return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort_flag, err);
-}
-// The softmax warps wait most of the time, up to sixteen of them at once: between polls they sleep, which
-// leaves the issue slots to the warps that work (a guarded tile took warp 3 up to 7 k cycles beside
-// polling warps).
-__device__ __noinline__ bool mbar_doze(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err, uint32_t ns) {
+// Polls until the phase has completed or the limit has passed (then the flag and the error word are
+// set).  ns: sleep between polls.  The softmax warps wait most of the time, up to sixteen of them at
+// once; asleep they leave the issue slots to the warps that work (a guarded tile took warp 3 up to 7 k
+// cycles beside polling warps).
+__device__ __noinline__ bool poll_at(uint32_t bar, uint32_t parity, uint32_t ns, Give* give) {
+    volatile int* flag = &give->abort;
+    const uint64_t t0 = global_ns();
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i) {
-        __nanosleep(ns);
-        if (mbar_try_wait(bar, parity)) return true;
+    while (true) {
+        if (ns) __nanosleep(ns);
+        if (try_at(bar, parity)) return true;
+        if (*flag) return false;
+        if (global_ns() - t0 > WAIT_LIMIT_NS) {
+            *flag = 1;
+            atomicOr(give->err, DEV_WAIT_TIMEOUT);
+            return false;
+        }
     }
-    return mbar_wait(bar, parity, abort_flag, err);
-}
-__device__ __forceinline__ bool wait_dozing(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* err, uint32_t ns) {
-    return mbar_try_wait(bar, parity) || mbar_doze(bar, parity, abort_flag, err, ns);
 }
 template <bool JOINT>
 __device__ __noinline__ void zero_rows(const RaggedParams& p, int tid, int n) {
@@ -311,7 +334,12 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     Misc& M = *reinterpret_cast<Misc*>(ring + C::NSLOT * C::TILE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = 1 << p.lgG;
-    int* ab = &M.abort_flag;
+    volatile int* ab = &M.give.abort;
+    // Waits for a barrier's phase (false: gave up); sleep: ns between polls.
+    auto wait_on = [&](uint64_t* bar, uint32_t parity, uint32_t sleep = 0) {
+        const uint32_t at = smem_addr(bar);
+        return try_at(at, parity) || poll_at(at, parity, sleep, &M.give);
+    };
     if (smem_addr(rt_smem) & 1023) {  // (the swizzled tiles need it; the declaration asks for it)
         if (tid == 0) atomicOr(p.err, DEV_WAIT_TIMEOUT);
         return;
@@ -337,7 +365,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         }
         mbar_init(&M.drain, 1);
         for (int i = 0; i < 5; ++i) M.nq[i] = 0;
-        M.abort_flag = 0;
+        M.give.abort = 0;
+        M.give.err = p.err;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -361,7 +390,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
 
     // A role's segment s of set q, as soon as it is known (the caller releases the place).
     auto fetch_seg = [&](int q, int s, Seg& g) {
-        const bool ok = wait_on(&M.segfull[q][s & 1], (s >> 1) & 1, ab, p.err);
+        const bool ok = wait_on(&M.segfull[q][s & 1], (s >> 1) & 1);
         if (ok) g = M.seg[q][s & 1];
         return ok;
     };
@@ -446,7 +475,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             const int t0 = g.kv0 + j * C::KT, rows = min(g.kv_end - t0, C::KT), nbox = (rows + (1 << lgr) - 1) >> lgr;
             bool ok = true;
             if (lane == 0) {
-                if (issued >= C::NSLOT) ok = wait_on(&M.empty[slot], filled & 1 ^ 1, ab, p.err);
+                if (issued >= C::NSLOT) ok = wait_on(&M.empty[slot], filled & 1 ^ 1);
                 if (ok) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)((nbox << lgr) * D * 2));
             }
             if (!__all_sync(ALL, ok)) return false;
@@ -484,7 +513,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     const int rows = g.ntok << p.lgG, few = G > 16 ? G : 16, sc = l.q ? sc1 : sc0, place = sc & 1;
                     const bool small = rows <= few;
                     bool ok = true;
-                    if (lane == 0 && npair > 0 && sc == 0) ok = wait_on(&M.qfree, (npair - 1) & 1, ab, p.err);
+                    if (lane == 0 && npair > 0 && sc == 0) ok = wait_on(&M.qfree, (npair - 1) & 1);
                     if (lane == 0 && ok) {
                         M.nq[1 + 2 * l.q + place] = (sc >> 1) + 1;
                         mbar_arrive_expect_tx(&M.qfull[l.q][place], C::CB * (small ? few * 128 : 8192));
@@ -520,7 +549,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 // done
                 const int boxes = ((g.ntok << p.lgG) + 63) / 64;
                 bool ok = true;
-                if (lane == 0 && npair > 0) ok = wait_on(&M.qfree, (npair - 1) & 1, ab, p.err);
+                if (lane == 0 && npair > 0) ok = wait_on(&M.qfree, (npair - 1) & 1);
                 ++npair;
                 if (lane == 0 && ok) {
                     M.nq[0] = npair;
@@ -555,13 +584,13 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const uint32_t tm = __shfl_sync(ALL, tmem, 0);
         uint32_t item = 0, fix = 0, np = 0;  // parities: each slot's next guarded use, each set's weights
         int npair = 0, sc0 = 0, sc1 = 0;
-        auto wait_item = [&](uint32_t it) { return wait_on(&M.full[it % C::NSLOT], (it / C::NSLOT) & 1, ab, p.err); };
+        auto wait_item = [&](uint32_t it) { return wait_on(&M.full[it % C::NSLOT], (it / C::NSLOT) & 1); };
         // a V tile that some row does not see all of has passed warp 3
         auto wait_v = [&](const Seg& g, int j) {
             bool ok = wait_item(item);
             if (ok && g.kv0 + (j + 1) * C::KT > g.lim0) {
                 const uint32_t sl = item % C::NSLOT;
-                ok = wait_on(&M.vfix[sl], (fix >> sl) & 1, ab, p.err);
+                ok = wait_on(&M.vfix[sl], (fix >> sl) & 1);
                 fix ^= 1u << sl;
             }
             return ok;
@@ -573,7 +602,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < C::KT / 16; ++kk)
-                    tc5_mma_ts(tm + 256 + q * D, tm + q * 128 + kk * 8, vb + ((kk * 2 * C::GSTR) >> 4), (uint32_t)(dV >> 32), ID2,
+                    tc5_mma_ts(tm + 256 + q * D, tm + q * 128 + (kk >> 2) * 64 + (kk & 3) * 8, vb + ((kk * 2 * C::GSTR) >> 4), (uint32_t)(dV >> 32), ID2,
                                kk > 0 ? 1u : acc);
                 if (done) tc5_commit(done);
                 if (freed) tc5_commit(freed);
@@ -605,13 +634,13 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 const uint32_t q = uni(l.q), acc = uni(l.j > 0 ? 1u : 0u);
                 const uint32_t qb = (uint32_t)dQ + ((q * C::QSET) >> 4);
                 if (v) {
-                    bool ok = wait_v(g, l.j) && wait_on(&M.pfull[q], (np >> q) & 1, ab, p.err);
+                    bool ok = wait_v(g, l.j) && wait_on(&M.pfull[q], (np >> q) & 1);
                     np ^= 1u << q;
                     if (!__all_sync(ALL, ok)) return false;
                     apply(q, vb, acc, k ? nullptr : &M.ofull[q], &M.empty[vs]);
                 }
                 if (k) {
-                    bool ok = v || wait_on(&M.qfull[q][place], (sc >> 1) & 1, ab, p.err);
+                    bool ok = v || wait_on(&M.qfull[q][place], (sc >> 1) & 1);
                     ok = ok && wait_item(ki);
                     if (!__all_sync(ALL, ok)) return false;
                     score(q, qb, kb, &M.empty[ks], nullptr);
@@ -630,11 +659,11 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 auto v_desc = [&](uint32_t it) { return (uint32_t)dV + uni(it % C::NSLOT) * (C::TILE >> 4); };
                 auto k_desc = [&](uint32_t it) { return (uint32_t)dK + uni(it % C::NSLOT) * (C::TILE >> 4); };
                 auto ready = [&](int q) {
-                    const bool ok = wait_on(&M.pfull[q], (np >> q) & 1, ab, p.err);
+                    const bool ok = wait_on(&M.pfull[q], (np >> q) & 1);
                     np ^= 1u << q;
                     return __all_sync(ALL, ok) != 0;
                 };
-                if (!__all_sync(ALL, wait_on(&M.qpair, npair++ & 1, ab, p.err) && wait_item(item))) return false;
+                if (!__all_sync(ALL, wait_on(&M.qpair, npair++ & 1) && wait_item(item))) return false;
                 issued = 1;
                 const uint32_t k0 = k_desc(item);
 #pragma unroll 1
@@ -678,7 +707,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         auto look = [&](const Lane<Seg>& l, int j) {
             const Seg& g = l.g;
             const uint32_t slot = item % C::NSLOT;
-            if (!__all_sync(ALL, wait_on(&M.full[slot], (item / C::NSLOT) & 1, ab, p.err))) return false;
+            if (!__all_sync(ALL, wait_on(&M.full[slot], (item / C::NSLOT) & 1))) return false;
             const int t0 = g.kv0 + j * C::KT;
             if (j >= 0 && t0 + C::KT > g.lim0) {
                 char* tile = ring + slot * C::TILE;
@@ -761,7 +790,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         // stores), so the barrier between them always completes.
         const int bar = 1 + set * 4 + quad;
         auto fetch_dozing = [&](int q, int s, Seg& g) {
-            const bool ok = wait_dozing(&M.segfull[q][s & 1], (s >> 1) & 1, ab, p.err, 40);
+            const bool ok = wait_on(&M.segfull[q][s & 1], (s >> 1) & 1, 40);
             if (ok) g = M.seg[q][s & 1];
             return ok;
         };
@@ -773,8 +802,9 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             const bool dry = s < 0;
             if (dry) {
                 g.n = 1;
-                g.seq = g.h = g.row0 = g.kv0 = g.cl = 0;
-                g.ntok = 256 >> p.lgG;
+                g.seq = g.h = g.row0 = g.kv0 = 0;
+                g.cl = JOINT || p.N > p.B ? 0 : 1;  // (the likelier first)
+                g.ntok = (g.cl == 0 ? 256 : 64) >> p.lgG;
                 g.kv_end = 100;
                 g.lim0 = 1;
                 g.causal = 1;
@@ -787,7 +817,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG;
             const int r0 = g.cl == 0 ? set * 128 : -class1_row(set, sc, nrow);  // the set's lane 0 is row r0
-            if (g.cl != 0) ++sc;
+            if (g.cl != 0 && !dry) ++sc;
             const int r = r0 + r128, rw = r - lane;                             // the warp's first row sees least
             const bool idle = rw < 0 || rw >= nrow;
             bool ok = true;
@@ -799,22 +829,62 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 const int limit = min(g.kv_end, g.lim0 + g.causal * (r >> p.lgG));
                 const int limit_w = min(g.kv_end, g.lim0 + g.causal * (rw >> p.lgG));
                 float m = -INFINITY, l = 0.f;  // reference maximum of the raw scores, sum of this half's weights
+                // Tile j's scores are in: waits, and gives the columns this warp's rows see of its half.
+                auto begin = [&](int j) {
+                    if (!dry) ok = wait_on(&M.sfull[set], ns++ & 1, 20) && ok;
+                    __syncwarp();
+                    tc5_fence_after();
+                    return g.kv0 + j * C::KT + half * 64;
+                };
+                // The row's maximum so far from this half's `top`; the reference is raised, and O with it, only if
+                // it grew by more than 2^8 (weights against a lower one keep their relative precision).
+                // Returns the weights' offset.
+                auto agree = [&](float top, int j) {
+                    *mine = top;
+                    named_bar_sync(bar, 64);
+                    top = fmaxf(top, *other);
+                    const bool raise = (top - m) * c > 8.f;
+                    if (__any_sync(ALL, raise)) {
+                        const float mn = raise ? top : m;
+                        const float f = raise ? fast_exp2((m - mn) * c) : 1.f;
+                        if (j > 0) {
+                            // the products into O so far are complete (S of this tile came behind them)
+#pragma unroll 1
+                            for (int d = 0; d < C::HD; d += 32) {
+                                float o[32];
+                                tc5_ld32(tO + d, o);
+                                uint32_t u[32];
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+                                tc5_st32(tO + d, u);
+                            }
+                        }
+                        l *= f;
+                        m = mn;
+                    }
+                    return m == -INFINITY ? 0.f : -m * c;  // nothing seen yet: weights 2^-inf = 0
+                };
+                auto finish = [&](const float2& s) {
+                    l += s.x + s.y;
+                    tc5_wait_st();
+                    tc5_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], count);
+                };
                 if (idle) {
-                    if (count > 1) {
+                    if (dry) {
+                    } else if (count > 1) {
                         ns += g.n;
                     } else {
                         for (int j = 0; j < g.n; ++j) {
-                            ok = wait_dozing(&M.sfull[set], ns++ & 1, ab, p.err, 20) && ok;
+                            ok = wait_on(&M.sfull[set], ns++ & 1, 20) && ok;
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&M.pfull[set]);
                         }
                     }
-                } else {
+                } else if (g.cl == 0) {
                     for (int j = 0; j < g.n; ++j) {
-                        if (!dry) ok = wait_dozing(&M.sfull[set], ns++ & 1, ab, p.err, 20) && ok;
-                        __syncwarp();
-                        tc5_fence_after();
-                        const int t0 = g.kv0 + j * C::KT + half * 64;
+                        const int t0 = begin(j);
                         float v[64];
                         tc5_ld64(tS + half * 64, v);
                         if (t0 + 64 > limit_w) {
@@ -830,34 +900,9 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             mx[2] = fmaxf(mx[2], v[i + 2]);
                             mx[3] = fmaxf(mx[3], v[i + 3]);
                         }
-                        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        *mine = top;
-                        // (also: both halves' scores are loaded, the weights may cover them)
-                        named_bar_sync(bar, 64);
-                        top = fmaxf(top, *other);
-                        // weights up to 2^8 against the reference keep their relative precision
-                        const bool raise = (top - m) * c > 8.f;
-                        if (__any_sync(ALL, raise)) {
-                            const float mn = raise ? top : m;
-                            const float f = raise ? fast_exp2((m - mn) * c) : 1.f;
-                            if (j > 0) {
-                                // the products into O so far are complete (S of this tile came behind them)
-#pragma unroll 1
-                                for (int d = 0; d < C::HD; d += 32) {
-                                    float o[32];
-                                    tc5_ld32(tO + d, o);
-                                    uint32_t u[32];
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                                    tc5_st32(tO + d, u);
-                                }
-                            }
-                            l *= f;
-                            m = mn;
-                        }
-                        const float mc = m == -INFINITY ? 0.f : -m * c;  // nothing seen yet: weights 2^-inf = 0
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        const float mc = agree(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), j);
                         const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         uint32_t w[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -866,16 +911,45 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                             w[i] = bf16x2_rn(e.x, e.y);
                         }
-                        if (!dry) tc5_st32(tS + half * 32, w);
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        tc5_wait_st();
-                        tc5_fence_before();
-                        __syncwarp();
-                        if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], count);
+                        if (!dry) tc5_st32(tS + half * 64, w);
+                        finish(__fadd2_rn(sum[0], sum[1]));
+                    }
+                } else {
+                    // Few rows: the loop is kept short instead, 16 columns at a time, loaded again for the weights (all
+                    // roles' code runs in turns here and has to fit the instruction cache).
+                    for (int j = 0; j < g.n; ++j) {
+                        const int see = limit - begin(j);
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int d = 0; d < 64; d += 16) {
+                            float x[16];
+                            tc5_ld16(tS + half * 64 + d, x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) top = fmaxf(top, d + i < see ? x[i] : -INFINITY);
+                        }
+                        const float mc = agree(top, j);
+                        const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+                        for (int d = 0; d < 64; d += 16) {
+                            float x[16];
+                            tc5_ld16(tS + half * 64 + d, x);
+                            uint32_t w[8];  // (they take the place of scores already read)
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 y = make_float2(d + i < see ? x[i] : -INFINITY, d + i + 1 < see ? x[i + 1] : -INFINITY);
+                                const float2 a = __ffma2_rn(y, c2, mc2);
+                                const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                                sum = __fadd2_rn(sum, e);
+                                w[i / 2] = bf16x2_rn(e.x, e.y);
+                            }
+                            if (!dry) tc5_st8(tS + half * 64 + d / 2, w);
+                        }
+                        finish(sum);
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                if (!dry) ok = wait_dozing(&M.ofull[set], no++ & 1, ab, p.err, idle ? 400 : 20) && ok;
+                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, idle ? 400 : 20) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
