@@ -22,6 +22,7 @@ def _built():
 def test_views_hold_their_cache(make, monkeypatch):
     # the handle is destroyed when the last view goes, not before (counted on the host: a view
     # without its cache is never read)
+    gc.collect()  # caches that earlier tests left
     destroyed = []
     real = kvc.kvc_destroy
     monkeypatch.setattr(kvc, "kvc_destroy", lambda h: (destroyed.append(h), real(h)))
@@ -30,13 +31,13 @@ def test_views_hold_their_cache(make, monkeypatch):
     h = cache.h
     del cache
     gc.collect()
-    assert destroyed == []
+    assert h not in destroyed
     views[0].zero_()
     assert not views[0].float().any()
     last = views[-1][0]
     del views
     gc.collect()
-    assert destroyed == []
+    assert h not in destroyed
     del last
     gc.collect()
-    assert destroyed == [h]
+    assert destroyed.count(h) == 1
