@@ -226,6 +226,19 @@ __device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Has the phase completed?  Returns at once: try_wait may hold its thread for thousands of cycles, which is
+// what a thread that waits wants and one with other work does not.
+__device__ __forceinline__ bool done_at(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Polls until the phase has completed or the limit has passed (then the flag and the error word are
 // set).  ns: sleep between polls.  The softmax warps wait most of the time, up to sixteen of them at
 // once; asleep they leave the issue slots to the warps that work (a guarded tile took warp 3 up to 7 k
@@ -439,7 +452,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (lane > 0 && s < s0) s = s0;
             const int q0 = lane == 2 ? 1 : 0, q1 = lane == 1 ? 0 : 1;
             const uint32_t ph = ((s - 2) >> 1) & 1;
-            if (s < 2 || (mbar_try_wait(&M.segempty[q0][s & 1], ph) && mbar_try_wait(&M.segempty[q1][s & 1], ph))) {
+            if (s < 2 || (done_at(&M.segempty[q0][s & 1], ph) && done_at(&M.segempty[q1][s & 1], ph))) {
                 for (int q = q0; q <= q1; ++q) {
                     M.seg[q][s & 1] = g;
                     mbar_arrive(&M.segfull[q][s & 1]);
@@ -536,7 +549,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 }
                 // the segment after this one may be known: its first blocks are looked up ahead
                 if (k && (v ? l.j + 2 : 1) == g.n &&
-                    __all_sync(ALL, mbar_try_wait(&M.segfull[l.q][l.s & 1], (l.s >> 1) & 1))) {
+                    __all_sync(ALL, done_at(&M.segfull[l.q][l.s & 1], (l.s >> 1) & 1))) {
                     const Seg& n = M.seg[l.q][l.s & 1];
                     l.next = n.n > 0 ? entry(n, 0) : 0;
                     l.peeked = true;
@@ -864,16 +877,19 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     }
                     return m == -INFINITY ? 0.f : -m * c;  // nothing seen yet: weights 2^-inf = 0
                 };
-                auto finish = [&](const float2& s) {
+                // All 8 warps arrive for a segment's first tile, each of them once its rows of the segment before are
+                // stored (its first product overwrites O, of all rows); later tiles' idle ones are arrived for.
+                auto finish = [&](const float2& s, int j) {
                     l += s.x + s.y;
                     tc5_wait_st();
                     tc5_fence_before();
                     __syncwarp();
-                    if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], count);
+                    if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], j == 0 ? 1 : count);
                 };
                 if (idle) {
                     if (dry) {
                     } else if (count > 1) {
+                        if (lane == 0) mbar_arrive(&M.pfull[set]);
                         ns += g.n;
                     } else {
                         for (int j = 0; j < g.n; ++j) {
@@ -912,7 +928,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             w[i] = bf16x2_rn(e.x, e.y);
                         }
                         if (!dry) tc5_st32(tS + half * 64, w);
-                        finish(__fadd2_rn(sum[0], sum[1]));
+                        finish(__fadd2_rn(sum[0], sum[1]), j);
                     }
                 } else {
                     // Few rows: the loop is kept short instead, 16 columns at a time, loaded again for the weights (all
@@ -945,11 +961,11 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             }
                             if (!dry) tc5_st8(tS + half * 64 + d / 2, w);
                         }
-                        finish(sum);
+                        finish(sum, j);
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, idle ? 400 : 20) && ok;
+                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, idle ? 100 : 20) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
