@@ -133,11 +133,15 @@ __device__ __forceinline__ void tc5_st8(uint32_t taddr, const uint32_t (&r)[8]) 
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// Query rows of the smaller copied box: 16, or a token's if it has more.
+__host__ __device__ constexpr int few_rows(int G) { return G > 16 ? G : 16; }
 // First row, of the set's 128, of its sc-th segment of class 1: its places are rows 0-63 and 64-127 in
 // turn.  A warp reads the tensor-memory lanes of its quarter and a quarter's warps sit on one
-// sub-partition of the SM, so up to 32 rows of set 1 take the places' upper halves: the sets work on
-// sub-partitions of their own.
-__device__ __forceinline__ int class1_row(int q, int sc, int rows) { return (sc & 1) * 64 + (rows <= 32 ? q * 32 : 0); }
+// sub-partition of the SM, so a smaller box of up to 32 rows of set 1 takes the places' upper halves: the
+// sets work on sub-partitions of their own.  (The box of 64 rows fills a place.)
+__device__ __forceinline__ int class1_row(int q, int sc, int rows, int G) {
+    return (sc & 1) * 64 + (rows <= min(few_rows(G), 32) ? q * 32 : 0);
+}
 // 3-D copy of query rows: box (64 columns, G heads, tokens).
 __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, int col, int head, int token,
                                            uint64_t* bar) {
@@ -523,7 +527,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 if (!v) {
                     // the segment's query rows, into the set's places in turn: a place comes free with the
                     // segment before the last, the first ones with class 0's last products
-                    const int rows = g.ntok << p.lgG, few = G > 16 ? G : 16, sc = l.q ? sc1 : sc0, place = sc & 1;
+                    const int rows = g.ntok << p.lgG, few = few_rows(G), sc = l.q ? sc1 : sc0, place = sc & 1;
                     const bool small = rows <= few;
                     bool ok = true;
                     if (lane == 0 && npair > 0 && sc == 0) ok = wait_on(&M.qfree, (npair - 1) & 1);
@@ -531,7 +535,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         M.nq[1 + 2 * l.q + place] = (sc >> 1) + 1;
                         mbar_arrive_expect_tx(&M.qfull[l.q][place], C::CB * (small ? few * 128 : 8192));
                         for (int cb = 0; cb < C::CB; ++cb)
-                            tma_load_q(q_s + l.q * C::QSET + cb * 16384 + class1_row(l.q, sc, rows) * 128, small ? &tmQ1 : &tmQ,
+                            tma_load_q(q_s + l.q * C::QSET + cb * 16384 + class1_row(l.q, sc, rows, G) * 128, small ? &tmQ1 : &tmQ,
                                        cb * 64, g.h * G, g.row0, &M.qfull[l.q][place]);
                     }
                     if (l.q) ++sc1;
@@ -829,7 +833,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG;
-            const int r0 = g.cl == 0 ? set * 128 : -class1_row(set, sc, nrow);  // the set's lane 0 is row r0
+            const int r0 = g.cl == 0 ? set * 128 : -class1_row(set, sc, nrow, G);  // the set's lane 0 is row r0
             if (g.cl != 0 && !dry) ++sc;
             const int r = r0 + r128, rw = r - lane;                             // the warp's first row sees least
             const bool idle = rw < 0 || rw >= nrow;
