@@ -429,12 +429,12 @@ struct Ragged {
         return st;
     }
     // The stream of packed row `row` of entry e.
-    __device__ static Stream of_row(const RaggedParams& p, const Split& sp, const int* c, int e, int h, int row) {
+    __device__ static Stream of_row(const RaggedParams& p, const Split& sp, const int* c, int e, const Entry& s, int h, int row) {
         const int NE = groups(p) + p.B, lq = LRT - p.lgG;
         Stream st;
         st.e = e;
         st.h = h;
-        st.s = entry_of(p, e);
+        st.s = s;
         st.k = (row - st.s.row0) >> lq;
         const int cl = cls(p, st.s);
         c += cl * (NE + 1);

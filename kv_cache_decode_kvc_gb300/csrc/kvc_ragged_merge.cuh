@@ -211,6 +211,14 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const Ragg
         merge_store<T>(p, merge_pieces(p, a.x, 0, 1, lane, at_row(r)), out_of(r), lane);
 }
 
+// The last i < n <= MAX_B with a[i] <= x of an ascending array with a[0] <= x, by a converged warp in two
+// loads one behind the other (halving it takes up to ten).
+__device__ __forceinline__ int last_at(const int* a, int n, int x, int lane) {
+    static_assert(MAX_B <= 32 * 32);
+    const int b = 32 * (__popc(__ballot_sync(0xFFFFFFFFu, 32 * lane < n && __ldg(a + 32 * lane) <= x)) - 1);
+    return b + __popc(__ballot_sync(0xFFFFFFFFu, b + lane < n && __ldg(a + b + lane) <= x)) - 1;
+}
+
 // With groups: block (row, KV head, y), a warp per query head 8 y + warp of the group; the row's
 // pieces are those of its prefix stream and of its sequence's own stream.
 template <typename T, class R>
@@ -221,12 +229,11 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
     if (!sp.valid) return;
     const int row = blockIdx.x, h = blockIdx.y, G = 1 << p.lgG;
     if (row >= __ldg(p.cu + p.B)) return;
-    int lo = 0, hi = p.B - 1;  // the sequence: largest b with cu[b] <= row
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.cu + mid) <= row) lo = mid; else hi = mid - 1;
-    }
-    const typename R::Stream own = R::of_row(p, sp, p.plan, p.NG + lo, h, row);
+    const int lo = last_at(p.cu, p.B, row, lane);  // the sequence
+    const int a = last_at(p.groups, p.NG, lo, lane), b0 = __ldg(p.groups + a), b1 = __ldg(p.groups + a + 1);
+    const int P = __ldg(p.prefix + a), used = prefix_used(p, b0, b1, P);
+    const typename R::Stream own =
+        R::of_row(p, sp, p.plan, p.NG + lo, seq_entry(p, lo, __ldg(p.cu + lo), __ldg(p.cu + lo + 1), __ldg(p.lens + lo), P, used), h, row);
     if (!own.s.ok) return;
     const int oc = R::cls(p, own.s);
     const int of = R::owner_of(sp, own, oc, 0), ol = R::owner_of(sp, own, oc, own.n - 1);
@@ -234,12 +241,8 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
     if (!joint && of == ol) return;  // written by its worker
     int pf = 0, pl = -1, pr = 0, pc = 0;
     if (joint) {
-        int a = 0, b = p.NG - 1;
-        while (a < b) {
-            const int mid = (a + b + 1) >> 1;
-            if (__ldg(p.groups + mid) <= lo) a = mid; else b = mid - 1;
-        }
-        const typename R::Stream pre = R::of_row(p, sp, p.plan, a, h, row);
+        const typename R::Stream pre =
+            R::of_row(p, sp, p.plan, a, group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), used), h, row);
         pc = R::cls(p, pre.s);
         pf = R::owner_of(sp, pre, pc, 0);
         pl = R::owner_of(sp, pre, pc, pre.n - 1);
