@@ -273,7 +273,8 @@ int kvc_get_paged_shape(kvc_t h, int* num_blocks, int* block_size, int* max_bloc
  *     pointers and strides are multiples of 16 bytes, stride >= H * D.
  *   - cu_seqlens (int32 [B + 1], device): sequence b's new tokens are rows [cu[b], cu[b + 1]),
  *     T_b of them.  cu[0] = 0, cu does not decrease, cu[B] <= N; else KVC_DEV_BAD_SEQ is set and
- *     the call writes nothing.  Rows [cu[B], N) are padding: neither read nor written.
+ *     the call writes nothing.  Rows [cu[B], N) are padding: whatever they hold is not used, and
+ *     nothing is written to them.
  *   - lens[b] counts the sequence's positions with its new tokens: row i of sequence b is position
  *     lens[b] - T_b + i.  T_b <= lens[b] <= T_max, else KVC_DEV_BAD_LENS is set, that sequence's
  *     rows are not appended and its attention outputs are zero.  lens[b] of a sequence without new

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) append_rope_kernel(const Rope
             int64_t kr = -1;
             if (b < p.B && row < p.N) {
                 const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
-                if (c0 <= row) {  // (else cu does not ascend)
+                if (c0 >= 0 && c0 <= row && row < c1 && c1 <= p.N) {  // (else cu does not ascend within 0 .. N)
                     if (L < c1 - c0 || L > p.T_max) {
                         atomicOr(p.err, DEV_BAD_LENS);
                     } else {
@@ -219,7 +219,7 @@ static int launch_rope(const RopeParams& p, const RopeTable& t, int sms, cudaStr
     // a few rows).
     const bool many = p.N >= 8 * sms;
     const int tb = many ? 4 : 1;
-    cfg.gridDim = dim3((unsigned)((p.N + tb - 1) / tb));
+    cfg.gridDim = dim3(((unsigned)p.N + tb - 1) / tb);
     cfg.blockDim = dim3(ROPE_THREADS);
     cfg.stream = s;
     cfg.attrs = attr;

@@ -524,16 +524,17 @@ class Rope:
 def _packed(t, heads, D, dtype, what):
     """Elements between tokens of a packed [N, heads, D] tensor."""
     sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype:
-        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype}, got {tuple(sh)} {t.dtype}")
+    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype} on the GPU, got {tuple(sh)} {t.dtype} on {t.device}")
     if st[2] != 1 or (st[1] != D and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {st}")
     return st[0] if sh[0] > 1 else max(st[0], heads * D)
 
 
 def _index(t, what, int32, *shape):
-    if t.dtype != int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: want contiguous int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.dtype != int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: want contiguous int32 {list(shape)} on the GPU, got {t.dtype} {list(t.shape)} on "
+                         f"{t.device}")
 
 
 class PagedKVCache(KVCache):
@@ -600,9 +601,9 @@ class PagedKVCache(KVCache):
             if positions.dim() == 1 and rope.n_axes == 1:
                 positions = positions[None]
             if positions.dtype != int32 or tuple(positions.shape) != (rope.n_axes, N) or (
-                    N > 1 and positions.stride(1) != 1):
-                raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}], got {positions.dtype} "
-                                 f"{list(positions.shape)}")
+                    N > 1 and positions.stride(1) != 1) or not positions.is_cuda:
+                raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}] on the GPU, got {positions.dtype} "
+                                 f"{list(positions.shape)} on {positions.device}")
             ps = max(positions.stride(0), N)
         self._batch(block_table, cu_seqlens, lens, int32)
         kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
@@ -623,8 +624,8 @@ class PagedKVCache(KVCache):
             # allocated on the call's stream, so that its next use is ordered behind this call
             with _torch.cuda.stream(_as_stream(stream)):
                 workspace = _torch.empty(self.attn_workspace_bytes(N, NG), dtype=_torch.uint8, device="cuda")
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace: want a contiguous tensor")
+        elif not workspace.is_contiguous() or not workspace.is_cuda:
+            raise ValueError("workspace: want a contiguous tensor on the GPU")
         return N, qs, os_, workspace, workspace.numel() * workspace.element_size()
 
     def attn_ragged(self, layer, q, out, block_table, cu_seqlens, lens, workspace=None, stream=None):

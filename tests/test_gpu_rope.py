@@ -144,3 +144,21 @@ def test_append_rope_flags_and_skips_bad_sequences():
         assert c.last_error() == (kvc.KVC_EDEVICE, kvc.KVC_DEV_BAD_SEQ)
         K, V = (x.cpu() for x in c.layer_views(0))
         assert torch.equal(K, bt.K) and torch.equal(V, bt.V) and not q_out.any()
+
+
+def test_append_rope_looks_nothing_up_for_rows_outside_their_sequence():
+    # sequence bounds out of order or out of range in the middle: whichever sequence a row falls to, its
+    # slot is looked up only if the row lies within it
+    bt = Batch([2, 3, 1, 2, 1], [4, 40, 9, 0, 30], 16, 4, 2, 64, seed=6)
+    rope = kvc.Rope(_freq(64))
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    for cu in ([0, 50, 6, 3, 8, 9], [0, lo, 5, 6, 8, 9], [0, 2, 5, hi, 8, 9], [0, 2, 5, 6, 8, hi], [0, hi, hi, lo, 8, 9],
+               [lo, lo, lo, lo, lo, hi]):
+        c, d = bt.cache(kvc), bt.dev()
+        d["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        q_out = torch.zeros_like(d["q"])
+        c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], q_out)
+        status, word = c.last_error()
+        assert status == kvc.KVC_EDEVICE and word & kvc.KVC_DEV_BAD_SEQ
+        K, V = (x.cpu() for x in c.layer_views(0))
+        assert torch.equal(K, bt.K) and torch.equal(V, bt.V) and not q_out.any()

@@ -60,3 +60,12 @@ def test_null_handles_are_refused(lib):
     assert lib.kvc_paged_attn_shared(None, 0, 16, 16, 16, 16, 16, 16, 16, 1, 16, 16, 1, 256, 1 << 40,
                                      None) == kvc.KVC_EINVAL
     assert lib.kvc_paged_attn_workspace(None, 1, 0, ctypes.byref(n)) == kvc.KVC_EINVAL
+
+
+def test_tensors_on_the_host_are_refused():
+    import torch
+    x, i = torch.zeros(3, 2, 64), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the GPU"):
+        kvc._packed(x, 2, 64, torch.float32, "q")
+    with pytest.raises(ValueError, match="on the GPU"):
+        kvc._index(i, "lens", torch.int32, 4)
