@@ -170,8 +170,10 @@ struct Ragged {
     __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
     __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 8 : 4; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
-    // of it (a worker's share, half of that in class 1, is a tile's cost or more).
-    static constexpr int LG_MIN = PAIRS ? 3 : 1;
+    // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
+    // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at
+    // 500 positions 26.5 against 31.3 with the smaller).
+    __device__ static int lg_min(int W0) { return !PAIRS ? 0 : W0 > 0 ? 3 : 2; }
     __device__ static int groups(const RaggedParams& p) { return JOINT ? p.NG : 0; }
     __device__ static Entry entry_of(const RaggedParams& p, int e) {
         if (JOINT && e < p.NG) return group_entry(p, e);
@@ -211,7 +213,7 @@ struct Ragged {
         bool valid;
     };
     __device__ static void divide(const RaggedParams& p, Split& sp) {
-        const int want = sp.U >> LG_MIN;
+        const int want = sp.U >> lg_min(sp.W0);
         sp.P = sp.U == 0 ? 0 : max(1, min(want, p.P));
         sp.each = sp.U == 0 ? 0 : (int)((unsigned)sp.U / (unsigned)sp.P);
         sp.more = sp.U - sp.each * sp.P;

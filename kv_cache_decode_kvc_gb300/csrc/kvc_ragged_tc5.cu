@@ -12,9 +12,21 @@
 // S = Q K^T (A = Q, B = K, both K-major); two threads per row load 64 scores each and agree on
 // the row's maximum through shared memory; the reference maximum is raised only if it grew by more
 // than 2^8 (then O is rescaled in place); the weights are written as bf16 over the scores'
-// columns (each half over its own); O += P V (A = P from tensor memory, B = V read MN-major).  Weights as bf16: a rounding
-// of 2^-9 per weight, at most the output's own rounding after the division; fp32-like weights
-// would need a second product per tile.  The denominator sums the unrounded weights in fp32.
+// columns (each half over its own); O += P V (A = P from tensor memory, B = V read MN-major).
+// Weights as bf16: each is off by at most half a step, 2^-8 of it, as the output itself is after the
+// division; weights in two bf16 parts would need a second product per tile.  The denominator sums the
+// unrounded weights in fp32.
+//
+// What bounds it.  Class 0: the chain of a set, S product (512 cycles at D = 128) - softmax (about 1600: 64
+// scores a thread, of which 540 are the exponentials of two warps on one sub-partition) - P product
+// (512), against 1024 cycles of the tensor core for the other set in the meantime; tensor memory holds S
+// and O of two sets and no more.  1216 tokens of 32 heads at 16,384 positions: tensor pipe 65 % busy; a chunk
+// of 4096 tokens of 64 heads behind 12,288 positions: 1284 us, 1.50 PFLOP/s (0.77 of cuBLAS's burst rate).
+// Signalling the weights in two parts (their product begins earlier) took 1457, the extra waits cost more.
+// Class 1, long streams: memory (24 single tokens at 3000 positions: a pair of 32 KB tiles per set every 6.9 k
+// cycles, 5.4 TB/s).  Class 1, streams of a tile or two: the roles' code, run in turns, exceeds the 32 KB
+// instruction cache (5200 misses per SM in 84 us at 256 tokens of 251 positions, no-instruction stalls ahead
+// of all but the waits), so a stream costs about 8 k cycles per set whatever it holds.
 //
 // Warps: 0 copies (TMA), 1 issues the products, 2 computes the split and walks the streams, 3 guards
 // masked values, 4-11 set 0 and 12-19 set 1 (four warps per half of the columns).  K and V tiles
@@ -811,30 +823,15 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             if (ok) g = M.seg[q][s & 1];
             return ok;
         };
-        // The first pass (s = -1) is dry: one made-up tile, nothing waited for, stored or signalled.  It brings
-        // the loop's code into the instruction cache while warp 2 computes the split (10 us less on
-        // small batches).
-        for (int s = -1;; ++s) {
+        for (int s = 0;; ++s) {
             Seg g;
-            const bool dry = s < 0;
-            if (dry) {
-                g.n = 1;
-                g.seq = g.h = g.row0 = g.kv0 = 0;
-                g.cl = JOINT || p.N > p.B ? 0 : 1;  // (the likelier first)
-                g.ntok = (g.cl == 0 ? 256 : 64) >> p.lgG;
-                g.kv_end = 100;
-                g.lim0 = 1;
-                g.causal = 1;
-                g.dst = -1;
-            } else if (!pair_all(bar, fetch_dozing(set, s, g))) {
-                break;
-            }
+            if (!pair_all(bar, fetch_dozing(set, s, g))) break;
             if (s == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG;
             const int r0 = g.cl == 0 ? set * 128 : -class1_row(set, sc, nrow, G);  // the set's lane 0 is row r0
-            if (g.cl != 0 && !dry) ++sc;
+            if (g.cl != 0) ++sc;
             const int r = r0 + r128, rw = r - lane;                             // the warp's first row sees least
             const bool idle = rw < 0 || rw >= nrow;
             bool ok = true;
@@ -848,7 +845,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 float m = -INFINITY, l = 0.f;  // reference maximum of the raw scores, sum of this half's weights
                 // Tile j's scores are in: waits, and gives the columns this warp's rows see of its half.
                 auto begin = [&](int j) {
-                    if (!dry) ok = wait_on(&M.sfull[set], ns++ & 1, 20) && ok;
+                    ok = wait_on(&M.sfull[set], ns++ & 1, 20) && ok;
                     __syncwarp();
                     tc5_fence_after();
                     return g.kv0 + j * C::KT + half * 64;
@@ -888,11 +885,10 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     tc5_wait_st();
                     tc5_fence_before();
                     __syncwarp();
-                    if (lane == 0 && !dry) mbar_arrive_n(&M.pfull[set], j == 0 ? 1 : count);
+                    if (lane == 0) mbar_arrive_n(&M.pfull[set], j == 0 ? 1 : count);
                 };
                 if (idle) {
-                    if (dry) {
-                    } else if (count > 1) {
+                    if (count > 1) {
                         if (lane == 0) mbar_arrive(&M.pfull[set]);
                         ns += g.n;
                     } else {
@@ -931,7 +927,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
                             w[i] = bf16x2_rn(e.x, e.y);
                         }
-                        if (!dry) tc5_st32(tS + half * 64, w);
+                        tc5_st32(tS + half * 64, w);
                         finish(__fadd2_rn(sum[0], sum[1]), j);
                     }
                 } else {
@@ -963,18 +959,18 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                                 sum = __fadd2_rn(sum, e);
                                 w[i / 2] = bf16x2_rn(e.x, e.y);
                             }
-                            if (!dry) tc5_st8(tS + half * 64 + d / 2, w);
+                            tc5_st8(tS + half * 64 + d / 2, w);
                         }
                         finish(sum, j);
                     }
                 }
                 // ---- the segment's state: written out, or left as a piece
-                if (!dry) ok = wait_on(&M.ofull[set], no++ & 1, idle ? 100 : 20) && ok;
+                ok = wait_on(&M.ofull[set], no++ & 1, idle ? 100 : 20) && ok;
                 if (!idle) {
                     __syncwarp();
                     tc5_fence_after();
                     *mine = l;
-                    ok = pair_all(bar, ok && !dry);
+                    ok = pair_all(bar, ok);
                     l += *other;
                     named_bar_sync(bar, 64);  // read on both sides before the next segment's maxima
                     const bool nonfin = *(volatile int*)&M.nonfinite[set][s & 1] != 0;
@@ -1021,7 +1017,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 }
             }
             __syncwarp();
-            if (lane == 0 && !dry) mbar_arrive(&M.segempty[set][s & 1]);
+            if (lane == 0) mbar_arrive(&M.segempty[set][s & 1]);
         }
     }
     __syncwarp();
