@@ -22,7 +22,7 @@
 // (512), against 1024 cycles of the tensor core for the other set in the meantime; tensor memory holds S
 // and O of two sets and no more.  1216 tokens of 32 heads at 16,384 positions: tensor pipe 65 % busy; a chunk
 // of 4096 tokens of 64 heads behind 12,288 positions: 1284 us, 1.50 PFLOP/s (0.77 of cuBLAS's burst rate).
-// Signalling the weights in two parts (their product begins earlier) took 1457, the extra waits cost more.
+// Signalling the weights in two parts (their product begins earlier) took a fifth longer: the extra waits cost more.
 // Class 1, long streams: memory (24 single tokens at 3000 positions: a pair of 32 KB tiles per set every 6.9 k
 // cycles, 5.4 TB/s).  Class 1, streams of a tile or two: the roles' code, run in turns, exceeds the 32 KB
 // instruction cache (5200 misses per SM in 84 us at 256 tokens of 251 positions, no-instruction stalls ahead
