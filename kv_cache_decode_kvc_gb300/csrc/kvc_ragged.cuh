@@ -33,6 +33,9 @@
 
 namespace kvc {
 
+// Entries with more query rows per head than this are class 0.  (Class 1 holds 64 at most; as class 0, 24
+// sequences of 16 tokens x 4 heads at 3000 positions take 74.2 us against 68.5, 100 of them at 300 61.9
+// against 54.3: one set of two would work on a stream, and idle at its start.)
 constexpr int PAIR_ROWS = 64;
 
 struct RaggedParams {
@@ -516,7 +519,7 @@ struct Ragged {
     struct Walk {
         Stream st;
         int x, x1, own, cl;
-        bool cut;   // the last segment is the first piece of a stream that others share no rows with
+        bool cut;   // the last segment is a piece, not the last, of a stream that others share no rows with
         bool step;  // st is done: the next segment is in the stream after it
     };
     __device__ static Walk walk(const RaggedParams& p, const Split& sp, const Work& wk, int i, int w) {
@@ -536,18 +539,18 @@ struct Ragged {
         while (g.n == 0 && k.x < k.x1) {
             if (k.step && !next(p, k.st, k.cl)) break;
             g = segment(p, k.st, k.cl, k.own, k.x, k.x1);
-            k.cut = k.st.s.pfx == 0 && g.dst >= 0 && g.n > 0 && g.kv0 == 0;
+            k.cut = k.st.s.pfx == 0 && g.dst >= 0 && g.n > 0 && (g.kv0 == 0 || (g.kv0 >> LKT) + g.n < k.st.n);
             k.x = k.st.u0 + start_cost(k.cl) + k.st.n * tile_cost(k.cl);
             k.step = true;
         }
         return g;
     }
     // Leaves the cut stream that ends worker w's range (k.cut, g its last segment) for the merge:
-    // entry 3 i + w is (pieces, first owner, class, packed row), (rows of the tile, KV head).
+    // entry 3 i + w is (pieces, first owner, class, packed row), (rows of the tile, KV head, this piece).
     __device__ static void leave_cut(const RaggedParams& p, const Split& sp, const Walk& k, int i, int w, const Seg& g) {
-        const int last = owner_of(sp, k.st, k.cl, k.st.n - 1);
-        p.cuts[2 * (3 * i + w)] = make_int4(last - k.own + 1, k.own, k.cl, g.row0);
-        p.cuts[2 * (3 * i + w) + 1] = make_int4(g.ntok << p.lgG, g.h, 0, 0);
+        const int first = g.kv0 == 0 ? k.own : owner_of(sp, k.st, k.cl, 0), last = owner_of(sp, k.st, k.cl, k.st.n - 1);
+        p.cuts[2 * (3 * i + w)] = make_int4(last - first + 1, first, k.cl, g.row0);
+        p.cuts[2 * (3 * i + w) + 1] = make_int4(g.ntok << p.lgG, g.h, k.own - first, 0);
     }
 };
 

@@ -112,6 +112,26 @@ def test_blocks_past_32_bit_offsets(dtype, D, blocks):
             assert torch.equal(V[blk, :, t % 128].cpu(), bt.v[bt.cu[b] + i])
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("new", [[1], [3], [2, 1]])
+@pytest.mark.parametrize("ctas", [0, 19, 600])
+def test_few_long_sequences(dtype, D, new, ctas):
+    # one KV head, a stream or two cut into a piece for every worker: merges of up to hundreds of pieces, of 32
+    # to 96 rows
+    bt = Batch(new, [20011, 9000][:len(new)], 64, 32, 1, D, dtype, seed=29)
+    c, d = bt.cache(kvc), bt.dev()
+    c.set_ctas(ctas)
+    ref = attention64(bt)
+    out = torch.zeros(bt.rows, 32, D, dtype=bt.dtype, device="cuda")
+    _call(c, bt, d, out, False)
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    check_attention(out, bt, ref, dtype == "bf16")
+    out.zero_()
+    _call(c, bt, d, out, True)  # one group of all, no prefix: merged row by row
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    check_attention(out, bt, ref, dtype == "bf16")
+
+
 def test_graphs_with_scratch_of_their_own_run_at_once():
     bt = Batch([1] * 30 + [40], [200 + 17 * i for i in range(31)], 32, 8, 2, 128, "bf16", [0, 31], [192], seed=25)
     c, d = bt.cache(kvc), bt.dev()
