@@ -59,7 +59,7 @@ struct RtCfg {
     static constexpr int QSET = 128 * D * 2;         // a set's query bytes: 128 rows
     static constexpr int TILE = KT * D * 2;          // bytes of a K or V tile
     static constexpr int GSTR = 1024 * CB;           // 8-row group stride of a K / V tile
-    static constexpr int MISC = 3072;                // barriers, segments, exchanged maxima
+    static constexpr int MISC = 3 << 10;             // barriers, segments, exchanged maxima
     static constexpr int BUDGET = 232448;            // 227 KB
     static constexpr int NSLOT_A = (BUDGET - MISC - 2 * QSET) / TILE;
     static constexpr int NSLOT = NSLOT_A > 10 ? 10 : NSLOT_A;
