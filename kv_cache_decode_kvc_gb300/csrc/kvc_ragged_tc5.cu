@@ -17,12 +17,15 @@
 // division; weights in two bf16 parts would need a second product per tile.  The denominator sums the
 // unrounded weights in fp32.
 //
-// What bounds it.  Class 0: the chain of a set, S product (512 cycles at D = 128) - softmax (about 1600: 64
-// scores a thread, of which 540 are the exponentials of two warps on one sub-partition) - P product
-// (512), against 1024 cycles of the tensor core for the other set in the meantime; tensor memory holds S
-// and O of two sets and no more.  1216 tokens of 32 heads at 16,384 positions: tensor pipe 65 % busy; a chunk
-// of 4096 tokens of 64 heads behind 12,288 positions: 1284 us, 1.50 PFLOP/s (0.77 of cuBLAS's burst rate).
-// Signalling the weights in two parts (their product begins earlier) took a fifth longer: the extra waits cost more.
+// What bounds it.  Class 0: the chain of a set, from the S product's issue to its sight by the softmax 870
+// cycles (512 of the tensor core), softmax 1300 (64 scores a thread; arithmetic of two warps on one
+// sub-partition 594, of it exponentials 513), 430 to the P product's issue, 640 to the next S product's:
+// 3250 per key tile of both sets, in which the tensor core works 2048 and the products and copies move 256 KB
+// through shared memory.  Tensor memory holds S and O of two sets and no more.  1216 tokens of 32 heads at
+// 16,384 positions: tensor pipe 65 % busy; a chunk of 4096 tokens of 64 heads behind 12,288 positions:
+// 1290 us, 1.49 PFLOP/s (0.77 of cuBLAS's burst rate).  Weights signalled in two parts (their product begins
+// earlier) took a fifth longer; without the maximum's search past the first tile (the sum shows that the
+// reference holds), with products issued back to back or with other polling the period stayed as it is.
 // Class 1, long streams: memory (24 single tokens at 3000 positions: a pair of 32 KB tiles per set every 6.9 k
 // cycles, 5.4 TB/s).  Class 1, streams of a tile or two: the roles' code, run in turns, exceeds the 32 KB
 // instruction cache (5200 misses per SM in 84 us at 256 tokens of 251 positions, no-instruction stalls ahead
