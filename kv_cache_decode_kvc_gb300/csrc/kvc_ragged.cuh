@@ -167,11 +167,12 @@ struct Ragged {
     // its first piece 2-3 and then ends the range; set 0: 0 and 2, set 1: 3 and 4)
     static constexpr int SLOTS = PAIRS ? 5 : 2, SLOT_ROWS = PAIRS ? RT / 2 : RT;
 
-    // Cost units of a key tile and of a stream's start, by class.  (Measured with starts of 1, 2 and 4
-    // tiles in class 0: prompts 271, 246, 232 us; tiles of class 1 at 1/2, 1 and 3/2 of class 0's: the mixed
-    // batch 176, 133 and 168 us.)
+    // Cost units of a key tile and of a stream's start, by class.  (Measured with starts of 4, 6, 8 and 10 in
+    // class 0: six prompts of 700 to 4096 tokens 221, 220, 227, 234 us; of 2, 3, 4 in class 1: 256 single tokens
+    // with up to 500 positions behind 16,384 common ones 181, 153, 162 us, 200 with 350 behind as many 132,
+    // 139, 146; tiles of class 1 at 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
     __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
-    __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 8 : 4; }
+    __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 6 : 3; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at

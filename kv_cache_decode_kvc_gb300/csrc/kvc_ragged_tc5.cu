@@ -283,6 +283,10 @@ template <bool JOINT>
 __device__ __noinline__ void zero_rows(const RaggedParams& p, int tid, int n) {
     ragged_zero_rows<__nv_bfloat16, JOINT>(p, tid, n);
 }
+// sum += 0 x, two bf16 values each: stays 0 but for an infinite or NaN x.
+__device__ __forceinline__ void add_zero_times(uint32_t& sum, uint32_t x) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+}
 // Adds the non-finite V values of positions [a, b) to a row's stored columns [col, col + n): out (bf16,
 // already divided; the sum is the value or NaN either way) or a piece.
 __device__ __noinline__ void add_nonfinite(const RaggedParams& p, int seq, int h, int a, int b, int col, int n,
@@ -748,10 +752,24 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 const int end = min(g.kv_end - t0, C::KT), first = max(g.lim0 - t0, 0);
                 constexpr int W = C::CB * 8;  // 16-byte pieces of a row
                 uint32_t found = 0;
+                auto piece = [&](int r, int w) {
+                    return reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16);
+                };
+                // Are there any?  The sum of all values times 0 is NaN if so (a test of each value here took 6 k cycles
+                // for 64 rows, which the tile's product waits for).
+                uint32_t sum = 0;
 #pragma unroll 2
-                for (int c = first * W + lane; c < end * W; c += 32) {
-                    const int r = c / W, w = c % W;
-                    uint4* a = reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16);
+                for (int r = first + lane / W; r < end; r += 32 / W) {
+                    const uint4 d = *piece(r, lane % W);
+                    add_zero_times(sum, d.x);
+                    add_zero_times(sum, d.y);
+                    add_zero_times(sum, d.z);
+                    add_zero_times(sum, d.w);
+                }
+                const bool some = __any_sync(ALL, (sum & 0x7F807F80u) != 0);
+#pragma unroll 1
+                for (int r = first + lane / W; some && r < end; r += 32 / W) {
+                    uint4* a = piece(r, lane % W);
                     const uint4 d = *a;
                     // an all-ones exponent in either half of a word
                     auto bad = [](uint32_t u) {
@@ -766,9 +784,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 if (end < C::KT) {
                     const int g8 = (end + 7) & ~7;
                     for (int c = end * W + lane; c < g8 * W; c += 32) {
-                        const int r = c / W, w = c % W;
-                        *reinterpret_cast<uint4*>(tile + (r >> 3) * C::GSTR + (w >> 3) * 1024 + (r & 7) * 128 + (w & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                        *piece(c / W, c % W) = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll 4
                     for (int at = (g8 >> 3) * C::GSTR + lane * 16; at < C::TILE; at += 512)
