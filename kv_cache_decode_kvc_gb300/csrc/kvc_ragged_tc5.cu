@@ -23,9 +23,11 @@
 // 3250 per key tile of both sets, in which the tensor core works 2048 and the products and copies move 256 KB
 // through shared memory.  Tensor memory holds S and O of two sets and no more.  1216 tokens of 32 heads at
 // 16,384 positions: tensor pipe 65 % busy; a chunk of 4096 tokens of 64 heads behind 12,288 positions:
-// 1290 us, 1.49 PFLOP/s (0.77 of cuBLAS's burst rate).  Weights signalled in two parts (their product begins
+// 1276 us, 1.51 PFLOP/s (0.78 of cuBLAS's burst rate).  Weights signalled in two parts (their product begins
 // earlier) took a fifth longer; without the maximum's search past the first tile (the sum shows that the
 // reference holds), with products issued back to back or with other polling the period stayed as it is.
+// A change of streams costs about 9 k cycles from the last weights to the next scores: the output's way
+// out, the segments' hand-over and the first products are code that has left the instruction cache.
 // Class 1, long streams: memory (24 single tokens at 3000 positions: a pair of 32 KB tiles per set every 6.9 k
 // cycles, 5.4 TB/s).  Class 1, streams of a tile or two: the roles' code, run in turns, exceeds the 32 KB
 // instruction cache (5200 misses per SM in 84 us at 256 tokens of 251 positions, no-instruction stalls ahead
