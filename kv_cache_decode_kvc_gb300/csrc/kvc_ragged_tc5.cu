@@ -693,6 +693,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 return true;
             },
             [&](Lane<Seg>& l) {  // class 0: V of tile j, K of tile j + 1, set by set
+                // (written out for each set: with the set as a loop's variable a chunk of 4096 tokens takes a
+                // quarter longer)
                 const Seg& g = l.g;
                 const int sets = (g.ntok << p.lgG) > 128 ? 2 : 1, n = g.n;
                 const uint32_t qb = (uint32_t)dQ;
@@ -706,12 +708,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 if (!__all_sync(ALL, wait_on(&M.qpair, npair++ & 1) && wait_item(item))) return false;
                 issued = 1;
                 const uint32_t k0 = k_desc(item);
-#pragma unroll 1
-                for (int q = 0; q < sets; ++q) {
-                    const bool last = q + 1 == sets;
-                    score(uni(q), qb + ((uni(q) * C::QSET) >> 4), k0, last ? &M.empty[item % C::NSLOT] : nullptr,
-                          last && n == 1 ? &M.qfree : nullptr);
-                }
+                score(0, qb, k0, sets == 1 ? &M.empty[item % C::NSLOT] : nullptr, sets == 1 && n == 1 ? &M.qfree : nullptr);
+                if (sets == 2) score(1, qb + (C::QSET >> 4), k0, &M.empty[item % C::NSLOT], n == 1 ? &M.qfree : nullptr);
                 ++item;
 #pragma unroll 1
                 for (int j = 0; j + 1 < n; ++j) {
@@ -731,10 +729,11 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 }
                 if (!__all_sync(ALL, wait_v(g, n - 1))) return false;
                 const uint32_t vb = v_desc(item), acc = uni(n > 1 ? 1u : 0u);
-#pragma unroll 1
-                for (int q = 0; q < sets; ++q) {
-                    if (!ready(q)) return false;
-                    apply(uni(q), vb, acc, &M.ofull[q], q + 1 == sets ? &M.empty[item % C::NSLOT] : nullptr);
+                if (!ready(0)) return false;
+                apply(0, vb, acc, &M.ofull[0], sets == 1 ? &M.empty[item % C::NSLOT] : nullptr);
+                if (sets == 2) {
+                    if (!ready(1)) return false;
+                    apply(1, vb, acc, &M.ofull[1], &M.empty[item % C::NSLOT]);
                 }
                 ++item;
                 return true;
