@@ -211,3 +211,37 @@ def test_an_empty_batch_writes_nothing(shared):
     assert c.last_error() == (kvc.KVC_OK, 0)
     assert (out == 7.0).all()
     assert all(torch.equal(a, b) for a, b in zip(before, c.layer_views(0)))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("bf16", 256), ("f32", 64)])
+def test_tensors_aligned_to_16_bytes_only(dtype, D):
+    # base pointers 16 bytes past a multiple of 32 and row strides of an odd number of 16-byte pieces
+    bt = Batch([3, 70, 1, 2], [100, 30, 400, 64], 16, 4, 2, D, dtype, [0, 2, 4], [16, 64], pad=2, seed=30)
+    c, d = bt.cache(kvc), bt.dev()
+    piece = 16 // bt.K.element_size()
+
+    def odd(x=None, heads=4):
+        row = heads * D + piece
+        buf = torch.full((bt.rows * row + piece,), 7.0, dtype=bt.dtype, device="cuda")
+        v = buf[piece:].view(bt.rows, row)[:, :heads * D].unflatten(1, (heads, D))
+        assert v.data_ptr() % 32 == 16
+        if x is not None:
+            v.copy_(x)
+        return v, buf
+
+    ref = attention64(bt)
+    for shared in (False, True):
+        q, out, buf = odd(d["q"])[0], *odd()
+        _call(c, bt, dict(d, q=q), out, shared)
+        assert c.last_error() == (kvc.KVC_OK, 0)
+        check_attention(out, bt, ref, dtype == "bf16" and D < 256)
+        out.fill_(7.0)
+        assert (buf == 7.0).all()  # nothing between the rows is written
+    q, k, v = odd(d["q"])[0], odd(d["k"], 2)[0], odd(d["v"], 2)[0]
+    rope = kvc.Rope([1.0, 0.25] * (D // 4))
+    c.append_rope(0, rope, q, k, v, d["table"], d["cu"], d["lens"])
+    got = [x.clone() for x in c.layer_views(0)]
+    c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"])
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    assert torch.equal(q[:bt.n], d["q"][:bt.n])
+    assert all(torch.equal(a, b) for a, b in zip(got, c.layer_views(0)))
