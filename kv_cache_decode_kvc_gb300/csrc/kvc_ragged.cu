@@ -99,8 +99,10 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
         for (int i = tid; i < n; i += C::THREADS) p.plan[i] = sp.valid ? work.c[i] : 0;
         if (!sp.valid && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
     }
-    if (tid < 6) p.cuts[6 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
     if (tid >= C::NT) {  // the segments, one ahead of the threads that attend them
+        // The block's cuts start out empty.  The warp that leaves them (leave_cut) empties them: from another
+        // warp nothing would order the two writes, and a cut that is lost is a stream that is never merged.
+        if (tid - C::NT < 6) p.cuts[6 * blockIdx.x + tid - C::NT] = make_int4(0, 0, 0, 0);
         __syncwarp();
         typename R::Walk wk;
         if (tid == C::NT) wk = R::walk(p, sp, work, blockIdx.x, 1);
