@@ -258,7 +258,10 @@ struct Ragged {
             k.groups[g] = b0;
             if (g < p.NG) k.prefix[g] = __ldg(p.prefix + g);
         }
-        if (JOINT) bad = __any_sync(0xFFFFFFFFu, bad);
+        if (JOINT) {
+            bad = __any_sync(0xFFFFFFFFu, bad);
+            __syncwarp();  // the copies are read by other lanes below, and a vote orders no memory
+        }
         for (int e0 = 0; e0 < NE && !bad; e0 += 32) {
             const int e = e0 + lane;
             Entry s;

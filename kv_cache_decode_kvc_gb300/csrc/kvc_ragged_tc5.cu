@@ -437,6 +437,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     // ... by a whole warp that keeps its own copy and needs the place no longer.
     auto take_seg = [&](Lane<Seg>& l) {
         const bool ok = __all_sync(ALL, fetch_seg(l.q, l.s, l.g)) != 0;
+        __syncwarp();  // (a vote orders no memory: all lanes have read it)
         if (ok && lane == 0) mbar_arrive(&M.segempty[l.q][l.s & 1]);
         return ok;
     };
@@ -519,6 +520,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 if (ok) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)((nbox << lgr) * D * 2));
             }
             if (!__all_sync(ALL, ok)) return false;
+            __syncwarp();  // lane 0 has seen the slot empty
             ++issued;
             if (lane < nbox) {
                 if ((unsigned)e >= (unsigned)p.num_blocks) {
@@ -806,6 +808,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         replay<Seg>(
             [&](Lane<Seg>& l) {
                 const bool ok = __all_sync(ALL, fetch_seg(l.q, l.s, l.g)) != 0;
+                __syncwarp();
                 if (ok && lane == 0) {
                     M.nonfinite[l.q][l.s & 1] = 0;
                     mbar_arrive(&M.segempty[l.q][l.s & 1]);

@@ -34,3 +34,27 @@ def test_every_cut_stream_is_merged(dtype, D, math, ctas):
     check_attention(outs[0], bt, attention64(bt), dtype == "bf16" and D < 256 and math == 0)
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("groups", [33, 100, 341])
+def test_many_groups_call_after_call(dtype, D, groups):
+    # more groups than a warp has lanes, of three sequences or an odd one: their bounds and prefixes are read by
+    # other threads than those that fetched them, in every worker
+    B = 3 * groups
+    start = [3 * g - g % 2 for g in range(groups)] + [B]
+    prefix = [16 * (1 + g % 4) for g in range(groups)]
+    hist = [0] * B
+    for g, (a, b) in enumerate(zip(start, start[1:])):
+        for s in range(a, b):
+            hist[s] = prefix[g] + (5 * s) % 23
+    bt = Batch([s % 3 for s in range(B)], hist, 16, 2, 1, D, dtype, start, prefix, seed=32)
+    c, d = bt.cache(kvc), bt.dev()
+    ws = torch.full((c.attn_workspace_bytes(bt.rows, groups),), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.full((bt.rows, 2, D), float("nan"), dtype=bt.dtype, device="cuda") for _ in range(100)]
+    for o in outs:
+        c.attn_shared(0, d["q"], o, d["table"], d["cu"], d["lens"], d["groups"], d["prefix"], workspace=ws)
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    check_attention(outs[0], bt, attention64(bt), dtype == "bf16")
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
