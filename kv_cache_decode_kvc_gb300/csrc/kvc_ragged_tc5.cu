@@ -426,7 +426,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     const uint32_t tmem = warp != 2 ? M.tmem : 0;
     uint32_t issued = 0;  // copies / products begun (copy and product threads)
     if (warp != 2) named_bar_arrive(9, C::THREADS);
-    if (warp < 4) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Before any wait: a kernel that releases its dependents early may run for longer than a wait's limit.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // A role's segment s of set q, as soon as it is known (the caller releases the place).
     auto fetch_seg = [&](int q, int s, Seg& g) {
@@ -851,7 +852,6 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         for (int s = 0;; ++s) {
             Seg g;
             if (!pair_all(bar, fetch_dozing(set, s, g))) break;
-            if (s == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             if (s == 0 && M.valid) zero_rows<JOINT>(p, tid - 128, C::THREADS - 128);
             if (g.n == 0) break;
             const int nrow = g.ntok << p.lgG;
