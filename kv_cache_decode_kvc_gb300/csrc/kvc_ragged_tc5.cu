@@ -464,7 +464,9 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         bool done = lane > 2, have = false;
         Seg g;
         g.n = 0;
-        uint64_t t0 = global_ns();
+        // When this lane first found its segment's place taken, 0: not yet.  (Counted from then on only: lanes 1 and 2
+        // look for the first time when class 0 is over, which may take longer than a wait's limit.)
+        uint64_t t0 = 0;
         while (__any_sync(ALL, !done)) {
             const bool pairs = (__ballot_sync(ALL, !done) & 1) != 0;
             const int s0 = __shfl_sync(ALL, s, 0);
@@ -490,12 +492,16 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 done = g.n == 0;
                 have = false;
                 ++s;
-                t0 = global_ns();
+                t0 = 0;
             } else if (*ab) {
                 done = true;
-            } else if (global_ns() - t0 > WAIT_LIMIT_NS) {
-                *ab = 1;
-                atomicOr(p.err, DEV_WAIT_TIMEOUT);
+            } else {
+                const uint64_t now = global_ns();
+                if (t0 == 0) t0 = now;
+                if (now - t0 > WAIT_LIMIT_NS) {
+                    *ab = 1;
+                    atomicOr(p.err, DEV_WAIT_TIMEOUT);
+                }
             }
         }
     } else if (warp == 0) {

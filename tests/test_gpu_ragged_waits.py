@@ -64,3 +64,45 @@ def test_behind_a_kernel_that_releases_its_dependents_and_runs_on(linger, D, sha
         c.attn_ragged(0, d["q"], out, d["table"], d["cu"], d["lens"], workspace=ws)
     assert c.last_error() == (kvc.KVC_OK, 0)
     check_attention(out, bt, attention64(bt), True)
+
+
+def test_single_tokens_behind_seconds_of_prompts():
+    # one worker takes in a prompt of 131,072 tokens (more than 2 s, a wait's limit), then single tokens of two
+    # other sequences: their hand-over begins when the prompt is done
+    T, H, D, bs, long = 131072, 8, 128, 256, 700
+    new, hist = [T, 1, 1], [0, long, 130]
+    lens = [n + h for n, h in zip(new, hist)]
+    blocks = [-(-L // bs) for L in lens]
+    c = kvc.PagedKVCache(1, sum(blocks), bs, 3, blocks[0], H, H, D)
+    K, V = c.layer_views(0)
+    g = torch.Generator("cuda").manual_seed(41)
+    for x in (K, V):
+        x.copy_(torch.randn(x.shape, dtype=x.dtype, device="cuda", generator=g))
+    table = torch.zeros(3, blocks[0], dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, ln = torch.tensor([0, T, T + 1, T + 2], **i32), torch.tensor(lens, **i32)
+    q = torch.randn(T + 2, H, D, dtype=torch.bfloat16, device="cuda", generator=g)
+    out = torch.full_like(q, float("nan"))
+    ws = torch.empty(c.attn_workspace_bytes(T + 2), dtype=torch.uint8, device="cuda")
+    c.set_ctas(1)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    c.attn_ragged(0, q, out, table, cu, ln, workspace=ws)
+    ev[1].record()
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    assert ev[0].elapsed_time(ev[1]) > 2100  # else the sizes no longer make the case
+    assert out.isfinite().all()
+    for row, b, n in [(0, 0, 1), (1, 0, 2), (300, 0, 301), (T // 2, 0, T // 2 + 1), (T - 1, 0, T), (T, 1, long + 1),
+                      (T + 1, 2, 131)]:
+        t = torch.arange(n, device="cuda")
+        at = table[b, t // bs].long(), t % bs
+        for h in (0, 7):
+            Kb, Vb = (x[at[0], h, at[1]].cpu().double() for x in (K, V))
+            p = torch.softmax(Kb @ q[row, h].cpu().double() / D ** 0.5, 0)
+            want, A, got = p @ Vb, p @ Vb.abs(), out[row, h].cpu().double()
+            # the weights' and the output's rounding to bf16, and as much again of the first for the fp32 sums
+            assert ((got - want).abs() <= 2.0 ** -7 * A + 2.0 ** -8 * want.abs()).all(), (row, h)
