@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
             const int t0 = g.kv0 + j * C::KT;
             for (int i = tid; i < C::KT * VPR; i += C::NT) {
                 const int t = i / VPR, v = (i - t * VPR) * VEC;
-                const bool there = t0 + t < g.kv_end;
+                const bool there = t < g.kv_end - t0;  // (t0 + t may pass 2^31)
                 int64_t row = 0;
                 if (there)
                     row = cache_row_rd(p.table, p.bs, p.max_blocks, p.num_blocks, p.H_kv, p.T_max, g.seq, g.h, t0 + t, p.err);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
         for (int i = 0; i < 4; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
-            lim[i] = min(g.kv_end, g.lim0 + g.causal * ((ty * 4 + i) >> p.lgG));
+            lim[i] = g.sees((ty * 4 + i) >> p.lgG);
 #pragma unroll
             for (int v = 0; v < C::NV; ++v) acc[i][v].lo.f = acc[i][v].hi.f = make_float2(0.f, 0.f);
         }
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
                 float mx = -INFINITY, x[C::NC];
 #pragma unroll
                 for (int c = 0; c < C::NC; ++c) {
-                    x[c] = t0 + tx + C::TX * c < lim[i] ? (s[i][c].f.x + s[i][c].f.y) * p.qscale : -INFINITY;
+                    x[c] = tx + C::TX * c < lim[i] - t0 ? (s[i][c].f.x + s[i][c].f.y) * p.qscale : -INFINITY;
                     mx = fmaxf(mx, x[c]);
                 }
 #pragma unroll
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
                             const Four x = load4(vs + (t + tt) * D + (v * C::TX + tx) * 4);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                if (decltype(guard)::value && t0 + t + tt >= lim[i]) continue;
+                                if (decltype(guard)::value && t + tt >= lim[i] - t0) continue;
                                 Two f;
                                 f.f.x = f.f.y = tt == 0 ? w[i].x : tt == 1 ? w[i].y : tt == 2 ? w[i].z : w[i].w;
                                 fma_two(acc[i][v].lo, f, x.lo);

@@ -149,11 +149,12 @@ __device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
     return group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), prefix_used(p, b0, b1, P));
 }
 
-// sum of ceil(x / 2^lg) for x = 1 .. X
-__device__ __forceinline__ int triangle(int n) { return ((n + 1) >> 1) * (n | 1); }  // 1 + .. + n
-__device__ __forceinline__ int ceil_sum(int X, int lg) {
-    const int n = X >> lg;
-    return (triangle(n) << lg) + (X & ((1 << lg) - 1)) * (n + 1);
+// sum of ceil(x / 2^lg) for x = 1 .. X, modulo 2^32 (of far positions only differences fit: unsigned
+// sums wrap, signed ones may not)
+__host__ __device__ __forceinline__ unsigned triangle(unsigned n) { return ((n + 1) >> 1) * (n | 1); }  // 1 + .. + n
+__host__ __device__ __forceinline__ unsigned ceil_sum(unsigned X, int lg) {
+    const unsigned n = X >> lg;
+    return (triangle(n) << lg) + (X & ((1u << lg) - 1)) * (n + 1);
 }
 
 // Work split.  LRT, LKT: log2 of a stream's rows and of a key tile; PAIRS: classes as the
@@ -171,8 +172,8 @@ struct Ragged {
     // class 0: six prompts of 700 to 4096 tokens 221, 220, 227, 234 us; of 2, 3, 4 in class 1: 256 single tokens
     // with up to 500 positions behind 16,384 common ones 181, 153, 162 us, 200 with 350 behind as many 132,
     // 139, 146; tiles of class 1 at 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
-    __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
-    __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 6 : 3; }
+    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
+    __host__ __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 6 : 3; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at
@@ -183,28 +184,28 @@ struct Ragged {
         if (JOINT && e < p.NG) return group_entry(p, e);
         return seq_entry<JOINT>(p, e - groups(p));
     }
-    __device__ static int cls(const RaggedParams& p, const Entry& s) {
+    __host__ __device__ static int cls(const RaggedParams& p, const Entry& s) {
         return PAIRS && ((int64_t)s.T << p.lgG) > PAIR_ROWS ? 0 : 1;
     }
     // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
-    __device__ static int tiles(int S0, int t1) { return (int)(((unsigned)S0 + (unsigned)t1 + KT - 1) >> LKT); }
+    __host__ __device__ static int tiles(int S0, int t1) { return (int)(((unsigned)S0 + (unsigned)t1 + KT - 1) >> LKT); }
     // Costs are 32-bit (a call of 2^31 units, hours of work, is refused: scan).  Key tiles of an entry's first
     // k streams, all full (TQ = 2^lq tokens each): sum over i = 1 .. k of ceil((S0 + i TQ) / KT).
-    __device__ static int tiles_full(int S0, int k, int lq) {
-        if (lq >= LKT) return k * (int)((unsigned)(S0 + KT - 1) >> LKT) + (triangle(k) << (lq - LKT));
+    __host__ __device__ static int tiles_full(int S0, int k, int lq) {
+        if (lq >= LKT) return (int)((unsigned)k * (((unsigned)S0 + KT - 1) >> LKT) + (triangle(k) << (lq - LKT)));
         // ceil((S0 + i TQ) / KT) = ceil((ceil(S0 / TQ) + i) / (KT / TQ))
-        const int s = (int)((unsigned)(S0 + (1 << lq) - 1) >> lq);
-        return ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq);
+        const unsigned s = ((unsigned)S0 + (1u << lq) - 1) >> lq;
+        return (int)(ceil_sum(s + k, LKT - lq) - ceil_sum(s, LKT - lq));
     }
-    __device__ static int cost(const RaggedParams& p, const Entry& s, int cl) {
+    __host__ __device__ static int cost(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0;
         const int lq = LRT - p.lgG, nk = (int)((unsigned)(s.T + (1 << lq) - 1) >> lq), S0 = s.L - s.T - s.pfx;
-        const int n = JOINT && s.group ? nk * ((s.pfx + KT - 1) >> LKT) : tiles_full(S0, nk - 1, lq) + tiles(S0, s.T);
+        const int n = JOINT && s.group ? nk * tiles(s.pfx, 0) : tiles_full(S0, nk - 1, lq) + tiles(S0, s.T);
         return n * tile_cost(cl) + nk * start_cost(cl);
     }
     // The same to a few parts in a million, without wrapping.
-    __device__ static float cost_about(const RaggedParams& p, const Entry& s, int cl) {
+    __host__ __device__ static float cost_about(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0.f;
         const float nk = (float)s.T / (float)(RT >> p.lgG) + 1.f, own = (float)(JOINT && s.group ? s.pfx : s.L - s.pfx);
         return nk * ((own / KT + 1.f) * tile_cost(cl) + start_cost(cl));
@@ -381,7 +382,7 @@ struct Ragged {
     __device__ static void fill(const RaggedParams& p, Stream& st) {
         const int lq = LRT - p.lgG;
         if (JOINT && st.s.group) {
-            st.n = (st.s.pfx + KT - 1) >> LKT;
+            st.n = tiles(st.s.pfx, 0);
         } else {
             const int64_t t1 = (int64_t)(st.k + 1) << lq;
             st.n = tiles(st.s.L - st.s.T - st.s.pfx, t1 < st.s.T ? (int)t1 : st.s.T);
@@ -415,7 +416,7 @@ struct Ragged {
         r -= st.h * per;
         st.u0 = base + c[lo] * p.H_kv + st.h * per;
         if (JOINT && st.s.group) {
-            const int one = ((st.s.pfx + KT - 1) >> LKT) * tc + sc;
+            const int one = tiles(st.s.pfx, 0) * tc + sc;
             st.k = (int)((unsigned)r / (unsigned)one);
             st.u0 += st.k * one;
         } else {
@@ -448,7 +449,7 @@ struct Ragged {
         const int cl = cls(p, st.s);
         c += cl * (NE + 1);
         st.u0 = (cl == 0 ? 0 : sp.W0) + c[e] * p.H_kv + h * (c[e + 1] - c[e]);
-        const int n = JOINT && st.s.group ? st.k * ((st.s.pfx + KT - 1) >> LKT)
+        const int n = JOINT && st.s.group ? st.k * tiles(st.s.pfx, 0)
                                           : tiles_full(st.s.L - st.s.T - st.s.pfx, st.k, lq);
         st.u0 += n * tile_cost(cl) + st.k * start_cost(cl);
         fill(p, st);
@@ -483,7 +484,9 @@ struct Ragged {
         int row0, ntok;  // packed rows of the tile
         int kv0;         // position of its first key tile
         int kv_end;      // positions [kv0, kv_end) exist for the stream
-        int lim0, causal;  // row of token i sees positions below min(kv_end, lim0 + i * causal)
+        int lim0;        // row of token i sees positions below sees(i); all see those below lim0
+        // (no sum here passes kv_end, which may be close to 2^31)
+        __device__ int sees(int i) const { return lim0 + min(i, kv_end - lim0); }
         int dst;         // -1 out, -2 / -3 row buffer 0 / 1, else the slot
         int cl;          // class
     };
@@ -506,12 +509,10 @@ struct Ragged {
         if (JOINT && st.s.group) {
             g.kv_end = st.s.pfx;
             g.lim0 = st.s.pfx;
-            g.causal = 0;
         } else {
             const int S = st.s.L - st.s.T + (st.k << lq);  // position of the tile's first token
             g.kv_end = S + g.ntok;
             g.lim0 = S + 1;
-            g.causal = 1;
         }
         if (j0 > 0) g.dst = slot(cl, own, true);
         else if (JOINT && st.s.pfx > 0) g.dst = st.s.group ? -2 : -3;  // rows shared with another stream

@@ -515,8 +515,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         uint32_t slot = 0, filled = 0;    // the next item's slot; parity of the slots' uses
         int npair = 0, sc0 = 0, sc1 = 0;  // segments begun: of class 0, of class 1 by set
         auto entry = [&](const Seg& g, int j) {  // this lane's block of key tile j
-            const int t = g.kv0 + j * C::KT + bt;
-            return bt < C::KT && t < g.kv_end ? __ldg(p.table + (size_t)g.seq * p.max_blocks + (t >> p.lgbs)) : 0;
+            const unsigned t = (unsigned)g.kv0 + j * C::KT + bt;  // (of the last tiles it may pass 2^31)
+            return bt < C::KT && t < (unsigned)g.kv_end ? __ldg(p.table + (size_t)g.seq * p.max_blocks + (t >> p.lgbs)) : 0;
         };
         // K (isv false) or V of key tile j, whose block this CUDA lane knows
         auto copy = [&](const Seg& g, int j, int e, bool isv) {
@@ -637,7 +637,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         // a V tile that some row does not see all of has passed warp 3
         auto wait_v = [&](const Seg& g, int j) {
             bool ok = wait_item(item);
-            if (ok && g.kv0 + (j + 1) * C::KT > g.lim0) {
+            if (ok && g.lim0 - (g.kv0 + j * C::KT) < C::KT) {
                 const uint32_t sl = item % C::NSLOT;
                 ok = wait_on(&M.vfix[sl], (fix >> sl) & 1);
                 fix ^= 1u << sl;
@@ -757,7 +757,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             const uint32_t slot = item % C::NSLOT;
             if (!__all_sync(ALL, wait_on(&M.full[slot], (item / C::NSLOT) & 1))) return false;
             const int t0 = g.kv0 + j * C::KT;
-            if (j >= 0 && t0 + C::KT > g.lim0) {
+            if (j >= 0 && g.lim0 - t0 < C::KT) {
                 char* tile = ring + slot * C::TILE;
                 const int end = min(g.kv_end - t0, C::KT), first = max(g.lim0 - t0, 0);
                 constexpr int W = C::CB * 8;  // 16-byte pieces of a row
@@ -871,15 +871,14 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 // the protocol.
                 const int quads = (min(nrow - max(r0, 0), 128) + 31) >> 5;
                 const uint32_t count = quads == 1 ? 4 : quads == 2 ? 2 : 1;
-                const int limit = min(g.kv_end, g.lim0 + g.causal * (r >> p.lgG));
-                const int limit_w = min(g.kv_end, g.lim0 + g.causal * (rw >> p.lgG));
+                const int limit = g.sees(r >> p.lgG), limit_w = g.sees(rw >> p.lgG);
                 float m = -INFINITY, l = 0.f;  // reference maximum of the raw scores, sum of this half's weights
-                // Tile j's scores are in: waits, and gives the columns this warp's rows see of its half.
+                // Tile j's scores are in: waits, and gives its first position.
                 auto begin = [&](int j) {
                     ok = wait_on(&M.sfull[set], ns++ & 1, 20) && ok;
                     __syncwarp();
                     tc5_fence_after();
-                    return g.kv0 + j * C::KT + half * 64;
+                    return g.kv0 + j * C::KT;
                 };
                 // The row's maximum so far from this half's `top`; the reference is raised, and O with it, only if
                 // it grew by more than 2^8 (weights against a lower one keep their relative precision).
@@ -934,8 +933,8 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         const int t0 = begin(j);
                         float v[64];
                         tc5_ld64(tS + half * 64, v);
-                        if (t0 + 64 > limit_w) {
-                            const int see = limit - t0;
+                        if (limit_w - t0 < half * 64 + 64) {
+                            const int see = limit - t0 - half * 64;
 #pragma unroll
                             for (int i = 0; i < 64; ++i) v[i] = i < see ? v[i] : -INFINITY;
                         }
@@ -965,7 +964,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     // Few rows: the loop is kept short instead, 16 columns at a time, loaded again for the weights (all
                     // roles' code runs in turns here and has to fit the instruction cache).
                     for (int j = 0; j < g.n; ++j) {
-                        const int see = limit - begin(j);
+                        const int see = limit - begin(j) - half * 64;
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int d = 0; d < 64; d += 16) {
@@ -1040,10 +1039,12 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             }
                         }
                     }
-                    if (nonfin && r < nrow && ok)
+                    if (nonfin && r < nrow && ok) {
                         // the values warp 3 took out of tiles this row sees part of
-                        add_nonfinite(p, g.seq, g.h, max(g.lim0, g.kv0), min(limit, g.kv0 + g.n * C::KT), half * C::HD, C::HD, out,
+                        const int end = g.n > (limit - g.kv0) / C::KT ? limit : g.kv0 + g.n * C::KT;
+                        add_nonfinite(p, g.seq, g.h, max(g.lim0, g.kv0), end, half * C::HD, C::HD, out,
                                       g.dst == -1 ? nullptr : po);
+                    }
                     tc5_fence_before();
                 }
             }

@@ -1,0 +1,72 @@
+"""The cost sums that split ragged batches over the workers, compiled for the host and compared with exact sums:
+a wrong sum would put a stream's start, and with it every lookup of its keys, in the wrong place."""
+import ctypes
+import random
+import subprocess
+
+import pytest
+
+from kv_cache_decode_kvc_gb300 import build
+
+SOURCE = r"""
+#include "kvc_ragged.cuh"
+using namespace kvc;
+static Entry entry(int T, int L, int pfx, int group) {
+    Entry s;
+    s.row0 = 0; s.T = T; s.L = L; s.pfx = pfx; s.seq = 0; s.group = group != 0; s.ok = true; s.bad = false;
+    return s;
+}
+template <class R> static int units(int lgG, int T, int L, int pfx, int group) {
+    RaggedParams p{};
+    p.lgG = lgG;
+    const Entry s = entry(T, L, pfx, group);
+    return R::cost(p, s, R::cls(p, s));
+}
+extern "C" int ragged_units(int kind, int lgG, int T, int L, int pfx, int group) {
+    return kind == 0   ? units<Ragged<8, 7, true, true>>(lgG, T, L, pfx, group)
+           : kind == 1 ? units<Ragged<6, 6, false, true>>(lgG, T, L, pfx, group)
+                       : units<Ragged<6, 5, false, true>>(lgG, T, L, pfx, group);
+}
+"""
+KINDS = [(8, 7, True), (6, 6, False), (6, 5, False)]  # log2 of a tile's rows and keys; classes
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    at = tmp_path_factory.mktemp("split")
+    (at / "split.cu").write_text(SOURCE)
+    subprocess.run(["nvcc", *build.ARCH, *build.FLAGS, "-I", build.CSRC, "-shared", "-cudart", "static", "-o",
+                    str(at / "split.so"), str(at / "split.cu")], check=True, capture_output=True)
+    return ctypes.CDLL(str(at / "split.so"))
+
+
+def _exact(kind, lgG, T, L, pfx, group):
+    """Units of one KV head of an entry: its streams one by one."""
+    lrt, lkt, pairs = KINDS[kind]
+    tile = 2 if pairs else 1
+    start = 1 if not pairs else 6 if T << lgG > 64 else 3
+    TQ, n, streams = 1 << (lrt - lgG), 0, -(-T // (1 << (lrt - lgG)))
+    for k in range(streams):
+        last = pfx if group else L - T - pfx + min((k + 1) * TQ, T)
+        n += (last + (1 << lkt) - 1) >> lkt
+    return n * tile + streams * start
+
+
+@pytest.mark.parametrize("kind", range(3))
+def test_units_of_entries_near_and_far(lib, kind):
+    rng = random.Random(kind)
+    top = 2 ** 31 - 16  # the most positions a paged cache holds
+    cases = [(5, 1, top, 0, 0), (0, 1, top, 0, 0), (0, 1000, top, 0, 0), (0, 7, top, top, 1), (2, 900, top, top - 1000, 0),
+             (5, 3, 2 ** 30, 0, 0), (0, 1, 1, 0, 0), (3, 4096, 4096, 0, 0)]
+    for _ in range(600):
+        T = rng.choice([1, 2, rng.randint(1, 70), rng.randint(1, 3000)])
+        L = min(top, T + int(2 ** rng.uniform(0, 31)))
+        pfx = rng.choice([0, rng.randint(0, (L - T) // 16) * 16])
+        cases.append((rng.randint(0, 5), T, L, pfx, int(rng.random() < 0.2 and pfx > 0)))
+    tried = 0
+    for c in cases:
+        want = _exact(kind, *c)
+        if want < 2 ** 31:
+            tried += 1
+            assert lib.ragged_units(kind, *c) == want, c
+    assert tried > 400
