@@ -59,6 +59,7 @@ typedef struct kvc_cache* kvc_t;
 #define KVC_DEV_WAIT_TIMEOUT 2u /* an in-kernel wait gave up (internal error; output invalid) */
 #define KVC_DEV_BAD_BLOCK 4u    /* a paged call met a block-table entry outside [0, num_blocks) */
 #define KVC_DEV_BAD_SEQ 8u      /* cu_seqlens or groups do not ascend from 0 within their bounds */
+#define KVC_DEV_TOO_LARGE 16u   /* more attention work than one ragged call takes; nothing written */
 
 /* Create a cache of `layers` layers, each holding K and V of shape [B, H_kv, T_max, D].
  * Supported: dtype KVC_BF16 with D in {64, 128, 256}; KVC_F32 with D in {4, 64, 128, 256};
@@ -320,7 +321,11 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
  * 64 or 128 run on the tcgen05 tensor cores (softmax weights enter the second product as bf16),
  * every other shape, or math mode 1, on CUDA cores in fp32.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
- * once the call has completed on its stream; calls that may run at the same time need one each. */
+ * once the call has completed on its stream; calls that may run at the same time need one each.
+ * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on
+ * CUDA cores) by 128 positions (CUDA cores: 64 for D <= 64, else 32) that its last row sees.  A
+ * call of more than 10^9 tiles (2 10^9 on CUDA cores; some 12 and 30 s of work) may be refused:
+ * KVC_DEV_TOO_LARGE is set and nothing is written; give it fewer sequences or shorter chunks. */
 int kvc_paged_attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,
                           int64_t out_stride, const int32_t* block_table, const int32_t* cu_seqlens,
                           const int32_t* lens, int N, void* ws, uint64_t ws_bytes, void* stream);

@@ -17,6 +17,7 @@ constexpr uint32_t DEV_BAD_LENS = 1u;      // mirrors KVC_DEV_BAD_LENS
 constexpr uint32_t DEV_WAIT_TIMEOUT = 2u;  // mirrors KVC_DEV_WAIT_TIMEOUT
 constexpr uint32_t DEV_BAD_BLOCK = 4u;     // mirrors KVC_DEV_BAD_BLOCK
 constexpr uint32_t DEV_BAD_SEQ = 8u;       // mirrors KVC_DEV_BAD_SEQ
+constexpr uint32_t DEV_TOO_LARGE = 16u;    // mirrors KVC_DEV_TOO_LARGE
 constexpr int MAX_B = 1024;
 // An in-kernel wait that has not completed after this long gives up, flags
 // DEV_WAIT_TIMEOUT and lets the kernel run to its end (no hang, output marked invalid).

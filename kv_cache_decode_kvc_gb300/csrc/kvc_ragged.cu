@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
     if (blockIdx.x == 0) {
         const int n = 2 * (R::groups(p) + p.B + 1);
         for (int i = tid; i < n; i += C::THREADS) p.plan[i] = sp.valid ? work.c[i] : 0;
-        if (!sp.valid && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
+        if (!sp.valid && tid == 0) atomicOr(p.err, sp.why);
     }
     if (tid >= C::NT) {  // the segments, one ahead of the threads that attend them
         // The block's cuts start out empty.  The warp that leaves them (leave_cut) empties them: from another

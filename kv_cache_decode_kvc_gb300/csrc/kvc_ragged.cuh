@@ -190,7 +190,7 @@ struct Ragged {
     // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
     __host__ __device__ static int tiles(int S0, int t1) { return (int)(((unsigned)S0 + (unsigned)t1 + KT - 1) >> LKT); }
-    // Costs are 32-bit (a call of 2^31 units, hours of work, is refused: scan).  Key tiles of an entry's first
+    // Costs are 32-bit (a call of more than MOST units, some 12 s of work, is refused: scan).  Key tiles of an entry's first
     // k streams, all full (TQ = 2^lq tokens each): sum over i = 1 .. k of ceil((S0 + i TQ) / KT).
     __host__ __device__ static int tiles_full(int S0, int k, int lq) {
         if (lq >= LKT) return (int)((unsigned)k * (((unsigned)S0 + KT - 1) >> LKT) + (triangle(k) << (lq - LKT)));
@@ -201,21 +201,26 @@ struct Ragged {
     __host__ __device__ static int cost(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0;
         const int lq = LRT - p.lgG, nk = (int)((unsigned)(s.T + (1 << lq) - 1) >> lq), S0 = s.L - s.T - s.pfx;
-        const int n = JOINT && s.group ? nk * tiles(s.pfx, 0) : tiles_full(S0, nk - 1, lq) + tiles(S0, s.T);
-        return n * tile_cost(cl) + nk * start_cost(cl);
+        const unsigned n = JOINT && s.group ? (unsigned)nk * (unsigned)tiles(s.pfx, 0)
+                                            : (unsigned)tiles_full(S0, nk - 1, lq) + (unsigned)tiles(S0, s.T);
+        return (int)(n * tile_cost(cl) + (unsigned)nk * start_cost(cl));
     }
-    // The same to a few parts in a million, without wrapping.
+    // At least that, to a few parts in a million, and at most a tile or two per stream more; does not wrap.
     __host__ __device__ static float cost_about(const RaggedParams& p, const Entry& s, int cl) {
         if (!s.ok) return 0.f;
-        const float nk = (float)s.T / (float)(RT >> p.lgG) + 1.f, own = (float)(JOINT && s.group ? s.pfx : s.L - s.pfx);
-        return nk * ((own / KT + 1.f) * tile_cost(cl) + start_cost(cl));
+        const int lq = LRT - p.lgG, nk = (int)(((unsigned)s.T + (1u << lq) - 1) >> lq);
+        const float f = (float)nk, own = JOINT && s.group ? (float)s.pfx : (float)(s.L - s.T - s.pfx) + 0.5f * (1 << lq) * (f + 1.f);
+        return f * ((own / KT + 1.f) * tile_cost(cl) + start_cost(cl));
     }
+    // A call of more units is refused (2^31 less the estimate's part in a million, rounded down).
+    static constexpr float MOST = 2.1e9f;
 
     // The batch's split: total cost U, class 0's part W0, CTAs P.
     // CTA i of P takes `each` units, the first `more` of them one more.
     struct Split {
         int U, W0, P, each, more;
         bool valid;
+        uint32_t why;  // not valid: the error to flag
     };
     __device__ static void divide(const RaggedParams& p, Split& sp) {
         const int want = sp.U >> lg_min(sp.W0);
@@ -245,12 +250,12 @@ struct Ragged {
         k.prefix = k.groups + p.NG + 1;
         return k;
     }
-    // ... and whether cu and the groups ascend within their bounds.
+    // ... and whether cu and the groups ascend within their bounds and the sums hold the cost.
     __device__ static Split scan(const RaggedParams& p, const Work& k, int lane) {
         const int NE = groups(p) + p.B;
         int* c = k.c;
         int carry[2] = {0, 0};
-        float about = 0.f;  // the total cost: sums that 32 bits do not hold are refused
+        float about = 0.f;  // the total cost
         bool bad = false;
         if (lane < 2) c[lane * (NE + 1)] = 0;
         for (int g = lane; JOINT && g <= p.NG; g += 32) {
@@ -314,9 +319,9 @@ struct Ragged {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) about += __shfl_xor_sync(0xFFFFFFFFu, about, o);
-        bad |= about * (float)p.H_kv > 2.1e9f;
         Split sp;
-        sp.valid = !bad;
+        sp.why = bad ? DEV_BAD_SEQ : DEV_TOO_LARGE;
+        sp.valid = !bad && about * (float)p.H_kv <= MOST;
         sp.W0 = sp.valid ? carry[0] * p.H_kv : 0;
         sp.U = sp.valid ? sp.W0 + carry[1] * p.H_kv : 0;
         divide(p, sp);

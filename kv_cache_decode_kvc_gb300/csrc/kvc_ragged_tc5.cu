@@ -452,7 +452,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         if (blockIdx.x == 0) {
             const int n = 2 * (R::groups(p) + p.B + 1);
             for (int i = lane; i < n; i += 32) p.plan[i] = sp.valid ? work.c[i] : 0;
-            if (!sp.valid && lane == 0) atomicOr(p.err, DEV_BAD_SEQ);
+            if (!sp.valid && lane == 0) atomicOr(p.err, sp.why);
         }
         typename R::Walk wk;
         if (lane < 3) wk = R::walk(p, sp, work, blockIdx.x, lane);

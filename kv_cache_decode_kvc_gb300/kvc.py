@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "kvc.h")
 
 KVC_BF16, KVC_F32 = 0, 1
 KVC_OK, KVC_EINVAL, KVC_ENOMEM, KVC_ECUDA, KVC_ERANGE, KVC_EDEVICE, KVC_EUNSUPPORTED = range(7)
-KVC_DEV_BAD_LENS, KVC_DEV_WAIT_TIMEOUT, KVC_DEV_BAD_BLOCK, KVC_DEV_BAD_SEQ = 1, 2, 4, 8
+KVC_DEV_BAD_LENS, KVC_DEV_WAIT_TIMEOUT, KVC_DEV_BAD_BLOCK, KVC_DEV_BAD_SEQ, KVC_DEV_TOO_LARGE = 1, 2, 4, 8, 16
 KVC_CACHE_PLAIN, KVC_CACHE_INT8, KVC_CACHE_FP8 = 0, 1, 2
 KVC_ROPE_HALF, KVC_ROPE_ADJACENT = 0, 1
 

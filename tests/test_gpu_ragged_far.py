@@ -102,3 +102,21 @@ def test_append_to_the_last_slots():
     for x, old, new in zip(c.layer_views(0), before, (k, v)):
         old[1, :, BS - 5:] = new.transpose(0, 1)
         assert torch.equal(x, old)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_more_work_than_a_call_takes_is_refused(dtype, D, shared):
+    # one token of 64 KV heads at the last position: 64 x 2^24 tiles of 128 keys (2^25 of 64)
+    dt, i32 = torch.bfloat16 if dtype == "bf16" else torch.float32, dict(dtype=torch.int32, device="cuda")
+    c = kvc.PagedKVCache(1, 2, BS, 1, ONE, 64, 64, D, dtype)
+    table, q = torch.zeros(1, ONE, **i32), torch.randn(1, 64, D, device="cuda").to(dt)
+    out = torch.full_like(q, 7.0)
+    cu, lens = torch.tensor([0, 1], **i32), torch.tensor([BS * ONE], **i32)
+    ws = torch.full((c.attn_workspace_bytes(1, 1),), 255, dtype=torch.uint8, device="cuda")
+    if shared:
+        c.attn_shared(0, q, out, table, cu, lens, torch.tensor([0, 1], **i32), torch.tensor([BS], **i32), workspace=ws)
+    else:
+        c.attn_ragged(0, q, out, table, cu, lens, workspace=ws)
+    assert c.last_error() == (kvc.KVC_EDEVICE, kvc.KVC_DEV_TOO_LARGE)
+    assert (out == 7.0).all()

@@ -22,6 +22,18 @@ template <class R> static int units(int lgG, int T, int L, int pfx, int group) {
     const Entry s = entry(T, L, pfx, group);
     return R::cost(p, s, R::cls(p, s));
 }
+template <class R> static float about(int lgG, int T, int L, int pfx, int group) {
+    RaggedParams p{};
+    p.lgG = lgG;
+    const Entry s = entry(T, L, pfx, group);
+    return R::cost_about(p, s, R::cls(p, s));
+}
+extern "C" float ragged_about(int kind, int lgG, int T, int L, int pfx, int group) {
+    return kind == 0   ? about<Ragged<8, 7, true, true>>(lgG, T, L, pfx, group)
+           : kind == 1 ? about<Ragged<6, 6, false, true>>(lgG, T, L, pfx, group)
+                       : about<Ragged<6, 5, false, true>>(lgG, T, L, pfx, group);
+}
+extern "C" float ragged_most() { return Ragged<8, 7, true, true>::MOST; }
 extern "C" int ragged_units(int kind, int lgG, int T, int L, int pfx, int group) {
     return kind == 0   ? units<Ragged<8, 7, true, true>>(lgG, T, L, pfx, group)
            : kind == 1 ? units<Ragged<6, 6, false, true>>(lgG, T, L, pfx, group)
@@ -37,7 +49,9 @@ def lib(tmp_path_factory):
     (at / "split.cu").write_text(SOURCE)
     subprocess.run(["nvcc", *build.ARCH, *build.FLAGS, "-I", build.CSRC, "-shared", "-cudart", "static", "-o",
                     str(at / "split.so"), str(at / "split.cu")], check=True, capture_output=True)
-    return ctypes.CDLL(str(at / "split.so"))
+    so = ctypes.CDLL(str(at / "split.so"))
+    so.ragged_about.restype = so.ragged_most.restype = ctypes.c_float
+    return so
 
 
 def _exact(kind, lgG, T, L, pfx, group):
@@ -70,3 +84,28 @@ def test_units_of_entries_near_and_far(lib, kind):
             tried += 1
             assert lib.ragged_units(kind, *c) == want, c
     assert tried > 400
+
+
+@pytest.mark.parametrize("kind", range(3))
+def test_estimates_refuse_what_32_bits_do_not_hold_and_little_else(lib, kind):
+    # the estimate is no less than the cost (up to fp32's rounding, 2^-20 for its few steps) and more by at most
+    # 2.5 tiles a stream (a rounded-up tile, and for the last, partial stream up to 256 keys' tiles of difference)
+    lrt, lkt, pairs = KINDS[kind]
+    rng = random.Random(10 + kind)
+    top, tile = 2 ** 31 - 16, 2 if pairs else 1
+    assert lib.ragged_most() * (1 + 2.0 ** -20) < 2 ** 31
+    for _ in range(400):
+        lgG, T = rng.randint(0, 5), rng.choice([1, rng.randint(1, 100), int(2 ** rng.uniform(0, 16))])
+        L = min(top, T + int(2 ** rng.uniform(0, 31)))
+        pfx = rng.choice([0, rng.randint(0, (L - T) // 16) * 16])
+        c = (lgG, T, L, pfx, int(rng.random() < 0.2 and pfx > 0))
+        want, est, streams = _exact(kind, *c), lib.ragged_about(kind, *c), -(-T // (1 << (lrt - lgG)))
+        assert want * (1 - 2.0 ** -20) <= est <= want * (1 + 2.0 ** -20) + tile * (streams + 1.5 * (256 >> lkt)), (c, want, est)
+
+
+def test_long_prompts_are_within_the_limit(lib):
+    # 64 heads on 8: a prompt of 800,000 tokens is 1.25 10^9 units, one of 1,000,000 1.95 10^9; 1,100,000 are too many
+    for T, fits in ((500000, True), (733000, True), (800000, True), (1000000, True), (1100000, False)):
+        c = (0, 3, T, T, 0, 0)
+        assert (8 * lib.ragged_about(*c) <= lib.ragged_most()) == fits, T
+        assert (8 * _exact(*c) < 2 ** 31) == fits, T
