@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) append_rope_kernel(const Rope
         for (int k = 0; k < PRE; ++k) load(tid + k * ROPE_THREADS, xa[k], xb[k]);
     }
     bool bad = false;
+    uint32_t flag = 0;  // of this warp's row: set once cu is known to be sound, else it speaks of no row
     for (int b = tid; b <= p.B; b += ROPE_THREADS) {
         const int c = __ldg(p.cu + b);
         bad |= (b == 0 ? c != 0 : c < __ldg(p.cu + b - 1)) || c > p.N;
@@ -98,11 +99,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) append_rope_kernel(const Rope
                 const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
                 if (c0 >= 0 && c0 <= row && row < c1 && c1 <= p.N) {  // (else cu does not ascend within 0 .. N)
                     if (L < c1 - c0 || L > p.T_max) {
-                        atomicOr(p.err, DEV_BAD_LENS);
+                        flag = DEV_BAD_LENS;
                     } else {
                         slot = L - (c1 - c0) + (row - c0);
                         const int e = __ldg(p.table + (size_t)b * p.max_blocks + slot / p.bs);
-                        if ((unsigned)e >= (unsigned)p.num_blocks) atomicOr(p.err, DEV_BAD_BLOCK);
+                        if ((unsigned)e >= (unsigned)p.num_blocks) flag = DEV_BAD_BLOCK;
                         else kr = (int64_t)e * p.H_kv * p.bs + slot % p.bs;
                     }
                 }
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) append_rope_kernel(const Rope
         if (blockIdx.x == 0 && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
         return;
     }
+    if (flag) atomicOr(p.err, flag);
     for (int i = tid; i < TB * pairs; i += ROPE_THREADS) {
         const int t = i / pairs, j = i - t * pairs;
         if (slot_s[t] < 0) continue;

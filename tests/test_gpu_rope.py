@@ -162,3 +162,21 @@ def test_append_rope_looks_nothing_up_for_rows_outside_their_sequence():
         assert status == kvc.KVC_EDEVICE and word & kvc.KVC_DEV_BAD_SEQ
         K, V = (x.cpu() for x in c.layer_views(0))
         assert torch.equal(K, bt.K) and torch.equal(V, bt.V) and not q_out.any()
+
+
+def test_append_rope_flags_unsound_bounds_alone():
+    # lens below the new tokens and bad table entries say nothing where cu_seqlens is unsound elsewhere
+    bt = Batch([2, 3, 1, 2, 1], [4, 40, 9, 0, 30], 16, 4, 2, 64, seed=7)
+    rope = kvc.Rope(_freq(64))
+    for cu in ([0, 2, 5, 6, 8, 7], [0, 2, 5, 6, 8, 10], [0, 2, 5, 6, 5, 9], [0, 2, -1, 6, 8, 9]):
+        for bad in ("lens", "table", "both"):
+            c, d = bt.cache(kvc), bt.dev()
+            d["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+            if bad != "table":
+                d["lens"][:] = 0
+            if bad != "lens":
+                d["table"][:] = -1
+            q_out = torch.zeros_like(d["q"])
+            c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], q_out)
+            assert c.last_error() == (kvc.KVC_EDEVICE, kvc.KVC_DEV_BAD_SEQ), (cu, bad)
+            assert not q_out.any()
