@@ -290,9 +290,10 @@ int kvc_get_paged_shape(kvc_t h, int* num_blocks, int* block_size, int* max_bloc
  * With several axes (time, height, width, ...) pair i takes its position from axis[i] in
  * [0, n_axes), 1 <= n_axes <= 8; axis = NULL puts every pair on axis 0.  inv_freq (double) and axis
  * are HOST arrays of rot_dim / 2 entries; frequency scaling for long contexts is the caller's choice of
- * them and of scale (finite).  The angle is kept as a 64-bit fraction of a turn, so positions far
- * from 0 lose nothing.  A plain host object: no device memory, usable with any handle (create
- * returns KVC_EUNSUPPORTED for rot_dim > 256). */
+ * them and of scale (finite).  Angles are 64-bit fractions of a turn (within 2^-62 of a turn per
+ * position), rounded to fp32 for the cosine and sine, so far positions are as exact as near ones.
+ * A plain host object: no device memory, usable with any handle (create returns KVC_EUNSUPPORTED
+ * for rot_dim > 256). */
 typedef struct kvc_rope* kvc_rope_t;
 #define KVC_ROPE_HALF 0
 #define KVC_ROPE_ADJACENT 1

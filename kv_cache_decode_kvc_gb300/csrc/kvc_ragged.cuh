@@ -29,6 +29,8 @@
 // the sequences' own); of other streams, and all later pieces, to slots of their worker.
 #pragma once
 
+#include <math.h>
+
 #include "kvc_internal.cuh"
 
 namespace kvc {
@@ -604,8 +606,21 @@ int launch_ragged_cc(int dtype, const RaggedParams& p, cudaStream_t s);
 // pool's maps with min(bs, 128)-row boxes.
 int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtensorMap& q1, const CUtensorMap& k,
                       const CUtensorMap& v, cudaStream_t s);
+// Radians per position as turns per position modulo 1 (whole turns change nothing), in 2^-64 turns.
+// 1 / (2 pi) and the product are sums of two doubles, so the result is within 2^-62 of a turn for rates
+// up to 2^44 (an angle at position 2^31 within 2^-31); a negative rate is the negated fraction, not the
+// rest to the next turn, which a double would round.
+inline uint64_t rope_turns(double rate) {
+    const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double a = fabs(rate), p = a * hi, e = fma(a, hi, -p) + a * lo;
+    const double pf = p - floor(p), ef = fmod(e, 1.0);  // both exact
+    uint64_t t = (uint64_t)ldexp(pf, 64);
+    if (ef < 0) t -= (uint64_t)ldexp(-ef, 64);
+    else t += (uint64_t)ldexp(ef, 64);
+    return rate < 0 ? 0 - t : t;
+}
 struct RopeTable {
-    uint64_t freq[128];  // inv_freq in 2^-64 turns per position
+    uint64_t freq[128];  // rope_turns of inv_freq
     uint8_t axis[128];
     int rot_dim, adjacent, n_axes;
     float scale;

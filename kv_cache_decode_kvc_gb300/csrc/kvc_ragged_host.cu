@@ -122,11 +122,7 @@ int kvc_rope_create(kvc_rope_t* out, int rot_dim, const double* inv_freq, int la
             delete r;
             return KVC_EINVAL;
         }
-        // turns per position modulo 1 (whole turns change nothing), as a 64-bit fraction; double
-        // keeps 53 significant bits of it, so an angle is off by 2^-53 of itself at most
-        double f = inv_freq[i] * 0.15915494309189535;
-        f -= floor(f);
-        r->t.freq[i] = f >= 1.0 ? 0 : (uint64_t)ldexp(f, 64);
+        r->t.freq[i] = kvc::rope_turns(inv_freq[i]);
         r->t.axis[i] = (uint8_t)a;
     }
     *out = r;

@@ -3,10 +3,10 @@
 // Pair i of a head's first rot_dim dimensions turns by a_i = position * inv_freq[i] ("第 1 周 ·
 // Day 4：KV Cache 与 MQA / GQA" §3.2: a new token's position is its place in the sequence):
 //     y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a.
-// The frequency is kept as a 64-bit fraction of a turn per position, so position * frequency
-// modulo one turn is one wrapping integer product: exact at any distance, where an fp32 product
-// would lose the angle's low bits (2^-24 of 10^5 radians is 0.006).  The top 32 bits give the
-// half-turns in [-1, 1) that sincospif takes (error below 2^-24 of a turn).
+// The frequency is kept as a 64-bit fraction of a turn per position, within 2^-62 (rope_turns), so
+// position * frequency modulo one turn is one wrapping integer product: exact at any distance, where an
+// fp32 product would lose the angle's low bits (2^-24 of 10^5 radians is 0.006).  The top 32 bits give
+// the half-turns in [-1, 1) that sincospif takes, rounded to fp32 (error below 2^-24 of a turn).
 #include "kvc_ragged.cuh"
 
 namespace kvc {

@@ -180,3 +180,25 @@ def test_append_rope_flags_unsound_bounds_alone():
             c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], q_out)
             assert c.last_error() == (kvc.KVC_EDEVICE, kvc.KVC_DEV_BAD_SEQ), (cu, bad)
             assert not q_out.any()
+
+
+def test_append_rope_negative_and_tiny_frequencies_at_far_positions():
+    # a rate of -x turns back by exactly what x turns; small ones are not rounded to the next whole turn first
+    bt = Batch([6], [10], 16, 2, 1, 128, "f32", seed=8)
+    pos = torch.tensor([[0, 1, -1, -(2 ** 31), 2 ** 31 - 1, 1234567890]], dtype=torch.int32)
+    rates = [1e-9 * 3.0 ** (i / 4) for i in range(64)]
+    got = []
+    for sign in (1, -1):
+        c, d = bt.cache(kvc), bt.dev()
+        freq = [sign * f for f in rates]
+        q_out = torch.empty_like(d["q"])
+        c.append_rope(0, kvc.Rope(freq), d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], q_out,
+                      (sign * pos.long()).clamp(-2 ** 31, 2 ** 31 - 1).to(torch.int32).cuda())
+        y, w = rotate64(bt.q, (sign * pos.long()).clamp(-2 ** 31, 2 ** 31 - 1).T, freq, [0] * 64, False)
+        err = (q_out.cpu().double() - y).abs()
+        # the reference's angles reach 2^31 x 3.4e-2 < 2^27 radians in double: off by 2^27 2^-53; the fraction by
+        # 2^31 2^-62 turns
+        assert (err <= w * (12 * U + 2.0 ** -25) + U * y.abs()).all(), float(err.max())
+        got.append(q_out)
+    rows = [0, 1, 2, 4, 5]  # (-2^31 has no negative)
+    assert (got[0][rows] - got[1][rows]).abs().max() < 1e-5

@@ -1,6 +1,8 @@
-"""The cost sums that split ragged batches over the workers, compiled for the host and compared with exact sums:
-a wrong sum would put a stream's start, and with it every lookup of its keys, in the wrong place."""
+"""Host arithmetic of the ragged calls, compiled from their headers and compared with exact values: the cost sums that
+split a batch over the workers (a wrong sum would put a stream's start, and with it every lookup of its keys,
+in the wrong place), and the rotary frequencies as fractions of a turn."""
 import ctypes
+import decimal
 import random
 import subprocess
 
@@ -33,6 +35,7 @@ extern "C" float ragged_about(int kind, int lgG, int T, int L, int pfx, int grou
            : kind == 1 ? about<Ragged<6, 6, false, true>>(lgG, T, L, pfx, group)
                        : about<Ragged<6, 5, false, true>>(lgG, T, L, pfx, group);
 }
+extern "C" uint64_t turns(double rate) { return rope_turns(rate); }
 extern "C" float ragged_most() { return Ragged<8, 7, true, true>::MOST; }
 extern "C" int ragged_units(int kind, int lgG, int T, int L, int pfx, int group) {
     return kind == 0   ? units<Ragged<8, 7, true, true>>(lgG, T, L, pfx, group)
@@ -50,6 +53,7 @@ def lib(tmp_path_factory):
     subprocess.run(["nvcc", *build.ARCH, *build.FLAGS, "-I", build.CSRC, "-shared", "-cudart", "static", "-o",
                     str(at / "split.so"), str(at / "split.cu")], check=True, capture_output=True)
     so = ctypes.CDLL(str(at / "split.so"))
+    so.turns.argtypes, so.turns.restype = [ctypes.c_double], ctypes.c_uint64
     so.ragged_about.restype = so.ragged_most.restype = ctypes.c_float
     return so
 
@@ -109,3 +113,20 @@ def test_long_prompts_are_within_the_limit(lib):
         c = (0, 3, T, T, 0, 0)
         assert (8 * lib.ragged_about(*c) <= lib.ragged_most()) == fits, T
         assert (8 * _exact(*c) < 2 ** 31) == fits, T
+
+
+def test_frequencies_as_fractions_of_a_turn(lib):
+    # 80 digits of 1 / (2 pi); the fraction is within 2^-62 of a turn, 4 units, for rates of up to 2^44 of either sign
+    with decimal.localcontext() as ctx:
+        ctx.prec = 80
+        pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+        rng = random.Random(5)
+        rates = [0.0, 1.0, 0.5, 2.0 ** 44, 6.283185307179586, 3.141592653589793, 1e-6, 1e-19, 1e-300, 5e-324]
+        rates += [10000.0 ** (-i / 64) for i in range(64)] + [2 ** rng.uniform(-70, 44) for _ in range(3000)]
+        for f in rates:
+            want = decimal.Decimal(f) / (2 * pi) * 2 ** 64
+            for sign in (1, -1):
+                off = (decimal.Decimal(lib.turns(sign * f)) - sign * want) % 2 ** 64
+                assert min(abs(off), abs(2 ** 64 - abs(off))) <= 4, (sign * f, off)
+        for f in (2.0 ** 60, 1e30, 1e308, -1e308):  # whatever the fraction, no overflow
+            assert 0 <= lib.turns(f) < 2 ** 64
