@@ -304,8 +304,8 @@ int kvc_rope_destroy(kvc_rope_t r);
 /* Append with rotation: k, rotated by its position, and v as it is go to the sequences' new slots
  * lens[b] - T_b + i of `layer` through the block table; q, rotated, goes to q_out (which may be q
  * itself with the same stride; otherwise the two do not overlap).  q = q_out = NULL appends only.
- * positions (int32 [n_axes, N] with axis rows pos_stride >= N elements apart, device) gives each
- * row's position per axis; NULL takes the slot for every axis.  Products in fp32, rounded once to
+ * positions (int32 [n_axes, N] with axis rows pos_stride >= N elements apart, or 0: one row for all
+ * axes, device) gives each row's position per axis; NULL takes the slot for every axis.  Products in fp32, rounded once to
  * the cache dtype.  Only the new slots change; two rows must not share a slot (a block that two
  * sequences both write).  A row whose table entry is out of range is not stored
  * (KVC_DEV_BAD_BLOCK); its q is still rotated. */

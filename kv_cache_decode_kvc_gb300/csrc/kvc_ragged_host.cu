@@ -145,7 +145,7 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
     if (q && (!packed_ok(q, q_stride, qrow, h->es) || !packed_ok(q_out, q_out_stride, qrow, h->es))) return KVC_EINVAL;
     if (q && q == q_out && q_stride != q_out_stride) return KVC_EINVAL;
     if (!packed_ok(k, k_stride, krow, h->es) || !packed_ok(v, v_stride, krow, h->es)) return KVC_EINVAL;
-    if (positions && (!aligned(positions, 4) || (rope->t.n_axes > 1 && pos_stride < N))) return KVC_EINVAL;
+    if (positions && (!aligned(positions, 4) || (rope->t.n_axes > 1 && pos_stride < N && pos_stride != 0))) return KVC_EINVAL;
     if (!aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(lens, 4)) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;

@@ -604,7 +604,10 @@ class PagedKVCache(KVCache):
                     N > 1 and positions.stride(1) != 1) or not positions.is_cuda:
                 raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}] on the GPU, got {positions.dtype} "
                                  f"{list(positions.shape)} on {positions.device}")
-            ps = max(positions.stride(0), N)
+            # axes that are views of one row (an expanded tensor) are read there; other rows that overlap are refused
+            ps = positions.stride(0) if rope.n_axes > 1 else N
+            if rope.n_axes > 1 and 0 < ps < N:
+                raise ValueError(f"positions: axes overlap, got strides {positions.stride()}")
         self._batch(block_table, cu_seqlens, lens, int32)
         kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
                               cu_seqlens, lens, N, stream)

@@ -202,3 +202,24 @@ def test_append_rope_negative_and_tiny_frequencies_at_far_positions():
         got.append(q_out)
     rows = [0, 1, 2, 4, 5]  # (-2^31 has no negative)
     assert (got[0][rows] - got[1][rows]).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_append_rope_positions_shared_by_the_axes(N):
+    # an expanded tensor: one row of positions for all axes, at the end of its memory
+    bt = Batch([N], [10], 16, 2, 1, 64, seed=9)
+    freq, axis = _freq(64), [i % 3 for i in range(32)]
+    pos = torch.randint(0, 5000, (N,), generator=torch.Generator().manual_seed(2)).to(torch.int32)
+    rope = kvc.Rope(freq, axis=axis)
+    d = bt.dev()
+    for p in (pos.cuda()[None].expand(3, N), pos.repeat(3, 2).cuda()[:, :N], pos.repeat(3, 1).cuda()):
+        c = bt.cache(kvc)
+        q_out = torch.zeros_like(d["q"])
+        c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], q_out, p)
+        assert c.last_error() == (kvc.KVC_OK, 0)
+        _check(bt, c, q_out, pos[:, None].expand(N, 3), freq, axis, False, bt.q)
+    c = bt.cache(kvc)
+    if N > 1:
+        overlapping = torch.zeros(200, dtype=torch.int32, device="cuda").as_strided((3, N), (N - 1, 1))
+        with pytest.raises(ValueError, match="overlap"):
+            c.append_rope(0, rope, d["q"], d["k"], d["v"], d["table"], d["cu"], d["lens"], None, overlapping)
