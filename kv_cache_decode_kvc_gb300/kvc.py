@@ -126,19 +126,28 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
-def _current_stream() -> int:
+def _current_stream(device=None) -> int:
     """The current torch stream's handle.  torch.cuda.current_stream() spends 4 us on wrapping it;
-    the raw getter, where this torch has it, takes the device's index."""
+    the raw getter, where this torch has it, takes the device's index (None: the current device)."""
     global _raw_stream
-    import torch
     if _raw_stream is None:
+        import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
-    torch.cuda._lazy_init()
-    return _raw_stream(torch._C._cuda_getDevice())
+    return _raw_stream(_device() if device is None else device)
 
 
-_raw_stream = None
+def _device() -> int:
+    """The current device, which is the handle's (the library refuses another): the tensors' device has to be it."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        torch.cuda._lazy_init()
+        _get_device = torch._C._cuda_getDevice
+    return _get_device()
+
+
+_raw_stream = _get_device = None
 
 
 def _as_stream(stream):
@@ -521,20 +530,24 @@ class Rope:
             pass
 
 
-def _packed(t, heads, D, dtype, what):
+def _packed(t, heads, D, dtype, what, dev=None):
     """Elements between tokens of a packed [N, heads, D] tensor."""
     sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype} on the GPU, got {tuple(sh)} {t.dtype} on {t.device}")
+    if dev is None:
+        dev = _device() if t.is_cuda else 0
+    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype} on the GPU (the current device), got {tuple(sh)} {t.dtype} on {t.device}")
     if st[2] != 1 or (st[1] != D and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {st}")
     return st[0] if sh[0] > 1 else max(st[0], heads * D)
 
 
-def _index(t, what, int32, *shape):
-    if t.dtype != int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: want contiguous int32 {list(shape)} on the GPU, got {t.dtype} {list(t.shape)} on "
-                         f"{t.device}")
+def _index(t, what, int32, *shape, dev=None):
+    if dev is None:
+        dev = _device() if t.is_cuda else 0
+    if t.dtype != int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what}: want contiguous int32 {list(shape)} on the GPU (the current device), got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
 
 
 class PagedKVCache(KVCache):
@@ -568,10 +581,10 @@ class PagedKVCache(KVCache):
         kvc_paged_decode_step(self.h, layer, q, k_new, v_new, out, block_table, lens, stream)
 
 
-    def _batch(self, block_table, cu_seqlens, lens, int32):
-        _index(block_table, "block_table", int32, self.B, self.max_blocks)
-        _index(cu_seqlens, "cu_seqlens", int32, self.B + 1)
-        _index(lens, "lens", int32, self.B)
+    def _batch(self, block_table, cu_seqlens, lens, int32, dev):
+        _index(block_table, "block_table", int32, self.B, self.max_blocks, dev=dev)
+        _index(cu_seqlens, "cu_seqlens", int32, self.B + 1, dev=dev)
+        _index(lens, "lens", int32, self.B, dev=dev)
 
     def append_rope(self, layer, rope, q, k, v, block_table, cu_seqlens, lens, q_out=None, positions=None,
                     stream=None):
@@ -581,17 +594,17 @@ class PagedKVCache(KVCache):
         int32 [n_axes, N] or, for one axis, [N] (None: the slot in the sequence)."""
         dt = self.torch_dtype
         int32 = _torch.int32
-        N, D = k.shape[0], self.D
-        ks, vs = _packed(k, self.H_kv, D, dt, "k"), _packed(v, self.H_kv, D, dt, "v")
+        N, D, dev = k.shape[0], self.D, _device()
+        ks, vs = _packed(k, self.H_kv, D, dt, "k", dev), _packed(v, self.H_kv, D, dt, "v", dev)
         if v.shape[0] != N:
             raise ValueError(f"v: want {N} rows, got {v.shape[0]}")
         qs = qos = 0
         if q is not None:
-            qs = qos = _packed(q, self.H_q, D, dt, "q")
+            qs = qos = _packed(q, self.H_q, D, dt, "q", dev)
             if q_out is None:
                 q_out = q
             else:
-                qos = _packed(q_out, self.H_q, D, dt, "q_out")
+                qos = _packed(q_out, self.H_q, D, dt, "q_out", dev)
             if q.shape[0] != N or q_out.shape[0] != N:
                 raise ValueError(f"q, q_out: want {N} rows, got {q.shape[0]}, {q_out.shape[0]}")
         elif q_out is not None:
@@ -601,14 +614,16 @@ class PagedKVCache(KVCache):
             if positions.dim() == 1 and rope.n_axes == 1:
                 positions = positions[None]
             if positions.dtype != int32 or tuple(positions.shape) != (rope.n_axes, N) or (
-                    N > 1 and positions.stride(1) != 1) or not positions.is_cuda:
-                raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}] on the GPU, got {positions.dtype} "
-                                 f"{list(positions.shape)} on {positions.device}")
+                    N > 1 and positions.stride(1) != 1) or positions.get_device() != dev:
+                raise ValueError(f"positions: want int32 [{rope.n_axes}, {N}] on the GPU (the current device), got "
+                                 f"{positions.dtype} {list(positions.shape)} on {positions.device}")
             # axes that are views of one row (an expanded tensor) are read there; other rows that overlap are refused
             ps = positions.stride(0) if rope.n_axes > 1 else N
             if rope.n_axes > 1 and 0 < ps < N:
                 raise ValueError(f"positions: axes overlap, got strides {positions.stride()}")
-        self._batch(block_table, cu_seqlens, lens, int32)
+        self._batch(block_table, cu_seqlens, lens, int32, dev)
+        if stream is None:
+            stream = _current_stream(dev)
         kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
                               cu_seqlens, lens, N, stream)
 
@@ -618,17 +633,17 @@ class PagedKVCache(KVCache):
 
     def _attn_args(self, q, out, block_table, cu_seqlens, lens, NG, workspace, stream):
         dt = self.torch_dtype
-        N = q.shape[0]
-        qs, os_ = _packed(q, self.H_q, self.D, dt, "q"), _packed(out, self.H_q, self.D, dt, "out")
+        N, dev = q.shape[0], _device()
+        qs, os_ = _packed(q, self.H_q, self.D, dt, "q", dev), _packed(out, self.H_q, self.D, dt, "out", dev)
         if out.shape[0] != N:
             raise ValueError(f"out: want {N} rows, got {out.shape[0]}")
-        self._batch(block_table, cu_seqlens, lens, _torch.int32)
+        self._batch(block_table, cu_seqlens, lens, _torch.int32, dev)
         if workspace is None:
             # allocated on the call's stream, so that its next use is ordered behind this call
             with _torch.cuda.stream(_as_stream(stream)):
                 workspace = _torch.empty(self.attn_workspace_bytes(N, NG), dtype=_torch.uint8, device="cuda")
-        elif not workspace.is_contiguous() or not workspace.is_cuda:
-            raise ValueError("workspace: want a contiguous tensor on the GPU")
+        elif not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace: want a contiguous tensor on the GPU (the current device)")
         return N, qs, os_, workspace, workspace.numel() * workspace.element_size()
 
     def attn_ragged(self, layer, q, out, block_table, cu_seqlens, lens, workspace=None, stream=None):

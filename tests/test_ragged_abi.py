@@ -69,3 +69,53 @@ def test_tensors_on_the_host_are_refused():
         kvc._packed(x, 2, 64, torch.float32, "q")
     with pytest.raises(ValueError, match="on the GPU"):
         kvc._index(i, "lens", torch.int32, 4)
+
+
+class _On:
+    """What the binding's checks see of a tensor on GPU `device` (no GPU needed)."""
+
+    def __init__(self, t, device):
+        self.t, self.n, self.device = t, device, f"cuda:{device}"
+        self.is_cuda, self.shape, self.dtype = True, t.shape, t.dtype
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.n
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    # every tensor of the two calls in turn, on device 1 while the cache and the current device are 0; a call whose
+    # tensors are all in place reaches the library
+    import torch
+    called = []
+    monkeypatch.setattr(kvc, "_device", lambda: 0)
+    monkeypatch.setattr(kvc, "_current_stream", lambda device=None: 0)
+    for name in ("kvc_paged_append_rope", "kvc_paged_attn_ragged", "kvc_paged_attn_shared"):
+        monkeypatch.setattr(kvc, name, lambda *a, name=name: called.append(name))
+    c = kvc.PagedKVCache.__new__(kvc.PagedKVCache)
+    c.h, c.dtype_code = None, kvc.KVC_BF16
+    c.B, c.max_blocks, c.H_q, c.H_kv, c.D = 2, 5, 4, 2, 64
+    rope = kvc.Rope.__new__(kvc.Rope)
+    rope.r, rope.n_axes = None, 2
+
+    def i32(*shape):
+        return torch.zeros(shape, dtype=torch.int32)
+
+    bf = dict(dtype=torch.bfloat16)
+    batch = dict(block_table=i32(2, 5), cu_seqlens=i32(3), lens=i32(2))
+    append = dict(batch, q=torch.zeros(3, 4, 64, **bf), k=torch.zeros(3, 2, 64, **bf), v=torch.zeros(3, 2, 64, **bf),
+                  q_out=torch.zeros(3, 4, 64, **bf), positions=i32(2, 3))
+    attn = dict(batch, q=append["q"], out=append["q_out"], workspace=torch.zeros(64, dtype=torch.uint8))
+    shared = dict(attn, groups=i32(2), prefix_lens=i32(1))
+    for call, args in ((lambda **a: c.append_rope(0, rope, **a), append), (lambda **a: c.attn_ragged(0, **a), attn),
+                       (lambda **a: c.attn_shared(0, **a), shared)):
+        here = {k: _On(v, 0) for k, v in args.items()}
+        called.clear()
+        call(**here)
+        assert len(called) == 1
+        for k in args:
+            with pytest.raises(ValueError, match="current device"):
+                call(**dict(here, **{k: _On(args[k], 1)}))
+        assert len(called) == 1
