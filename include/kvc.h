@@ -319,8 +319,9 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
  * [0, lens[b] - T_b + i] (its own included; append first):
  *     out = softmax_t(q . K_t / sqrt(D)) V,   fp32 softmax and sums, rounded once.
  * Values at positions a row does not see never reach it, whatever they are.  bf16 caches with D =
- * 64 or 128 run on the tcgen05 tensor cores (softmax weights enter the second product as bf16),
- * every other shape, or math mode 1, on CUDA cores in fp32.  ws is device scratch of at least
+ * 64 or 128 run on the tcgen05 tensor cores: softmax weights enter the second product as two bf16
+ * terms (within 2^-15 of a weight) for sequences, and shared prefixes, of up to 64 query rows per
+ * KV head (tokens x H_q / H_kv, of a prefix all its group's), as one (2^-8) for larger ones.  Every other shape, or math mode 1, runs on CUDA cores in fp32.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each.
  * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on

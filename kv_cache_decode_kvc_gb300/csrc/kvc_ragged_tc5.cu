@@ -13,9 +13,12 @@
 // the row's maximum through shared memory; the reference maximum is raised only if it grew by more
 // than 2^8 (then O is rescaled in place); the weights are written as bf16 over the scores'
 // columns (each half over its own); O += P V (A = P from tensor memory, B = V read MN-major).
-// Weights as bf16: each is off by at most half a step, 2^-8 of it, as the output itself is after the
-// division; weights in two bf16 parts would need a second product per tile.  The denominator sums the
-// unrounded weights in fp32.
+// Weights enter O += P V in bf16.  Class 1, which waits for memory, takes each as two terms (the leading bits
+// and the rounded rest: off by 2^-15 of it; 256 tokens at 251 positions 96 us against
+// 92 with one, 24 at 3000 72 to 74).  Class 0 takes one, off by at most half a step, 2^-8, as the output itself is after
+// the division: there the tensor core and the softmax bound it, and the second term's products and arithmetic
+// cost 40 % (a chunk of 4096 tokens behind 12,288 positions 1276 us -> 1796, six prompts 222 -> 305).  The
+// denominator sums the unrounded weights in fp32.
 //
 // What bounds it.  Class 0: the chain of a set, from the S product's issue to its sight by the softmax 870
 // cycles (512 of the tensor core), softmax 1300 (64 scores a thread; arithmetic of two warps on one
@@ -42,6 +45,8 @@
 // NaN.  Warp 3 zeroes V rows behind the stream's end (stale or never loaded), and in the tiles of the
 // causal diagonal the non-finite values of positions that some row does not see; rows that do
 // see them add them at the end of the segment (a finite sum plus an infinity or NaN is that).
+#include <type_traits>
+
 #include "kvc_decode_tc5.cuh"
 #include "kvc_ragged_merge.cuh"
 
@@ -645,14 +650,21 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
             return ok;
         };
         auto uni = [&](uint32_t x) { return __shfl_sync(ALL, x, 0); };
-        // O[q] (+)= P[q] V, V's descriptor vb; its commits.  (one elected thread issues)
-        auto apply = [&](uint32_t q, uint32_t vb, uint32_t acc, uint64_t* done, uint64_t* freed) {
+        // O[q] (+)= P[q] V, V's descriptor vb; its commits.  (one elected thread issues)  The weights of 16
+        // keys are 8 columns: in class 0 one behind the other in the first half of their scores' columns, in class 1
+        // in the first half of those 16 keys' and their second terms in the second.
+        auto apply = [&](auto cl, uint32_t q, uint32_t vb, uint32_t acc, uint64_t* done, uint64_t* freed) {
             tc5_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < C::KT / 16; ++kk)
-                    tc5_mma_ts(tm + 256 + q * D, tm + q * 128 + (kk >> 2) * 64 + (kk & 3) * 8, vb + ((kk * 2 * C::GSTR) >> 4), (uint32_t)(dV >> 32), ID2,
-                               kk > 0 ? 1u : acc);
+                // (unrolled in class 1 as well, 256 tokens at 251 positions take 100 us against 96: instruction fetch)
+                constexpr int UNROLL = decltype(cl)::value == 0 ? C::KT / 16 : 2;
+#pragma unroll UNROLL
+                for (int kk = 0; kk < C::KT / 16; ++kk) {
+                    const uint32_t a = tm + q * 128 + (cl == 0 ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 16);
+                    const uint32_t b = vb + ((kk * 2 * C::GSTR) >> 4);
+                    tc5_mma_ts(tm + 256 + q * D, a, b, (uint32_t)(dV >> 32), ID2, kk > 0 ? 1u : acc);
+                    if (cl != 0) tc5_mma_ts(tm + 256 + q * D, a + 8, b, (uint32_t)(dV >> 32), ID2, 1u);
+                }
                 if (done) tc5_commit(done);
                 if (freed) tc5_commit(freed);
             }
@@ -686,7 +698,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     bool ok = wait_v(g, l.j) && wait_on(&M.pfull[q], (np >> q) & 1);
                     np ^= 1u << q;
                     if (!__all_sync(ALL, ok)) return false;
-                    apply(q, vb, acc, k ? nullptr : &M.ofull[q], &M.empty[vs]);
+                    apply(std::integral_constant<int, 1>{}, q, vb, acc, k ? nullptr : &M.ofull[q], &M.empty[vs]);
                 }
                 if (k) {
                     bool ok = v || wait_on(&M.qfull[q][place], (sc >> 1) & 1);
@@ -705,6 +717,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 // (written out for each set: with the set as a loop's variable a chunk of 4096 tokens takes a
                 // quarter longer)
                 const Seg& g = l.g;
+                constexpr std::integral_constant<int, 0> class0;
                 const int sets = (g.ntok << p.lgG) > 128 ? 2 : 1, n = g.n;
                 const uint32_t qb = (uint32_t)dQ;
                 auto v_desc = [&](uint32_t it) { return (uint32_t)dV + uni(it % C::NSLOT) * (C::TILE >> 4); };
@@ -726,12 +739,12 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     uint64_t *ve = &M.empty[item % C::NSLOT], *ke = &M.empty[(item + 1) % C::NSLOT];
                     uint64_t* qf = j + 2 == n ? &M.qfree : nullptr;
                     if (!__all_sync(ALL, wait_v(g, j)) || !ready(0)) return false;
-                    apply(0, vb, acc, nullptr, sets == 1 ? ve : nullptr);
+                    apply(class0, 0, vb, acc, nullptr, sets == 1 ? ve : nullptr);
                     if (!__all_sync(ALL, wait_item(item + 1))) return false;
                     score(0, qb, kb, sets == 1 ? ke : nullptr, sets == 1 ? qf : nullptr);
                     if (sets == 2) {
                         if (!ready(1)) return false;
-                        apply(1, vb, acc, nullptr, ve);
+                        apply(class0, 1, vb, acc, nullptr, ve);
                         score(1, qb + (C::QSET >> 4), kb, ke, qf);
                     }
                     item += 2;
@@ -739,10 +752,10 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                 if (!__all_sync(ALL, wait_v(g, n - 1))) return false;
                 const uint32_t vb = v_desc(item), acc = uni(n > 1 ? 1u : 0u);
                 if (!ready(0)) return false;
-                apply(0, vb, acc, &M.ofull[0], sets == 1 ? &M.empty[item % C::NSLOT] : nullptr);
+                apply(class0, 0, vb, acc, &M.ofull[0], sets == 1 ? &M.empty[item % C::NSLOT] : nullptr);
                 if (sets == 2) {
                     if (!ready(1)) return false;
-                    apply(1, vb, acc, &M.ofull[1], &M.empty[item % C::NSLOT]);
+                    apply(class0, 1, vb, acc, &M.ofull[1], &M.empty[item % C::NSLOT]);
                 }
                 ++item;
                 return true;
@@ -980,16 +993,23 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                         for (int d = 0; d < 64; d += 16) {
                             float x[16];
                             tc5_ld16(tS + half * 64 + d, x);
-                            uint32_t w[8];  // (they take the place of scores already read)
+                            // The weight as two bf16 terms, in the place of the 16 scores.  The first is cut off from a
+                            // little less than the weight, so both are positive where it is: an infinite value times
+                            // them stays that infinity (a second term of 0 or below would make it NaN).
+                            uint32_t w[8], w2[8];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
                                 const float2 y = make_float2(d + i < see ? x[i] : -INFINITY, d + i + 1 < see ? x[i + 1] : -INFINITY);
                                 const float2 a = __ffma2_rn(y, c2, mc2);
                                 const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
                                 sum = __fadd2_rn(sum, e);
-                                w[i / 2] = bf16x2_rn(e.x, e.y);
+                                const float2 h = __fmul2_rn(e, make_float2(1.f - 0x1p-16f, 1.f - 0x1p-16f));
+                                w[i / 2] = __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x7632);
+                                const float2 f = __ffma2_rn(make_float2(bf16_lo(w[i / 2]), bf16_hi(w[i / 2])), make_float2(-1.f, -1.f), e);
+                                w2[i / 2] = bf16x2_rn(f.x, f.y);
                             }
-                            tc5_st8(tS + half * 64 + d / 2, w);
+                            tc5_st8(tS + half * 64 + d, w);
+                            tc5_st8(tS + half * 64 + d + 8, w2);
                         }
                         finish(sum, j);
                     }

@@ -1,0 +1,91 @@
+"""How exact ragged attention is on the tensor cores: weights of two bf16 terms where few rows share a stream."""
+import pytest
+import torch
+
+from kv_cache_decode_kvc_gb300 import kvc
+
+from ragged_util import Batch, attention64, check_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _run(bt, shared=False, ctas=0):
+    c, d = bt.cache(kvc), bt.dev()
+    c.set_ctas(ctas)
+    out = torch.full((bt.rows, bt.H_q, bt.D), float("nan"), dtype=bt.dtype, device="cuda")
+    if shared:
+        c.attn_shared(0, d["q"], out, d["table"], d["cu"], d["lens"], d["groups"], d["prefix"])
+    else:
+        c.attn_ragged(0, d["q"], out, d["table"], d["cu"], d["lens"])
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    return c, d, out
+
+
+# A weight of two bf16 terms: the first is cut off (not rounded) from 1 - 2^-16 of it, so the rest is at most
+# 2^-7 + 2^-16 of the weight, exact in fp32 up to 2^-24, and its rounding at most 2^-8 of that.
+TWO_TERMS = 2.0 ** -8 * (2.0 ** -7 + 2.0 ** -16) + 2.0 ** -24
+
+
+def _check_two_terms(out, bt, ref):
+    o, tol, A = ref
+    check_attention(out, bt, (o, tol + TWO_TERMS * A, A))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H_q,H_kv", [(4, 4), (8, 2), (32, 1)])
+@pytest.mark.parametrize("ctas", [0, 5])
+def test_few_rows_have_weights_of_two_terms(D, H_q, H_kv, ctas):
+    # up to 64 rows per KV head: the bound leaves no room for weights of one term (2^-8 of A)
+    G = H_q // H_kv
+    bt = Batch([1, 64 // G, 2, 1, 0, 1], [900, 300, 0, 128, 5, 63], 32, H_q, H_kv, D, seed=51)
+    _, _, out = _run(bt, ctas=ctas)
+    _check_two_terms(out, bt, attention64(bt))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctas", [0, 5])
+def test_small_groups_have_weights_of_two_terms(D, ctas):
+    # 15 tokens of a group x 4 heads, 60 rows of its prefix
+    bt = Batch([1, 4, 1, 9, 1], [520, 512, 700, 533, 512], 32, 8, 2, D, "bf16", [0, 4, 5], [512, 256], seed=52)
+    _, _, out = _run(bt, True, ctas)
+    _check_two_terms(out, bt, attention64(bt))
+
+
+def test_single_tokens_are_as_exact_as_the_cache_s_own_attention():
+    # mean errors against 64 bits, the output's rounding apart, of the two calls for the same tokens
+    bt = Batch([1] * 12, [400 + 131 * i for i in range(12)], 16, 8, 2, 128, seed=53)
+    c, d, out = _run(bt)
+    ref = attention64(bt)[0]
+    own = torch.empty_like(out)
+    c.decode_attn(0, d["q"], own, d["table"], d["lens"])
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    # a value is off from its correctly rounded one where the error before rounding crosses a rounding border
+    missed = [int((o.cpu() != ref.to(torch.bfloat16)).sum()) for o in (out, own)]
+    # 12 x 8 x 128 values; with weights of one term (an error like the rounding's own) a third would miss
+    assert missed[1] < 0.02 * ref.numel() and missed[0] < 0.02 * ref.numel(), missed
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("ctas", [0, 1])
+def test_seen_values_that_are_not_finite_stay_what_they_are(D, value, ctas):
+    # at positions all tokens of a sequence see, in single tokens and in a few: every output of the column is that
+    # value, also where the weight is a bf16 number itself (equal keys: all weights 1)
+    for equal in (False, True):
+        bt = Batch([1, 3, 1], [300, 200, 129], 32, 8, 2, D, seed=55)
+        if equal:
+            bt.K.zero_()
+        ref = attention64(bt)
+        for b, at in ((0, 5), (1, 140), (2, 128)):
+            bt.V[bt.table[b, at // 32].long(), 1, at % 32, 7] = value
+        got = _run(bt, ctas=ctas)[2].cpu()
+        want = torch.full((5, 4), value, dtype=torch.bfloat16)
+        assert torch.equal(got[:, 4:, 7].nan_to_num(nan=9e9), want.nan_to_num(nan=9e9)), equal
+        got[:, 4:, 7], ref[0][:, 4:, 7] = 0, 0
+        _check_two_terms(got, bt, ref)
