@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
         const bool live = (tid >> 5) * (128 >> C::LTX) < nrow;  // alike in a warp
         float m[4], l[4];
         Four acc[4][C::NV];
-        int lim[4];
+        unsigned lim[4];  // (as positions of a tile: unsigned, they may pass 2^31)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             m[i] = -INFINITY;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
             for (int v = 0; v < C::NV; ++v) acc[i][v].lo.f = acc[i][v].hi.f = make_float2(0.f, 0.f);
         }
         for (int j = 0; j < g.n; ++j) {
-            const int t0 = g.kv0 + j * C::KT;
+            const unsigned t0 = g.kv0 + j * C::KT;
             const T* ks = kvs + (j & 1) * C::KV;
             const T* vs = ks + C::KT * C::KS;
             copies_done();
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
                 float mx = -INFINITY, x[C::NC];
 #pragma unroll
                 for (int c = 0; c < C::NC; ++c) {
-                    x[c] = tx + C::TX * c < lim[i] - t0 ? (s[i][c].f.x + s[i][c].f.y) * p.qscale : -INFINITY;
+                    x[c] = t0 + tx + C::TX * c < lim[i] ? (s[i][c].f.x + s[i][c].f.y) * p.qscale : -INFINITY;
                     mx = fmaxf(mx, x[c]);
                 }
 #pragma unroll
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
                             const Four x = load4(vs + (t + tt) * D + (v * C::TX + tx) * 4);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                if (decltype(guard)::value && t + tt >= lim[i] - t0) continue;
+                                if (decltype(guard)::value && t0 + t + tt >= lim[i]) continue;
                                 Two f;
                                 f.f.x = f.f.y = tt == 0 ? w[i].x : tt == 1 ? w[i].y : tt == 2 ? w[i].z : w[i].w;
                                 fma_two(acc[i][v].lo, f, x.lo);
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(CcCfg<T, D, JOINT>::THREADS, D > 128 ? 1 : 2) 
                             }
                         }
                 };
-                const int all = min(C::KT, lim[0] - t0), some = min(C::KT, lim[3] - t0);
+                const int all = min(C::KT, (int)(lim[0] - t0)), some = min(C::KT, (int)(lim[3] - t0));
                 int t = 0;
 #pragma unroll 1
                 for (; t + 4 <= all; t += 4) sum_tile(t, std::false_type{});
