@@ -13,12 +13,12 @@
 // the row's maximum through shared memory; the reference maximum is raised only if it grew by more
 // than 2^8 (then O is rescaled in place); the weights are written as bf16 over the scores'
 // columns (each half over its own); O += P V (A = P from tensor memory, B = V read MN-major).
-// Weights enter O += P V in bf16.  Class 1, which waits for memory, takes each as two terms (the leading bits
-// and the rounded rest: off by 2^-15 of it; 256 tokens at 251 positions 96 us against
-// 92 with one, 24 at 3000 72 to 74).  Class 0 takes one, off by at most half a step, 2^-8, as the output itself is after
-// the division: there the tensor core and the softmax bound it, and the second term's products and arithmetic
-// cost 40 % (a chunk of 4096 tokens behind 12,288 positions 1276 us -> 1796, six prompts 222 -> 305).  The
-// denominator sums the unrounded weights in fp32.
+// Weights enter O += P V in bf16.  Class 1, which waits for memory, takes each as two terms, the leading bits
+// and the rounded rest: off by 2^-15 of it.  (24 tokens at 3000 to 6000 positions: the second term's products are
+// hidden, its arithmetic takes 4 us of 91.)  Class 0 takes one, off by at most half a step, 2^-8, as the output
+// itself is after the division: there the tensor core and the softmax bound it, and the second term costs 40 % (a
+// chunk of 4096 tokens behind 12,288 positions 1276 us -> 1796, six prompts 222 -> 305).  The denominator sums the
+// unrounded weights in fp32.
 //
 // What bounds it.  Class 0: the chain of a set, from the S product's issue to its sight by the softmax 870
 // cycles (512 of the tensor core), softmax 1300 (64 scores a thread; arithmetic of two warps on one
@@ -977,14 +977,30 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     // Few rows: the loop is kept short instead, 16 columns at a time, loaded again for the weights (all
                     // roles' code runs in turns here and has to fit the instruction cache).
                     for (int j = 0; j < g.n; ++j) {
-                        const int see = limit - begin(j) - half * 64;
+                        // In a tile some row does not see all of, scores are masked in place first: the two loops do
+                        // without comparisons, which cost 4 to 8 % of every tile (24 tokens at 3000 to 6000 positions
+                        // 91.6 us, without them 85.6; 24 behind a common prompt, D = 64, 49.9 and 45.9).
+                        const int t0 = begin(j) + half * 64;
+                        if (limit_w - t0 < 64) {
+                            const int see = limit - t0;
+#pragma unroll 1
+                            for (int d = 0; d < 64; d += 16) {
+                                float x[16];
+                                uint32_t u[16];
+                                tc5_ld16(tS + half * 64 + d, x);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(d + i < see ? x[i] : -INFINITY);
+                                tc5_st16(tS + half * 64 + d, u);
+                            }
+                            tc5_wait_st();
+                        }
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int d = 0; d < 64; d += 16) {
                             float x[16];
                             tc5_ld16(tS + half * 64 + d, x);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) top = fmaxf(top, d + i < see ? x[i] : -INFINITY);
+                            for (int i = 0; i < 16; ++i) top = fmaxf(top, x[i]);
                         }
                         const float mc = agree(top, j);
                         const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
@@ -996,20 +1012,18 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                             // The weight as two bf16 terms, in the place of the 16 scores.  The first is cut off from a
                             // little less than the weight, so both are positive where it is: an infinite value times
                             // them stays that infinity (a second term of 0 or below would make it NaN).
-                            uint32_t w[8], w2[8];
+                            uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float2 y = make_float2(d + i < see ? x[i] : -INFINITY, d + i + 1 < see ? x[i + 1] : -INFINITY);
-                                const float2 a = __ffma2_rn(y, c2, mc2);
+                                const float2 a = __ffma2_rn(make_float2(x[i], x[i + 1]), c2, mc2);
                                 const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
                                 sum = __fadd2_rn(sum, e);
                                 const float2 h = __fmul2_rn(e, make_float2(1.f - 0x1p-16f, 1.f - 0x1p-16f));
                                 w[i / 2] = __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x7632);
                                 const float2 f = __ffma2_rn(make_float2(bf16_lo(w[i / 2]), bf16_hi(w[i / 2])), make_float2(-1.f, -1.f), e);
-                                w2[i / 2] = bf16x2_rn(f.x, f.y);
+                                w[8 + i / 2] = bf16x2_rn(f.x, f.y);
                             }
-                            tc5_st8(tS + half * 64 + d, w);
-                            tc5_st8(tS + half * 64 + d + 8, w2);
+                            tc5_st16(tS + half * 64 + d, w);
                         }
                         finish(sum, j);
                     }
