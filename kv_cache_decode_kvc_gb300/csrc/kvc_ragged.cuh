@@ -173,7 +173,8 @@ struct Ragged {
     // Cost units of a key tile and of a stream's start, by class.  (Measured with starts of 4, 6, 8 and 10 in
     // class 0: six prompts of 700 to 4096 tokens 221, 220, 227, 234 us; of 2, 3, 4 in class 1: 256 single tokens
     // with up to 500 positions behind 16,384 common ones 181, 153, 162 us, 200 with 350 behind as many 132,
-    // 139, 146; tiles of class 1 at 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
+    // 139, 146: where the cuts happen to fall weighs as much as what a start costs, 3 is a middle; tiles of class 1 at
+    // 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
     __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
     __host__ __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 6 : 3; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile

@@ -33,8 +33,8 @@
 // out, the segments' hand-over and the first products are code that has left the instruction cache.
 // Class 1, long streams: memory (24 single tokens at 3000 positions: a pair of 32 KB tiles per set every 6.9 k
 // cycles, 5.4 TB/s).  Class 1, streams of a tile or two: the roles' code, run in turns, exceeds the 32 KB
-// instruction cache (5200 misses per SM in 84 us at 256 tokens of 251 positions, no-instruction stalls ahead
-// of all but the waits), so a stream costs about 8 k cycles per set whatever it holds.
+// instruction cache (4700 misses per SM in 87 us at 256 tokens of 251 positions, no-instruction stalls ahead
+// of all but the waits): its 2048 streams of two tiles take the 304 sets some 20 k cycles each.
 //
 // Warps: 0 copies (TMA), 1 issues the products, 2 computes the split and walks the streams, 3 guards
 // masked values, 4-11 set 0 and 12-19 set 1 (four warps per half of the columns).  K and V tiles
