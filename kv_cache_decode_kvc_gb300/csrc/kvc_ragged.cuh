@@ -613,7 +613,9 @@ int launch_ragged_tc5(const RaggedParams& p, const CUtensorMap& q, const CUtenso
 // rest to the next turn, which a double would round.
 inline uint64_t rope_turns(double rate) {
     const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;  // 1 / (2 pi)
-    const double a = fabs(rate), p = a * hi, e = fma(a, hi, -p) + a * lo;
+    const double a = fabs(rate);
+    const volatile double rounded = a * hi;  // (volatile: not fused into the difference below where hosts have fma)
+    const double p = rounded, e = fma(a, hi, -p) + a * lo;
     const double pf = p - floor(p), ef = fmod(e, 1.0);  // both exact
     uint64_t t = (uint64_t)ldexp(pf, 64);
     if (ef < 0) t -= (uint64_t)ldexp(-ef, 64);
