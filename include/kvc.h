@@ -315,6 +315,41 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
                           int64_t pos_stride, const int32_t* block_table, const int32_t* cu_seqlens,
                           const int32_t* lens, int N, void* stream);
 
+/* The same append with norms: before the rotation each head of q (and of k) is divided by the root of its mean square
+ * and multiplied by weights,
+ *     y_d = x_d w_d / sqrt(mean_d x_d^2 + eps)   over all D dimensions, in fp32, not rounded in between.
+ * q_norm, k_norm: device [D] in the cache dtype, 16-byte aligned; NULL: that side is not normalised (q_norm needs q).
+ * eps is finite and >= 0.  rope = NULL: no rotation (positions are not looked at). */
+int kvc_paged_append_norm_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q_norm, const void* k_norm, float eps,
+                               const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                               int64_t pos_stride, const int32_t* block_table, const int32_t* cu_seqlens,
+                               const int32_t* lens, int N, void* stream);
+
+/* Reads positions back: row i of sequence b (T_b rows, packed as above) is position lens[b] - T_b + i of `layer`, its
+ * keys to k_out and its values to v_out ([N, H_kv, D] in the cache dtype, strides as above; either may be NULL).  Any
+ * paged handle; an 8-bit cache gives code * scale.  A row whose table entry is out of range (KVC_DEV_BAD_BLOCK), and
+ * the rows of a sequence with T_b > lens[b] or lens[b] > T_max (KVC_DEV_BAD_LENS), read as zeros; rows of padding
+ * stay as they are. */
+int kvc_paged_read(kvc_t h, int layer, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                   const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* lens, int N, void* stream);
+
+/* Paged cache held in 8 bits: per layer, K and V are pools of E4M3 codes [num_blocks, H_kv, block_size, D] (one byte
+ * each, kvc_layer_ptrs) with one fp32 scale per block and KV head [num_blocks, H_kv] (kvc_layer_scales), a power of
+ * two 2^e; value = code * scale.  dtype is that of q, k, v, out (bf16 or fp32); D in {64, 128, 256}.  Calls:
+ * kvc_paged_append_rope, kvc_paged_append_norm_rope, kvc_paged_read, kvc_paged_attn_ragged, kvc_paged_attn_shared (the
+ * others are KVC_EUNSUPPORTED).
+ *   - An append quantizes k (after norm and rotation, unrounded) and v.  Per block and head, with amax the largest finite
+ *     |x| of the new rows, it takes the smallest e >= -64 with amax <= 448 * 2^e, or the block's present e if that
+ *     is larger and the block holds earlier positions of the sequence.  code = E4M3(x / 2^e), to the nearest, ties to even
+ *     (values that would read back as infinite: the largest finite one).  Where e grows, the earlier positions'
+ *     codes become E4M3(code * 2^(old - new)): the same values but for those that fall below 2^-6 * 2^new, which
+ *     stay within 2^-9 * 2^new of what they were, however often that happens.  Infinite and NaN values are stored as NaN.
+ *   - So a block belongs to one sequence from its first new row on; other sequences may read whole shared blocks.
+ *   - Rotations of rot_dim a multiple of 16 (fp32: 8), else KVC_EUNSUPPORTED. */
+int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size, int B, int max_blocks, int H_q,
+                         int H_kv, int D, int dtype);
+
 /* Attention of the new tokens over the paged cache: row i of sequence b, head j sees positions
  * [0, lens[b] - T_b + i] (its own included; append first):
  *     out = softmax_t(q . K_t / sqrt(D)) V,   fp32 softmax and sums, rounded once.

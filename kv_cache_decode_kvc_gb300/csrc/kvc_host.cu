@@ -87,10 +87,6 @@ bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, i
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace kvc
-
-namespace {
-
 // 4-D map over a paged pool with D = 128 (rows of 256 bytes): dimensions (64 columns, 8 rows,
 // 2 column blocks, rows / 8 groups) with byte strides (256, 128, 2048) for dimensions 1..3, so
 // one box of box_rows / 8 groups lands in shared memory as [group][column block][8 rows][128 B]
@@ -106,6 +102,14 @@ bool make_paged_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int box_
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+bool make_pool_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int D, int box_rows) {
+    return D == 128 ? make_paged_tensor_map(map, base, rows, box_rows) : make_kv_tensor_map(map, base, rows, D, box_rows);
+}
+
+}  // namespace kvc
+
+namespace {
 
 // 2-D map over an int8 cache with D = 128 (rows of 128 bytes): boxes of 128 bytes x box_rows rows,
 // no swizzle (the kernel widens them to bf16 itself).
@@ -205,6 +209,7 @@ int attn_common(kvc_t h, int layer, const void* q, const void* k_new, const void
         if ((T_q & (T_q - 1)) != 0 || h->G * T_q > 32) return KVC_EUNSUPPORTED;
         if (h->paged || h->rolling || h->quant || kvc_math_path(h) == 2) return KVC_EUNSUPPORTED;
     }
+    if (h->quant && h->paged) return KVC_EUNSUPPORTED;               // (kvc_paged_attn_ragged reads it)
     if (h->quant && kvc_math_path(h) != 3) return KVC_EUNSUPPORTED;  // only tcgen05 reads int8
     if (layer < 0 || layer >= h->layers) return KVC_EINVAL;
     if ((k_new == nullptr) != (v_new == nullptr)) return KVC_EINVAL;
@@ -380,7 +385,9 @@ static int create_common(kvc_t* out, int layers, int B, int H_q, int H_kv, int D
     const int ces = quant ? 1 : es;
     uint64_t total = 0;
     if (!mul_ok(rows, 2ull * (uint64_t)layers * (uint64_t)D * (uint64_t)ces, &total)) return KVC_ERANGE;
-    const size_t scale_stride = quant ? (size_t)((rows + 63) / 64 * 64) : 0;  // floats, 256-B aligned
+    // scales: one per row, or per block and head of a paged cache (floats, 256-byte aligned)
+    const uint64_t nscales = paged ? rows / (uint64_t)bs : rows;
+    const size_t scale_stride = quant ? (size_t)((nscales + 63) / 64 * 64) : 0;
     const size_t codes_total = (size_t)total;
     total += 2ull * (uint64_t)layers * scale_stride * 4;
 
@@ -463,10 +470,10 @@ static int create_common(kvc_t* out, int layers, int B, int H_q, int H_kv, int D
                      make_f8_tensor_map(&m4[2], kb, rows, box_full) &&
                      make_q8_tensor_map(&m4[3], vb, rows, box_full);
             else if (paged)  // the tcgen05 kernel's paged variant (D = 128) reads 4-D boxes
-                ok = make_paged_tensor_map(&m4[0], kb, rows, box_small) &&
-                     make_paged_tensor_map(&m4[1], vb, rows, box_small) &&
-                     make_paged_tensor_map(&m4[2], kb, rows, box_full) &&
-                     make_paged_tensor_map(&m4[3], vb, rows, box_full);
+                ok = kvc::make_paged_tensor_map(&m4[0], kb, rows, box_small) &&
+                     kvc::make_paged_tensor_map(&m4[1], vb, rows, box_small) &&
+                     kvc::make_paged_tensor_map(&m4[2], kb, rows, box_full) &&
+                     kvc::make_paged_tensor_map(&m4[3], vb, rows, box_full);
             else if (D == 128)  // whole tiles (tcgen05 kernel only) in one 3-D copy per tensor
                 ok = kvc::make_kv_tensor_map(&m4[0], kb, rows, D, box_small) &&
                      kvc::make_kv_tensor_map(&m4[1], vb, rows, D, box_small) &&
@@ -481,7 +488,7 @@ static int create_common(kvc_t* out, int layers, int B, int H_q, int H_kv, int D
         h->tc_ok = ok;
         if (!ok) h->tmaps.clear();
     }
-    if (paged && dtype == KVC_BF16 && D == 64 && rows < (1ull << 31)) {
+    if (paged && !quant && dtype == KVC_BF16 && D == 64 && rows < (1ull << 31)) {
         h->rmaps.resize(2 * (size_t)layers);
         bool ok = true;
         for (int l = 0; l < layers && ok; ++l) {
@@ -568,6 +575,20 @@ int kvc_create_paged(kvc_t* out, int layers, int num_blocks, int block_size, int
                          max_blocks, num_blocks);
 }
 
+int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size, int B, int max_blocks, int H_q,
+                         int H_kv, int D, int dtype) {
+    if (!out) return KVC_EINVAL;
+    *out = nullptr;
+    if (num_blocks < 1 || max_blocks < 1 || H_kv < 1) return KVC_EINVAL;
+    if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128 && block_size != 256)
+        return KVC_EUNSUPPORTED;
+    if (D != 64 && D != 128 && D != 256) return KVC_EUNSUPPORTED;
+    // (kernels count a block's codes in 32 bits)
+    if ((int64_t)max_blocks * block_size >= (1ll << 31) || (int64_t)H_kv * block_size * D >= (1ll << 31)) return KVC_ERANGE;
+    return create_common(out, layers, B, H_q, H_kv, D, max_blocks * block_size, dtype, block_size, max_blocks, num_blocks,
+                         true, true);
+}
+
 int kvc_destroy(kvc_t h) {
     if (!h) return KVC_OK;
     int rc = KVC_OK;
@@ -588,6 +609,11 @@ uint64_t kvc_payload_bytes(kvc_t h, const int32_t* lens_host) {
     if (!h || !lens_host) return 0;
     uint64_t sum = 0;
     for (int b = 0; b < h->B; ++b) sum += (uint64_t)(lens_host[b] > 0 ? lens_host[b] : 0);
+    if (h->quant && h->paged) {  // codes, and a scale for each block begun
+        uint64_t blocks = 0;
+        for (int b = 0; b < h->B; ++b) blocks += lens_host[b] > 0 ? ((uint64_t)lens_host[b] + h->bs - 1) / h->bs : 0;
+        return 2ull * h->layers * h->H_kv * ((uint64_t)h->D * sum + 4 * blocks);
+    }
     const uint64_t row = h->quant ? (uint64_t)h->D + 4 : (uint64_t)h->D * h->es;  // int8: + scale
     return 2ull * h->layers * h->H_kv * row * sum;
 }
@@ -628,7 +654,7 @@ int kvc_set_math(kvc_t h, int mode) {
     if (mode >= 2 && !h->tc_ok) return KVC_EUNSUPPORTED;
     if (mode == 3 && h->D != 128) return KVC_EUNSUPPORTED;
     if (mode == 2 && (h->paged || h->rolling)) return KVC_EUNSUPPORTED;  // warp MMA: plain caches only
-    if (h->quant && mode != 0 && mode != 3) return KVC_EUNSUPPORTED;     // int8: tcgen05 only
+    if (h->quant && !h->paged && mode != 0 && mode != 3) return KVC_EUNSUPPORTED;  // int8: tcgen05 only
     h->math = mode;
     return KVC_OK;
 }
@@ -739,6 +765,7 @@ int kvc_paged_prefill_write(kvc_t h, int layer, const void* K, const void* V, in
                             const int32_t* block_table, const int32_t* lens, void* stream) {
     if (!h || !K || !V || !lens || !block_table) return KVC_EINVAL;
     if (!h->paged || layer < 0 || layer >= h->layers) return KVC_EINVAL;
+    if (h->quant) return KVC_EUNSUPPORTED;  // (kvc_paged_append_rope quantizes)
     if (T_in < 1 || T_in > h->T_max) return KVC_ERANGE;
     kvc::CopyParams p{};
     p.Kc = h->slab + (size_t)(2 * layer) * h->layer_bytes;
@@ -757,6 +784,7 @@ int kvc_paged_append(kvc_t h, int layer, const void* k_new, const void* v_new,
                      const int32_t* block_table, const int32_t* lens, void* stream) {
     if (!h || !k_new || !v_new || !lens || !block_table) return KVC_EINVAL;
     if (!h->paged || layer < 0 || layer >= h->layers) return KVC_EINVAL;
+    if (h->quant) return KVC_EUNSUPPORTED;  // (kvc_paged_append_rope quantizes)
     kvc::CopyParams p{};
     p.Kc = h->slab + (size_t)(2 * layer) * h->layer_bytes;
     p.Vc = h->slab + (size_t)(2 * layer + 1) * h->layer_bytes;

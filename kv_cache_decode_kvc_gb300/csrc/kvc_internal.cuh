@@ -187,6 +187,10 @@ constexpr int TC_FULL_ROWS = 128;
 // or base is not 16-byte aligned.
 bool make_kv_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int D, int box_rows);
 bool make_kv3_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int box_rows);
+// Block pools [num_blocks, H_kv, bs, D] of bf16: boxes of box_rows rows; 4-D with D = 128 (whole 8-row groups of
+// both column blocks), else as make_kv_tensor_map.
+bool make_paged_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int box_rows);
+bool make_pool_tensor_map(CUtensorMap* map, void* base, uint64_t rows, int D, int box_rows);
 // Packed bf16 query rows [N, H_q, D] (tokens ts elements apart): boxes of 64 columns x G heads x
 // `tokens` tokens, 128-byte swizzle; tokens from N on read as zero.
 bool make_q_tensor_map(CUtensorMap* map, const void* q, int N, int H_q, int D, int64_t ts, int G, int tokens);

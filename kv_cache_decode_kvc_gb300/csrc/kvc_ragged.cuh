@@ -635,6 +635,9 @@ struct RopeParams {
     const int32_t *positions, *table, *cu, *lens;
     uint32_t* err;
     int B, N, H_q, H_kv, D, bs, max_blocks, num_blocks, T_max;
+    const void *q_norm, *k_norm;  // [D] weights of the heads' norms, nullptr: not normalised
+    float eps;
+    float *Ksc, *Vsc;  // 8-bit cache: scales [num_blocks, H_kv] (Kc, Vc: E4M3 codes)
 };
 int launch_append_rope(int dtype, const RopeParams& p, const RopeTable& t, int sms, cudaStream_t s);
 

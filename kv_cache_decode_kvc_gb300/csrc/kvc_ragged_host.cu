@@ -6,6 +6,7 @@
 #include <new>
 
 #include "kvc_handle.cuh"
+#include "kvc_q8.cuh"
 #include "kvc_ragged.cuh"
 
 struct kvc_rope {
@@ -29,6 +30,8 @@ int on_device(const kvc_cache* h) {
 
 // The tensor-core kernel takes bf16 pools with D = 64 or 128 unless CUDA cores are asked for.
 bool ragged_tc5(const kvc_cache* h) {
+    if (h->quant)  // (widened pools of as many rows, with maps of their own)
+        return h->dtype == KVC_BF16 && h->math != 1 && h->D <= 128 && h->layer_bytes / h->D < (1ull << 31);
     return h->dtype == KVC_BF16 && h->math != 1 && (h->D == 128 ? h->tc_ok : !h->rmaps.empty());
 }
 // CTAs of the attention kernels at most: the tensor-core kernel fills an SM, two blocks of the
@@ -38,6 +41,9 @@ int ragged_p(const kvc_cache* h, bool tc5) { return h->ctas > 0 ? h->ctas : (tc5
 kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, bool tc5) {
     return kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h, tc5), tc5 ? 5 : 2, tc5 ? 128 : 64);
 }
+
+// Bytes of a widened pool (K or V) of an 8-bit cache's layer, which follow the ragged scratch.
+uint64_t widened(const kvc_cache* h) { return h->quant ? ((uint64_t)h->layer_bytes * h->es + 255) / 256 * 256 : 0; }
 
 int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* table,
                 const int32_t* cu, const int32_t* lens, int N, const int32_t* groups, const int32_t* prefix, int NG,
@@ -49,7 +55,8 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(ws, 256)) return KVC_EINVAL;
     const bool tc5 = ragged_tc5(h);
     const kvc::RaggedScratch sc = ragged_ws(h, N, NG, tc5);
-    if (ws_bytes < sc.total) return KVC_EINVAL;
+    const uint64_t wide = widened(h);
+    if (ws_bytes < sc.total + 2 * wide) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;
     kvc::RaggedParams p{};
@@ -86,6 +93,35 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.T_max = h->T_max;
     p.P = ragged_p(h, tc5);
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CUtensorMap wk, wv;
+    if (h->quant) {
+        kvc::Q8Widen x{};
+        x.Kc = p.K;
+        x.Vc = p.V;
+        x.Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
+        x.Vsc = x.Ksc + h->scale_stride;
+        x.K = w + sc.total;
+        x.V = w + sc.total + wide;
+        x.table = table;
+        x.cu = cu;
+        x.lens = lens;
+        x.B = h->B;
+        x.N = N;
+        x.H_kv = h->H_kv;
+        x.D = h->D;
+        x.bs = h->bs;
+        x.max_blocks = h->max_blocks;
+        x.num_blocks = h->num_blocks;
+        x.T_max = h->T_max;
+        p.K = x.K;
+        p.V = x.V;
+        const uint64_t rows = h->layer_bytes / h->D;
+        const int box = h->bs < 128 ? h->bs : 128;
+        if (tc5 && (!kvc::make_pool_tensor_map(&wk, x.K, rows, h->D, box) || !kvc::make_pool_tensor_map(&wv, x.V, rows, h->D, box)))
+            return KVC_ECUDA;
+        if (kvc::launch_widen(h->dtype, x, h->sms, st) != 0) return KVC_ECUDA;
+    }
     if (tc5) {
         // boxes of 64 query rows, and of as few as one token's
         CUtensorMap mq, m1;
@@ -93,10 +129,11 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
         if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G, 64 / h->G) ||
             !kvc::make_q_tensor_map(&m1, q, N, h->H_q, h->D, q_stride, h->G, few / h->G))
             return KVC_ECUDA;
+        if (h->quant) return kvc::launch_ragged_tc5(p, mq, m1, wk, wv, st) == 0 ? KVC_OK : KVC_ECUDA;
         const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
-        return kvc::launch_ragged_tc5(p, mq, m1, kv[0], kv[1], static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
+        return kvc::launch_ragged_tc5(p, mq, m1, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
     }
-    return kvc::launch_ragged_cc(h->dtype, p, static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
+    return kvc::launch_ragged_cc(h->dtype, p, st) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
 }  // namespace
@@ -134,18 +171,24 @@ int kvc_rope_destroy(kvc_rope_t r) {
     return KVC_OK;
 }
 
-int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, int64_t q_stride, void* q_out,
-                          int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                          const int32_t* positions, int64_t pos_stride, const int32_t* block_table,
-                          const int32_t* cu_seqlens, const int32_t* lens, int N, void* stream) {
-    if (!h || !rope || !block_table || !cu_seqlens || !lens || N < 1) return KVC_EINVAL;
-    if (!h->paged || layer < 0 || layer >= h->layers || rope->t.rot_dim > h->D) return KVC_EINVAL;
+int kvc_paged_append_norm_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q_norm, const void* k_norm, float eps,
+                               const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                               int64_t pos_stride, const int32_t* block_table, const int32_t* cu_seqlens,
+                               const int32_t* lens, int N, void* stream) {
+    if (!h || !block_table || !cu_seqlens || !lens || N < 1) return KVC_EINVAL;
+    if (!h->paged || layer < 0 || layer >= h->layers || (rope && rope->t.rot_dim > h->D)) return KVC_EINVAL;
+    if (!isfinite(eps) || eps < 0 || (q_norm && !q) || !aligned(q_norm, 16) || !aligned(k_norm, 16)) return KVC_EINVAL;
+    static const kvc::RopeTable still{};  // no rotation: no pairs
+    const kvc::RopeTable& t = rope ? rope->t : still;
+    // (the 8-bit cache's kernel takes pairs in whole 16-byte vectors)
+    if (h->quant && t.rot_dim % (32 / h->es) != 0) return KVC_EUNSUPPORTED;
     if ((q == nullptr) != (q_out == nullptr)) return KVC_EINVAL;
     const int64_t qrow = (int64_t)h->H_q * h->D, krow = (int64_t)h->H_kv * h->D;
     if (q && (!packed_ok(q, q_stride, qrow, h->es) || !packed_ok(q_out, q_out_stride, qrow, h->es))) return KVC_EINVAL;
     if (q && q == q_out && q_stride != q_out_stride) return KVC_EINVAL;
     if (!packed_ok(k, k_stride, krow, h->es) || !packed_ok(v, v_stride, krow, h->es)) return KVC_EINVAL;
-    if (positions && (!aligned(positions, 4) || (rope->t.n_axes > 1 && pos_stride < N && pos_stride != 0))) return KVC_EINVAL;
+    if (positions && (!aligned(positions, 4) || (t.n_axes > 1 && pos_stride < N && pos_stride != 0))) return KVC_EINVAL;
     if (!aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(lens, 4)) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;
@@ -175,15 +218,70 @@ int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, in
     p.max_blocks = h->max_blocks;
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;
-    return kvc::launch_append_rope(h->dtype, p, rope->t, h->sms, static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK
-                                                                                                        : KVC_ECUDA;
+    p.q_norm = q_norm;
+    p.k_norm = k_norm;
+    p.eps = eps;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (h->quant) {
+        p.Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
+        p.Vsc = p.Ksc + h->scale_stride;
+        return kvc::launch_append8(h->dtype, p, t, h->sms, s) == 0 ? KVC_OK : KVC_ECUDA;
+    }
+    return kvc::launch_append_rope(h->dtype, p, t, h->sms, s) == 0 ? KVC_OK : KVC_ECUDA;
+}
+
+int kvc_paged_append_rope(kvc_t h, int layer, kvc_rope_t rope, const void* q, int64_t q_stride, void* q_out,
+                          int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* positions, int64_t pos_stride, const int32_t* block_table,
+                          const int32_t* cu_seqlens, const int32_t* lens, int N, void* stream) {
+    if (!rope) return KVC_EINVAL;
+    return kvc_paged_append_norm_rope(h, layer, rope, nullptr, nullptr, 0.f, q, q_stride, q_out, q_out_stride, k, k_stride, v,
+                                      v_stride, positions, pos_stride, block_table, cu_seqlens, lens, N, stream);
+}
+
+int kvc_paged_read(kvc_t h, int layer, void* k_out, int64_t k_stride, void* v_out, int64_t v_stride,
+                   const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* lens, int N, void* stream) {
+    if (!h || !block_table || !cu_seqlens || !lens || N < 1 || (!k_out && !v_out)) return KVC_EINVAL;
+    if (!h->paged || layer < 0 || layer >= h->layers) return KVC_EINVAL;
+    const int64_t row = (int64_t)h->H_kv * h->D;
+    if ((k_out && !packed_ok(k_out, k_stride, row, h->es)) || (v_out && !packed_ok(v_out, v_stride, row, h->es)))
+        return KVC_EINVAL;
+    if (!aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(lens, 4)) return KVC_EINVAL;
+    // (kernels count the 16-byte pieces of a few rows in 32 bits)
+    if (row * h->es >= (int64_t(1) << 30)) return KVC_EUNSUPPORTED;
+    const int rc = on_device(h);
+    if (rc != KVC_OK) return rc;
+    kvc::Q8Read p{};
+    p.Kc = h->slab + (size_t)(2 * layer) * h->layer_bytes;
+    p.Vc = h->slab + (size_t)(2 * layer + 1) * h->layer_bytes;
+    if (h->quant) {
+        p.Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
+        p.Vsc = p.Ksc + h->scale_stride;
+    }
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.k_ts = k_stride;
+    p.v_ts = v_stride;
+    p.table = block_table;
+    p.cu = cu_seqlens;
+    p.lens = lens;
+    p.err = h->err;
+    p.B = h->B;
+    p.N = N;
+    p.H_kv = h->H_kv;
+    p.D = h->D;
+    p.bs = h->bs;
+    p.max_blocks = h->max_blocks;
+    p.num_blocks = h->num_blocks;
+    p.T_max = h->T_max;
+    return kvc::launch_paged_read(h->dtype, p, static_cast<cudaStream_t>(stream)) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes) {
     if (!h || !bytes || !h->paged || N < 1 || NG < 0 || NG > h->B) return KVC_EINVAL;
     // enough for either path, whatever kvc_set_math does in between
     const uint64_t a = ragged_ws(h, N, NG, true).total, b = ragged_ws(h, N, NG, false).total;
-    *bytes = a > b ? a : b;
+    *bytes = (a > b ? a : b) + 2 * widened(h);
     return KVC_OK;
 }
 

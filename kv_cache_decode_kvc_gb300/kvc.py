@@ -90,6 +90,10 @@ def load() -> ctypes.CDLL:
         "kvc_rope_create": (I, [ctypes.POINTER(P), I, P, I, I, P, ctypes.c_float]),
         "kvc_rope_destroy": (I, [P]),
         "kvc_paged_append_rope": (I, [P, I, P, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, P, I, P]),
+        "kvc_paged_append_norm_rope": (I, [P, I, P, P, P, ctypes.c_float, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, P,
+                                           I, P]),
+        "kvc_paged_read": (I, [P, I, P, I64, P, I64, P, P, P, I, P]),
+        "kvc_create_paged_fp8": (I, [ctypes.POINTER(P), I, I, I, I, I, I, I, I, I]),
         "kvc_paged_attn_ragged": (I, [P, I, P, I64, P, I64, P, P, P, I, P, U64, P]),
         "kvc_paged_attn_shared": (I, [P, I, P, I64, P, I64, P, P, P, I, P, P, I, P, U64, P]),
         "kvc_paged_attn_workspace": (I, [P, I, I, ctypes.POINTER(U64)]),
@@ -249,6 +253,13 @@ def kvc_create_paged(layers, num_blocks, block_size, B, max_blocks, H_q, H_kv, D
     return h.value
 
 
+def kvc_create_paged_fp8(layers, num_blocks, block_size, B, max_blocks, H_q, H_kv, D, dtype) -> int:
+    h = ctypes.c_void_p()
+    _check(load().kvc_create_paged_fp8(ctypes.byref(h), layers, num_blocks, block_size, B, max_blocks, H_q, H_kv, D,
+                                       dtype), "kvc_create_paged_fp8")
+    return h.value
+
+
 def kvc_paged_prefill_write(h, layer, K, V, T_in, block_table, lens, stream=None) -> None:
     _check(load().kvc_paged_prefill_write(h, layer, _ptr(K), _ptr(V), T_in, _ptr(block_table),
                                           _ptr(lens), _stream(stream)), "kvc_paged_prefill_write")
@@ -297,6 +308,19 @@ def kvc_paged_append_rope(h, layer, rope, q, q_stride, q_out, q_out_stride, k, k
                                         k_stride, _ptr(v), v_stride, _ptr(positions), pos_stride,
                                         _ptr(block_table), _ptr(cu_seqlens), _ptr(lens), N, _stream(stream)),
            "kvc_paged_append_rope")
+
+
+def kvc_paged_append_norm_rope(h, layer, rope, q_norm, k_norm, eps, q, q_stride, q_out, q_out_stride, k, k_stride, v,
+                               v_stride, positions, pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
+    _check(load().kvc_paged_append_norm_rope(h, layer, rope, _ptr(q_norm), _ptr(k_norm), eps, _ptr(q), q_stride,
+                                             _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                             _ptr(positions), pos_stride, _ptr(block_table), _ptr(cu_seqlens),
+                                             _ptr(lens), N, _stream(stream)), "kvc_paged_append_norm_rope")
+
+
+def kvc_paged_read(h, layer, k_out, k_stride, v_out, v_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
+    _check(load().kvc_paged_read(h, layer, _ptr(k_out), k_stride, _ptr(v_out), v_stride, _ptr(block_table),
+                                 _ptr(cu_seqlens), _ptr(lens), N, _stream(stream)), "kvc_paged_read")
 
 
 def kvc_paged_attn_ragged(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, ws, ws_bytes,
@@ -587,11 +611,13 @@ class PagedKVCache(KVCache):
         _index(lens, "lens", int32, self.B, dev=dev)
 
     def append_rope(self, layer, rope, q, k, v, block_table, cu_seqlens, lens, q_out=None, positions=None,
-                    stream=None):
+                    stream=None, q_norm=None, k_norm=None, norm_eps=1e-6):
         """Append packed new tokens: k [N, H_kv, D] rotated by `rope` and v as it is into the cache, q
         [N, H_q, D] rotated into q_out (None: in place; q None: append only).  Sequence b's tokens are
         rows cu_seqlens[b] .. cu_seqlens[b + 1], lens[b] counts its positions with them.  positions
-        int32 [n_axes, N] or, for one axis, [N] (None: the slot in the sequence)."""
+        int32 [n_axes, N] or, for one axis, [N] (None: the slot in the sequence).  q_norm, k_norm: weights [D]
+        of the heads' norms, x * w / sqrt(mean(x^2) + norm_eps) before the rotation (None: not normalised).
+        rope = None: no rotation."""
         dt = self.torch_dtype
         int32 = _torch.int32
         N, D, dev = k.shape[0], self.D, _device()
@@ -610,6 +636,8 @@ class PagedKVCache(KVCache):
         elif q_out is not None:
             raise ValueError("q_out without q")
         ps = 0
+        if positions is not None and rope is None:
+            raise ValueError("positions without a rotation")
         if positions is not None:
             if positions.dim() == 1 and rope.n_axes == 1:
                 positions = positions[None]
@@ -624,8 +652,30 @@ class PagedKVCache(KVCache):
         self._batch(block_table, cu_seqlens, lens, int32, dev)
         if stream is None:
             stream = _current_stream(dev)
+        if q_norm is not None or k_norm is not None or rope is None:
+            for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+                if t is not None and (tuple(t.shape) != (D,) or t.dtype != dt or not t.is_contiguous() or
+                                      t.get_device() != dev):
+                    raise ValueError(f"{what}: want contiguous [{D}] {dt} on the GPU (the current device), got "
+                                     f"{list(t.shape)} {t.dtype} on {t.device}")
+            kvc_paged_append_norm_rope(self.h, layer, None if rope is None else rope.r, q_norm, k_norm, norm_eps, q, qs,
+                                       q_out, qos, k, ks, v, vs, positions, ps, block_table, cu_seqlens, lens, N, stream)
+            return
         kvc_paged_append_rope(self.h, layer, rope.r, q, qs, q_out, qos, k, ks, v, vs, positions, ps, block_table,
                               cu_seqlens, lens, N, stream)
+
+    def read(self, layer, k_out, v_out, block_table, cu_seqlens, lens, stream=None):
+        """Positions back out of the cache: rows cu_seqlens[b] .. cu_seqlens[b + 1] of k_out and v_out
+        [N, H_kv, D] (one may be None) become sequence b's last positions before lens[b]."""
+        dev, outs = _device(), [t for t in (k_out, v_out) if t is not None]
+        if not outs or any(t.shape[0] != outs[0].shape[0] for t in outs):
+            raise ValueError("k_out, v_out: want one, or both with as many rows")
+        st = [0 if t is None else _packed(t, self.H_kv, self.D, self.torch_dtype, what, dev)
+              for t, what in ((k_out, "k_out"), (v_out, "v_out"))]
+        self._batch(block_table, cu_seqlens, lens, _torch.int32, dev)
+        if stream is None:
+            stream = _current_stream(dev)
+        kvc_paged_read(self.h, layer, k_out, st[0], v_out, st[1], block_table, cu_seqlens, lens, outs[0].shape[0], stream)
 
     def attn_workspace_bytes(self, N, groups=0) -> int:
         """Scratch bytes of attn_ragged (groups = 0) or attn_shared for N packed rows."""
@@ -663,6 +713,29 @@ class PagedKVCache(KVCache):
         _index(prefix_lens, "prefix_lens", _torch.int32, NG)
         kvc_paged_attn_shared(self.h, layer, q, qs, out, os_, block_table, cu_seqlens, lens, N, groups, prefix_lens,
                               NG, ws, nb, stream)
+
+
+class PagedFP8KVCache(PagedKVCache):
+    """Owns one paged handle held in 8 bits: per layer, E4M3 codes [num_blocks, H_kv, block_size, D] and a
+    power-of-two scale per block and KV head [num_blocks, H_kv] (fp32) for K and for V; q, out and new rows
+    have the given dtype.  append_rope quantizes, read gives the values back, attn_ragged and attn_shared
+    attend over them."""
+
+    def __init__(self, layers, num_blocks, block_size, B, max_blocks, H_q, H_kv, D, dtype="bf16"):
+        self.dtype_code = {"bf16": KVC_BF16, "f32": KVC_F32, KVC_BF16: KVC_BF16, KVC_F32: KVC_F32}[dtype]
+        self.layers, self.B, self.H_q, self.H_kv, self.D = layers, B, H_q, H_kv, D
+        self.num_blocks, self.block_size, self.max_blocks = num_blocks, block_size, max_blocks
+        self.T_max = max_blocks * block_size
+        self.h = kvc_create_paged_fp8(layers, num_blocks, block_size, B, max_blocks, H_q, H_kv, D, self.dtype_code)
+
+    def layer_views(self, layer):
+        """torch views (no copy): K codes, V codes (uint8 E4M3 bit patterns) and K scales, V scales (fp32)."""
+        import torch
+        kp, vp = kvc_layer_ptrs(self.h, layer)
+        ks, vs = kvc_layer_scales(self.h, layer)
+        shape = (self.num_blocks, self.H_kv, self.block_size, self.D)
+        return (_wrap_device(kp, shape, torch.uint8, self), _wrap_device(vp, shape, torch.uint8, self),
+                _wrap_device(ks, shape[:2], torch.float32, self), _wrap_device(vs, shape[:2], torch.float32, self))
 
 
 class RollingKVCache(KVCache):
