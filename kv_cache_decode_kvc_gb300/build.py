@@ -28,7 +28,8 @@ def _units():
              ("kvc_noalloc", "kvc_noalloc.cu", []), ("kvc_selftest", "kvc_selftest.cu", []),
              ("kvc_ragged_host", "kvc_ragged_host.cu", []), ("kvc_ragged", "kvc_ragged.cu", []),
              ("kvc_ragged_tc5", "kvc_ragged_tc5.cu", []),
-             ("kvc_rope", "kvc_rope.cu", []), ("kvc_append8", "kvc_append8.cu", [])]
+             ("kvc_rope", "kvc_rope.cu", []), ("kvc_append8", "kvc_append8.cu", []),
+             ("kvc_ragged_q8", "kvc_ragged_q8.cu", [])]
     for d in (64, 128, 256):
         units.append((f"kvc_decode_tc_d{d}", "kvc_decode_tc_inst.cu", [f"-DKVC_INST_D={d}"]))
     units.append(("kvc_decode_tc5_d128", "kvc_decode_tc5_inst.cu", ["-DKVC_TC5_MODE=0"]))

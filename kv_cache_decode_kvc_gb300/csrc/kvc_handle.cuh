@@ -25,12 +25,14 @@ struct kvc_cache {
                                      // maps of whole tiles for a contiguous D = 128 cache);
                                      // paged: K, V, K, V with min(bs, 128)-row boxes
     std::vector<CUtensorMap> rmaps;  // paged bf16 pools with D = 64: per layer K, V (2-D boxes of
-                                     // min(bs, 128) rows) for the ragged attention kernel
+                                     // min(bs, 128) rows) for the ragged attention kernel; paged
+                                     // 8-bit pools with D = 64 or 128: boxes of 128-byte rows
     bool paged;                      // K / V of a layer are pools [num_blocks, H_kv, bs, D]
     bool rolling;                    // T_max = window slots, position p in slot p mod T_max
     bool quant;                      // 8-bit codes + fp32 row scales (q, out, new rows in dtype)
     bool fp8;                        // the codes are E4M3 (else int8)
-    float* scales;                   // int8 cache: K / V row scales of layer l at 2l, 2l + 1
+    float* scales;                   // 8-bit cache: K / V scales of layer l at 2l, 2l + 1 (a row's, or a
+                                     // paged block's and head's)
     size_t scale_stride;             // floats between consecutive scale arrays (256-byte aligned)
     int bs, max_blocks, num_blocks;  // paged geometry (T_max = max_blocks * bs)
 };

@@ -10,6 +10,7 @@
 
 #include "../../include/kvc.h"
 #include "kvc_handle.cuh"
+#include "kvc_q8.cuh"
 
 namespace {
 
@@ -149,6 +150,7 @@ bool mul_ok(uint64_t a, uint64_t b, uint64_t* r) {
 
 // Which kernel computes the attention: 1 CUDA cores, 2 warp-level MMA, 3 tcgen05.
 int kvc_math_path(const kvc_cache* h) {
+    if (h->quant && h->paged) return h->rmaps.empty() || h->math == 1 ? 1 : 3;
     if (!h->tc_ok || h->math == 1) return 1;
     if (h->math == 2) return 2;
     if (h->math == 3) return 3;
@@ -451,7 +453,7 @@ static int create_common(kvc_t* out, int layers, int B, int H_q, int H_kv, int D
     // a paged pool is copied one block (at most 128 rows) per box
     const int box_small = paged ? (bs < kvc::TC_FULL_ROWS ? bs : kvc::TC_FULL_ROWS) : kvc::TC_BOX_ROWS;
     const int box_full = paged ? box_small : kvc::TC_FULL_ROWS;
-    if (dtype == KVC_BF16 && rows < (1ull << 31) && ((!paged && !quant) || D == 128)) {
+    if (dtype == KVC_BF16 && rows < (1ull << 31) && ((!paged && !quant) || D == 128) && !(paged && quant)) {
         h->tmaps.resize(4 * (size_t)layers);
         bool ok = true;
         for (int l = 0; l < layers && ok; ++l) {
@@ -497,6 +499,17 @@ static int create_common(kvc_t* out, int layers, int B, int H_q, int H_kv, int D
                  kvc::make_kv_tensor_map(&h->rmaps[2 * (size_t)l + 1], h->slab + (size_t)(2 * l + 1) * h->layer_bytes,
                                          rows, D, box_full);
         }
+        if (!ok) h->rmaps.clear();
+    }
+    if (paged && quant && dtype == KVC_BF16 && D <= 128 && rows / (128 / D) < (1ull << 31)) {
+        // 128-byte rows of one or two tokens, for the attention on the codes
+        h->rmaps.resize(2 * (size_t)layers);
+        bool ok = true;
+        const int box = kvc::q8_box(D, bs) / (128 / D);
+        for (int l = 0; l < layers && ok; ++l)
+            for (int kv = 0; kv < 2 && ok; ++kv)
+                ok = make_f8_tensor_map(&h->rmaps[2 * (size_t)l + kv], h->slab + (size_t)(2 * l + kv) * h->layer_bytes,
+                                        rows / (128 / D), box);
         if (!ok) h->rmaps.clear();
     }
     *out = h;
@@ -651,10 +664,15 @@ int kvc_get_ctas(kvc_t h) {
 
 int kvc_set_math(kvc_t h, int mode) {
     if (!h || mode < 0 || mode > 3) return KVC_EINVAL;
+    if (h->quant && h->paged) {  // on the codes, or on CUDA cores
+        if (mode == 2 || (mode == 3 && h->rmaps.empty())) return KVC_EUNSUPPORTED;
+        h->math = mode;
+        return KVC_OK;
+    }
     if (mode >= 2 && !h->tc_ok) return KVC_EUNSUPPORTED;
     if (mode == 3 && h->D != 128) return KVC_EUNSUPPORTED;
     if (mode == 2 && (h->paged || h->rolling)) return KVC_EUNSUPPORTED;  // warp MMA: plain caches only
-    if (h->quant && !h->paged && mode != 0 && mode != 3) return KVC_EUNSUPPORTED;  // int8: tcgen05 only
+    if (h->quant && mode != 0 && mode != 3) return KVC_EUNSUPPORTED;  // int8: tcgen05 only
     h->math = mode;
     return KVC_OK;
 }

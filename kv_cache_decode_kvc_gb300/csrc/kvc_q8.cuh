@@ -44,6 +44,13 @@ struct Q8Widen {
     int B, N, H_kv, D, bs, max_blocks, num_blocks, T_max;
 };
 
+// Attention on the codes (kvc_ragged_q8.cu; bf16, D = 64 or 128): maps of 128-byte rows (128 / D tokens) in boxes of
+// q8_box tokens, scratch for P = ctas an SM with 2 slots of `rows` rows.
+void q8_shape(int D, int G, int* rows, int* ctas);
+constexpr int q8_box(int D, int bs) { return bs < 16384 / D ? bs : 16384 / D; }
+int launch_ragged_q8(const RaggedParams& p, const float* Ksc, const float* Vsc, const CUtensorMap& k, const CUtensorMap& v,
+                     cudaStream_t s);
+
 // Launchers (kvc_append8.cu); each returns a cudaError_t.
 int launch_append8(int dtype, const RopeParams& p, const RopeTable& t, int sms, cudaStream_t s);
 int launch_paged_read(int dtype, const Q8Read& p, cudaStream_t s);

@@ -28,22 +28,32 @@ int on_device(const kvc_cache* h) {
     return dev == h->device ? KVC_OK : KVC_EINVAL;
 }
 
-// The tensor-core kernel takes bf16 pools with D = 64 or 128 unless CUDA cores are asked for.
-bool ragged_tc5(const kvc_cache* h) {
-    if (h->quant)  // (widened pools of as many rows, with maps of their own)
-        return h->dtype == KVC_BF16 && h->math != 1 && h->D <= 128 && h->layer_bytes / h->D < (1ull << 31);
-    return h->dtype == KVC_BF16 && h->math != 1 && (h->D == 128 ? h->tc_ok : !h->rmaps.empty());
+// Which kernel attends: on CUDA cores, on the tensor cores, or on the tensor cores and an 8-bit cache's codes.
+// CUDA cores take an 8-bit cache's blocks widened to its dtype.
+enum class Path { CC, TC5, Q8 };
+Path ragged_path(const kvc_cache* h) {
+    if (h->dtype != KVC_BF16 || h->math == 1) return Path::CC;
+    if (h->quant) return h->rmaps.empty() ? Path::CC : Path::Q8;
+    return (h->D == 128 ? h->tc_ok : !h->rmaps.empty()) ? Path::TC5 : Path::CC;
 }
 // CTAs of the attention kernels at most: the tensor-core kernel fills an SM, two blocks of the
 // CUDA-core kernel fit.
-int ragged_p(const kvc_cache* h, bool tc5) { return h->ctas > 0 ? h->ctas : (tc5 ? 1 : 2) * h->sms; }
-// Scratch of a path: the tensor-core kernel's CTAs hold five slots of 128 rows, the others' two of 64.
-kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, bool tc5) {
-    return kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h, tc5), tc5 ? 5 : 2, tc5 ? 128 : 64);
+int ragged_p(const kvc_cache* h, Path path) {
+    int rows, ctas = path == Path::TC5 ? 1 : 2;
+    if (path == Path::Q8) kvc::q8_shape(h->D, h->G, &rows, &ctas);
+    return h->ctas > 0 ? h->ctas : ctas * h->sms;
 }
-
+// Scratch of a path: the tensor-core kernel's CTAs hold five slots of 128 rows, the others' two of 64 (on codes:
+// of a tile's rows).
+kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, Path path) {
+    int rows = path == Path::TC5 ? 128 : 64, ctas;
+    if (path == Path::Q8) kvc::q8_shape(h->D, h->G, &rows, &ctas);
+    return kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h, path), path == Path::TC5 ? 5 : 2, rows);
+}
 // Bytes of a widened pool (K or V) of an 8-bit cache's layer, which follow the ragged scratch.
-uint64_t widened(const kvc_cache* h) { return h->quant ? ((uint64_t)h->layer_bytes * h->es + 255) / 256 * 256 : 0; }
+uint64_t widened(const kvc_cache* h, Path path) {
+    return h->quant && path == Path::CC ? ((uint64_t)h->layer_bytes * h->es + 255) / 256 * 256 : 0;
+}
 
 int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* table,
                 const int32_t* cu, const int32_t* lens, int N, const int32_t* groups, const int32_t* prefix, int NG,
@@ -53,9 +63,9 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     const int64_t row = (int64_t)h->H_q * h->D;
     if (!packed_ok(q, q_stride, row, h->es) || !packed_ok(out, out_stride, row, h->es)) return KVC_EINVAL;
     if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(ws, 256)) return KVC_EINVAL;
-    const bool tc5 = ragged_tc5(h);
-    const kvc::RaggedScratch sc = ragged_ws(h, N, NG, tc5);
-    const uint64_t wide = widened(h);
+    const Path path = ragged_path(h);
+    const kvc::RaggedScratch sc = ragged_ws(h, N, NG, path);
+    const uint64_t wide = widened(h, path);
     if (ws_bytes < sc.total + 2 * wide) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;
@@ -91,10 +101,14 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.max_blocks = h->max_blocks;
     p.num_blocks = h->num_blocks;
     p.T_max = h->T_max;
-    p.P = ragged_p(h, tc5);
+    p.P = ragged_p(h, path);
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    CUtensorMap wk, wv;
+    if (path == Path::Q8) {
+        const float* Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
+        const CUtensorMap* kv = &h->rmaps[2 * (size_t)layer];
+        return kvc::launch_ragged_q8(p, Ksc, Ksc + h->scale_stride, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
+    }
     if (h->quant) {
         kvc::Q8Widen x{};
         x.Kc = p.K;
@@ -116,20 +130,15 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
         x.T_max = h->T_max;
         p.K = x.K;
         p.V = x.V;
-        const uint64_t rows = h->layer_bytes / h->D;
-        const int box = h->bs < 128 ? h->bs : 128;
-        if (tc5 && (!kvc::make_pool_tensor_map(&wk, x.K, rows, h->D, box) || !kvc::make_pool_tensor_map(&wv, x.V, rows, h->D, box)))
-            return KVC_ECUDA;
         if (kvc::launch_widen(h->dtype, x, h->sms, st) != 0) return KVC_ECUDA;
     }
-    if (tc5) {
+    if (path == Path::TC5) {
         // boxes of 64 query rows, and of as few as one token's
         CUtensorMap mq, m1;
         const int few = h->G > 16 ? h->G : 16;
         if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G, 64 / h->G) ||
             !kvc::make_q_tensor_map(&m1, q, N, h->H_q, h->D, q_stride, h->G, few / h->G))
             return KVC_ECUDA;
-        if (h->quant) return kvc::launch_ragged_tc5(p, mq, m1, wk, wv, st) == 0 ? KVC_OK : KVC_ECUDA;
         const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
         return kvc::launch_ragged_tc5(p, mq, m1, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
     }
@@ -279,9 +288,13 @@ int kvc_paged_read(kvc_t h, int layer, void* k_out, int64_t k_stride, void* v_ou
 
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes) {
     if (!h || !bytes || !h->paged || N < 1 || NG < 0 || NG > h->B) return KVC_EINVAL;
-    // enough for either path, whatever kvc_set_math does in between
-    const uint64_t a = ragged_ws(h, N, NG, true).total, b = ragged_ws(h, N, NG, false).total;
-    *bytes = (a > b ? a : b) + 2 * widened(h);
+    // enough for every path, whatever kvc_set_math does in between
+    uint64_t most = 0;
+    for (const Path path : {Path::CC, h->quant ? Path::Q8 : Path::TC5}) {
+        const uint64_t n = ragged_ws(h, N, NG, path).total + 2 * widened(h, path);
+        if (n > most) most = n;
+    }
+    *bytes = most;
     return KVC_OK;
 }
 

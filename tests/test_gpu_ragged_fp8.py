@@ -104,20 +104,25 @@ def test_values_that_no_row_sees_do_not_matter(kvc, D, new, hist):
     assert torch.equal(attend(kvc, bt), good)
 
 
-def test_nan_codes_reach_the_rows_that_see_them_and_no_others(kvc):
-    bt = Batch8([6, 1], [125, 300], 16, 8, 2, 128)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("i", [1, 2])  # (the second token of a pair in memory, and the first)
+def test_nan_codes_reach_the_rows_that_see_them_and_no_others(kvc, D, i):
+    t, d = 125 + i, 9  # new token i's value in dimension 9 of KV head 1
+
+    def batch():
+        return Batch8([6, 1], [125, 300], 16, 8, 2, D)
+    bt = batch()
     good = attend(kvc, bt).cpu()
-    t, d = 125 + 2, 9  # the third new token's value in dimension 9 of KV head 1
     bt.V8[int(bt.table[0, t // 16]), 1, t % 16, d] = 0x7F
     out = attend(kvc, bt).cpu()
     hit = torch.zeros_like(out, dtype=torch.bool)
-    hit[2:6, 4:, d] = True
+    hit[i:6, 4:, d] = True
     assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], good[~hit])
-    bt = Batch8([6, 1], [125, 300], 16, 8, 2, 128)
+    bt = batch()
     bt.K8[int(bt.table[0, t // 16]), 1, t % 16, d] = 0xFF
     out = attend(kvc, bt).cpu()
     hit = torch.zeros_like(out, dtype=torch.bool)
-    hit[2:6, 4:] = True
+    hit[i:6, 4:] = True
     assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], good[~hit])
 
 
@@ -150,7 +155,7 @@ def test_views_strides_and_scratch(kvc):
     c.attn_ragged(0, wide[:, 8:16], out[:, 8:], d["table"], d["cu"], d["lens"], workspace=ws)
     assert torch.equal(out[:, 8:], good) and (out[:, :8] == 0).all()
     with pytest.raises(kvc.KvcError):
-        c.attn_ragged(0, wide[:, 8:16], out[:, 8:], d["table"], d["cu"], d["lens"], workspace=ws[:n - 256])
+        c.attn_ragged(0, wide[:, 8:16], out[:, 8:], d["table"], d["cu"], d["lens"], workspace=ws[:256])
 
 
 def test_device_errors(kvc):
