@@ -163,7 +163,8 @@ __host__ __device__ __forceinline__ unsigned ceil_sum(unsigned X, int lg) {
 // tensor-core kernel has them, and two workers per CTA for class 1; JOINT: the call has groups.
 // (A CTA starts with a cold instruction cache, where code costs several times its warm time:
 // the split's is kept short, and without groups their part is compiled out.)
-template <int LRT, int LKT, bool PAIRS, bool JOINT>
+// START: (without PAIRS) key tiles that a stream's start costs as much as.
+template <int LRT, int LKT, bool PAIRS, bool JOINT, int START = 1>
 struct Ragged {
     static constexpr int RT = 1 << LRT, KT = 1 << LKT;
     // scratch slots of a CTA: with PAIRS five of 128 rows (a shared stream's later piece takes 0-1,
@@ -176,7 +177,7 @@ struct Ragged {
     // 139, 146: where the cuts happen to fall weighs as much as what a start costs, 3 is a middle; tiles of class 1 at
     // 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
     __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
-    __host__ __device__ static constexpr int start_cost(int cl) { return !PAIRS ? 1 : cl == 0 ? 6 : 3; }
+    __host__ __device__ static constexpr int start_cost(int cl) { return !PAIRS ? START : cl == 0 ? 6 : 3; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at

@@ -8,12 +8,15 @@
 //   - S^T = K Q^T (A = a tile of codes, K-major, B = the rows): a query row is scaled by a power of two to
 //     [128, 256) and split into two codes, q = 2^e (t0 + t1 / 16).  Two 4-bit significands hold bf16's 8 bits:
 //     exact but for elements below 2^-13 of the row's largest (off by 2^-21 of that).  Each term has columns of its own.
-//   - O^T += V^T W (A = the same tile of V read MN-major, B = the weights): w_t = 2^{x_t - m} 2^{b_t} 2^{m - M + 7} as
-//     three codes, w = u0 + u1 / 16 + u2 / 256, of f16's 11 bits (off by half a step, 2^-11 of w, or 2^-18 absolute with
-//     the row's largest above 64, i.e. 2^-24 of it).  m >= max x_t and M >= max(x_t + b_t) are integers: all factors
-//     between references are exact.  The denominator sums 2^{x_t - m} in fp32.
+//   - O^T += V^T W (A = the same tile of V read MN-major, B = the weights): w_t = 2^{x_t - m} 2^{b_t} 2^{m - M + 8} as
+//     three E5M2 terms with columns of their own: the top byte of w in f16, that of what is left, and of what is
+//     then left, rounded: within 2^-9 of w.  (A byte mask and a subtraction each, where E4M3 terms took conversions,
+//     and E4M3's range left a weight 2 binades to grow and cut those below 2^-25 of the largest off; here 7, 2^-32.)
+//     m >= max x_t and M >= max(x_t + b_t) are integers: all factors between references are exact.  The
+//     denominator sums 2^{x_t - m} in fp32.
 // A thread is a key position (lane of S^T), its columns the rows.  The references are raised only if a weight
-// passes 2^8: per tile one vote over the four warps instead of a maximum over the positions.
+// passes 2^15: per tile one vote over the four warps instead of a maximum over the positions.
+// S has two places: the scores of the next tile are computed while this one's are weighed.
 //
 // D = 64: a 128-byte row of the tile holds two tokens, tile rows are token pairs.  The operand has columns for
 // either token of the pair (the other half of a query row's 128 bytes is 0), and of O^T, whose 128 rows are
@@ -30,12 +33,12 @@
 
 namespace kvc {
 
-// TOK tokens per 128-byte row (D = 128 / TOK), RT = 2^LRT query rows.  Up to 96 + 64 columns of tensor memory
+// TOK tokens per 128-byte row (D = 128 / TOK), RT = 2^LRT query rows.  Up to 2 64 + 96 columns of tensor memory
 // fit two CTAs an SM; D = 64 with 32 rows takes one.
 template <int TOK_, int LRT, bool JOINT>
 struct Q8Cfg {
     static constexpr int TOK = TOK_, D = 128 / TOK, RT = 1 << LRT, LKT = TOK == 2 ? 8 : 7, KT = 1 << LKT;
-    using R = Ragged<LRT, LKT, false, JOINT>;
+    using R = Ragged<LRT, LKT, false, JOINT, 3>;
     using Seg = typename R::Seg;
     static constexpr int CTAS = TOK * RT > 32 ? 1 : 2;  // an SM
     static constexpr int TILE = 128 * 128;
@@ -48,17 +51,17 @@ struct Q8Cfg {
     static constexpr int NSLOT = NSLOT_A > 12 ? 12 : NSLOT_A;
     static constexpr int SMEM = NSLOT * TILE + QBYTES + PBYTES + MISC;
     static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
-    static constexpr int OCOL = QROWS;  // S at columns 0 .., O behind
+    static constexpr int OCOL = 2 * QROWS;  // two places of S, then O
     static constexpr int NSEG = 4;      // segments known ahead (a power of two; see the copies)
     static constexpr int NSC = 8;       // tiles whose scales are held
     static constexpr int THREADS = 256;
-    static_assert(QROWS + PCOLS <= TMEM_COLS, "tensor memory");
+    static_assert(2 * QROWS + PCOLS <= TMEM_COLS, "tensor memory");
     static_assert(NSLOT >= 4 && NSLOT / 2 + 2 <= NSC, "ring");
     static_assert(NSLOT * TILE >= R::work_ints(MAX_B, MAX_B) * 4, "the split's arrays lie under the ring");
     static_assert(PBYTES >= RT * 64 * 4 || TOK == 1, "the halves' exchange lies in the weights' place");
     struct Misc {
         uint64_t full[12], empty[12];
-        uint64_t sfull, pfull, ofull, qfull, kfix, drain;
+        uint64_t sfull[2], kfix[2], pfull, odone, qfull, drain;
         uint64_t segfull[NSEG], segempty[NSEG];
         Seg seg[NSEG];
         float2 scale[NSC][16];  // (K, V) scales of a tile's boxes
@@ -70,6 +73,7 @@ struct Q8Cfg {
         float m[32], M[32], fo[32], fl[32];
         float2 red[4][32];
         uint32_t knan[2][4];  // (TOK = 2, of two tiles in turn) second tokens whose key has NaN codes
+        uint32_t over[2];  // (of two tiles in turn) groups of eight rows whose references have to be raised
         int nonfinite;  // NaN codes were taken out of V in this segment
         int abort;
         uint32_t tmem;
@@ -83,6 +87,32 @@ struct Q8Attn {
     const float *Ksc, *Vsc;
     int once;  // every tile is read by one CTA: it leaves L2 first
 };
+
+// Waits for a barrier's phase, for at most WAIT_LIMIT_NS (false: gave up, see mbar_wait).  The hardware holds the
+// thread for up to the hint: polls without one were a fifth of the kernel's instructions.
+__device__ __forceinline__ bool q8_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool q8_poll(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+    const uint64_t t0 = global_ns();
+    while (true) {
+        if (q8_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > WAIT_LIMIT_NS) {
+            *abort_flag = 1;
+            atomicOr(err, DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
 
 // ---- operands
 __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -160,20 +190,33 @@ __device__ __forceinline__ bool any_of(int id, int n, bool pred) {
         : "memory");
     return r != 0;
 }
-// f16 pairs <-> E4M3 pairs.
-__device__ __forceinline__ uint32_t e4m3x2_of(__half2 h) {
-    const __half2_raw r = *reinterpret_cast<const __half2_raw*>(&h);
-    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ __half2 half2_of(uint32_t c2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c2 & 0xFFFFu), __NV_E4M3);
-    return *reinterpret_cast<const __half2*>(&h);
-}
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_from(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 // Largest of a value over a warp, as an ordered integer.
 __device__ __forceinline__ float warp_max(float x) {
     const int i = __float_as_int(x), o = i >= 0 ? i : i ^ 0x7FFFFFFF;
     const int r = __reduce_max_sync(0xFFFFFFFFu, o);
     return __int_as_float(r >= 0 ? r : r ^ 0x7FFFFFFF);
+}
+// Eight values summed over the warp: each halving exchanges what the other half keeps, so lane i ends with sum i / 4.
+__device__ __forceinline__ float rows_of_warp(const float (&sum)[8], int lane) {
+    float h4[4], h2[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        const float keep = up ? sum[4 + i] : sum[i], give = up ? sum[i] : sum[4 + i];
+        h4[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        const float keep = up ? h4[2 + i] : h4[i], give = up ? h4[i] : h4[2 + i];
+        h2[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+    }
+    const bool up = lane & 4;
+    float v = (up ? h2[1] : h2[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? h2[0] : h2[1], 4);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+    return v + __shfl_xor_sync(0xFFFFFFFFu, v, 1);
 }
 // 0xFF in the bytes that are NaN codes (0x7F, 0xFF).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t u) {
@@ -201,7 +244,10 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = 1 << p.lgG;
     volatile int* ab = &M.abort;
-    auto wait_on = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, ab, p.err); };
+    auto wait_on = [&](uint64_t* bar, uint32_t parity) {
+        const uint32_t at = smem_addr(bar);
+        return q8_try(at, parity) || q8_poll(at, parity, ab, p.err);
+    };
     if (smem_addr(q8_smem) & 1023) {  // (the swizzled tiles need it; the declaration asks for it)
         if (tid == 0) atomicOr(p.err, DEV_WAIT_TIMEOUT);
         return;
@@ -211,11 +257,13 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
             mbar_init(&M.full[i], 1);
             mbar_init(&M.empty[i], 1);
         }
-        mbar_init(&M.sfull, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M.sfull[i], 1);
+            mbar_init(&M.kfix[i], 1);
+        }
         mbar_init(&M.pfull, 4);
-        mbar_init(&M.ofull, 1);
+        mbar_init(&M.odone, 1);
         mbar_init(&M.qfull, 4);
-        mbar_init(&M.kfix, 1);
         mbar_init(&M.drain, 1);
         for (int i = 0; i < C::NSEG; ++i) {
             mbar_init(&M.segfull[i], 1);
@@ -235,6 +283,8 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         const CUtensorMap* m = lane == 0 ? &tmK : &tmV;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
+    // (the merge's blocks wait for this grid's end in their places)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     typename R::Split sp;
     typename R::Walk wk;
@@ -312,7 +362,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
             return __ldg(p.table + (size_t)a.g.seq * p.max_blocks + (((unsigned)a.g.kv0 + a.j * C::KT + bt) >> p.lgbs));
         };
         auto scales_of = [&](const At& a, int e) {
-            if (!there(a)) return make_float2(0.f, 0.f);
+            if (!there(a)) return make_float2(1.f, 1.f);  // (-inf times it stays that)
             const int64_t at = (int64_t)((unsigned)e < (unsigned)p.num_blocks ? e : 0) * p.H_kv + a.g.h;
             return make_float2(__ldg(pa.Ksc + at), __ldg(pa.Vsc + at));
         };
@@ -358,21 +408,20 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 if (issued >= C::NSLOT) ok = __all_sync(ALL, lane != 0 || wait_on(&M.empty[slot], use & 1 ^ 1)) != 0;
                 if (!ok) break;
                 __syncwarp();
-                if (kv == 0) {
-                    // (the tile that had this place is done with: V of a later one has left the ring)
-                    if (lane < 16) M.scale[tile % C::NSC][lane] = sc;
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)(nbox * box_bytes));
-                __syncwarp();
-                ++issued;
+                // (the bytes may land before they are announced: the phase ends with lane 0's arrival, and V's comes
+                // behind the scales, which were looked up a tile ago)
                 if (lane < nbox)
                     tma_load_2d(ring_s + slot * C::TILE + lane * box_bytes, kv ? &tmV : &tmK, 0, row, &M.full[slot], policy);
+                if (kv == 1 && lane < 16) M.scale[tile % C::NSC][lane] = sc;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&M.full[slot], (uint32_t)(nbox * box_bytes));
+                ++issued;
                 if (++slot == C::NSLOT) {
                     slot = 0;
                     ++use;
                 }
             }
+            if (!ok) break;
             ++tile;
         }
     } else if (warp == 1) {
@@ -382,7 +431,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         const uint64_t dQ = smem_desc_sw128(smem_addr(qop), 16u, 1024u);
         const uint64_t dW = smem_desc_plain(smem_addr(wop), 128u, 2048u);
         const uint32_t tm = __shfl_sync(ALL, tmem, 0);
-        uint32_t item = 0, tile = 0;
+        uint32_t item = 0, tile = 0, fixes = 0;
         auto uni = [&](uint32_t x) { return __shfl_sync(ALL, x, 0); };
         bool ok = true;
         for (int s = 0; ok; ++s) {
@@ -397,28 +446,11 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
             const int Rp = nrow <= 8 ? 8 : nrow <= 16 ? 16 : 32;
             const int NS = 2 * TOK * Rp, NO = (3 * TOK * Rp + 15) & ~15;
             const uint32_t idS = uni((1u << 4) | ((uint32_t)(NS >> 3) << 17) | (8u << 24));
-            const uint32_t idO = uni((1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NO >> 3) << 17) | (8u << 24));
+            const uint32_t idO = uni((1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(NO >> 3) << 17) | (8u << 24));
             ok = __all_sync(ALL, wait_on(&M.qfull, s & 1)) != 0;
             for (int j = 0; ok && j <= n; ++j) {
-                if (j > 0) {
-                    // O^T (+)= V^T W of tile j - 1
-                    const uint32_t vs = (item - 1) % C::NSLOT;
-                    ok = __all_sync(ALL, wait_on(&M.pfull, (tile - 1) & 1) && wait_on(&M.full[vs], ((item - 1) / C::NSLOT) & 1));
-                    if (!ok) break;
-                    tc5_fence_after();
-                    const uint32_t va = uni((uint32_t)dV + vs * (C::TILE >> 4)), acc = uni(j > 1 ? 1u : 0u);
-                    if (q8_elect()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            q8_mma(tm + C::OCOL, va + k * 256, (uint32_t)(dV >> 32), (uint32_t)dW + k * 32, (uint32_t)(dW >> 32),
-                                   idO, k > 0 ? 1u : acc);
-                        tc5_commit(&M.empty[vs]);
-                        if (j == n) tc5_commit(&M.ofull);
-                    }
-                    __syncwarp();
-                }
                 if (j < n) {
-                    // S^T = K Q^T of tile j (the softmax has read the scores of the tile before)
+                    // S^T = K Q^T of tile j, into the place of the tile before the last, whose weights are in
                     const uint32_t ks = item % C::NSLOT;
                     ok = __all_sync(ALL, wait_on(&M.full[ks], (item / C::NSLOT) & 1)) != 0;
                     if (!ok) break;
@@ -440,22 +472,40 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                             }
                             fence_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&M.kfix);
+                            if (lane == 0) mbar_arrive(&M.kfix[fixes & 1]);
+                            ++fixes;
                         }
                     }
                     tc5_fence_after();
                     issued = 1;
-                    const uint32_t ka = uni((uint32_t)dK + ks * (C::TILE >> 4));
+                    const uint32_t ka = uni((uint32_t)dK + ks * (C::TILE >> 4)), at = uni(tm + (tile & 1) * C::QROWS);
                     if (q8_elect()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            q8_mma(tm, ka + k * 2, (uint32_t)(dK >> 32), (uint32_t)dQ + k * 2, (uint32_t)(dQ >> 32), idS, k > 0);
-                        tc5_commit(&M.sfull);
+                            q8_mma(at, ka + k * 2, (uint32_t)(dK >> 32), (uint32_t)dQ + k * 2, (uint32_t)(dQ >> 32), idS, k > 0);
+                        tc5_commit(&M.sfull[tile & 1]);
                         tc5_commit(&M.empty[ks]);
                     }
                     __syncwarp();
                     item += 2;
                     ++tile;
+                }
+                if (j > 0) {
+                    // O^T (+)= V^T W of tile j - 1
+                    const uint32_t back = j < n ? 2 : 1, vi = item + 1 - 2 * back, vs = vi % C::NSLOT;
+                    ok = __all_sync(ALL, wait_on(&M.pfull, (tile - back) & 1) && wait_on(&M.full[vs], (vi / C::NSLOT) & 1));
+                    if (!ok) break;
+                    tc5_fence_after();
+                    const uint32_t va = uni((uint32_t)dV + vs * (C::TILE >> 4)), acc = uni(j > 1 ? 1u : 0u);
+                    if (q8_elect()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            q8_mma(tm + C::OCOL, va + k * 256, (uint32_t)(dV >> 32), (uint32_t)dW + k * 32, (uint32_t)(dW >> 32),
+                                   idO, k > 0 ? 1u : acc);
+                        tc5_commit(&M.odone);
+                        tc5_commit(&M.empty[vs]);
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -463,23 +513,26 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         // ====================================================== softmax and output
         const int sw = warp - 4, r = tid - 128;  // tile row of this thread, and its lane of O^T
         const uint32_t lanes = (uint32_t)(sw * 32) << 16;
-        const uint32_t tS = tmem + lanes, tO = tmem + C::OCOL + lanes;
+        const uint32_t tS0 = tmem + lanes, tO = tmem + C::OCOL + lanes;
         const int own_par = TOK == 2 ? r >> 6 : 0, dim = r & (D - 1);
         const int my_row = 8 * (lane & 3) + (lane >> 2);  // the row whose denominator this lane sums
         auto sync4 = [&] { named_bar_sync(1, 128); };
         // The segment's rows as the operand of S (all four warps).
-        auto write_q = [&](const Seg& g, int s) {
-            constexpr int VPR = D / 8;  // 16-byte vectors of a row
+        constexpr int VPR = D / 8;  // 16-byte vectors of a row
+        auto load_q = [&](const Seg& g, int i) {
+            const int rr = i / VPR, v = i & (VPR - 1);
+            if (rr >= (g.ntok << p.lgG)) return make_uint4(0, 0, 0, 0);
+            return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        (int64_t)(g.row0 + (rr >> p.lgG)) * p.q_ts +
+                                                        (int64_t)(g.h * G + (rr & (G - 1))) * D) +
+                         v);
+        };
+        auto write_q = [&](const Seg& g, int s, uint4 x) {  // x: this thread's first vector
             const int nrow = g.ntok << p.lgG, Rp = nrow <= 8 ? 8 : nrow <= 16 ? 16 : 32;
 #pragma unroll 1
             for (int i = r; i < Rp * VPR; i += 128) {
                 const int rr = i / VPR, v = i & (VPR - 1);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (rr < nrow)
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                             (int64_t)(g.row0 + (rr >> p.lgG)) * p.q_ts +
-                                                             (int64_t)(g.h * G + (rr & (G - 1))) * D) +
-                              v);
+                if (i != r) x = load_q(g, i);
                 float f[8];
                 Elem<__nv_bfloat16>::unpack(x, f);
                 uint32_t top = 0;
@@ -493,7 +546,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 // the row's largest goes to [128, 256); a NaN takes an infinity's place (the row is NaN either way)
                 int e = (int)(top >> 23) - 127 - 7;
                 e = top == 0 ? 0 : e < -119 ? -119 : e;
-                if (v == 0) M.qs[s & 1][rr] = rr < nrow ? p.qscale * exp2i(e) : 0.f;
+                if (v == 0) M.qs[s & 1][rr] = rr < nrow ? p.qscale * exp2i(e) : 1.f;
                 uint32_t c0[4], c1[4];
                 const float down = exp2i(-e);
 #pragma unroll
@@ -533,17 +586,29 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         Seg g;
         g.n = 0;
         bool live = !any_of(1, 128, !fetch(0, g));
-        if (live && g.n > 0) write_q(g, 0);
+        if (live && g.n > 0) write_q(g, 0, load_q(g, r));
         for (int s = 0; live && g.n > 0; ++s) {
             const int nrow = g.ntok << p.lgG, Rp = nrow <= 8 ? 8 : nrow <= 16 ? 16 : 32;
             const float* qs = M.qs[s & 1];
-            float l = 0.f;  // of row my_row, this warp's positions
-            if (r == 0) M.nonfinite = 0;
+            // Denominators: of up to 8 rows, this thread's part of each; of more, row my_row's over the warp's positions.
+            float l = 0.f, ls[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ls[i] = 0.f;
+            const bool few = Rp == 8;
+            if (r == 0) M.nonfinite = M.over[0] = M.over[1] = 0;
             sync4();
-            bool ok = true;
+            bool ok = true, known = false;
+            Seg g2;  // the next segment, fetched with this one's last tile, and a vector of its rows
+            g2.n = 0;
+            uint4 x2 = make_uint4(0, 0, 0, 0);
             for (int j = 0; j < g.n; ++j, ++tile, item += 2) {
                 const int t0 = g.kv0 + j * C::KT;
-                ok = wait_on(&M.sfull, tile & 1) && ok;
+                if (j + 1 == g.n) {
+                    known = fetch(s + 1, g2);
+                    if (known && g2.n > 0) x2 = load_q(g2, r);
+                }
+                ok = wait_on(&M.sfull[tile & 1], (tile >> 1) & 1) && ok;
+                const uint32_t tS = tS0 + (tile & 1) * C::QROWS;
                 // The scales lie there with the tile's copies.  (V's barrier, whose place is held until this tile's
                 // product; K's may be two uses on by now, which its parity does not tell.)
                 const bool whole = g.lim0 - t0 >= C::KT;
@@ -551,13 +616,35 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 ok = wait_on(&M.full[vslot], ((item + 1) / C::NSLOT) & 1) && ok;
                 bool knan = false;  // (TOK = 2) this row's second token has a NaN key
                 if (TOK == 2 && !whole) {
-                    ok = wait_on(&M.kfix, fixes++ & 1) && ok;
+                    ok = wait_on(&M.kfix[fixes & 1], (fixes >> 1) & 1) && ok;
+                    ++fixes;
                     knan = (M.knan[tile & 1][r >> 5] >> (r & 31) & 1) != 0;
                 }
                 __syncwarp();
                 tc5_fence_after();
                 const float2 sc = M.scale[tile % C::NSC][(TOK * r) >> min(p.lgbs, C::LKT)];
-                // Score of row rr at token par, in log2 units; -inf where the row does not see it.
+                if (!whole) {
+                    // Scores of positions that a row does not see become -inf in their place.
+#pragma unroll 1
+                    for (int i = 0; i < TOK * Rp / 8; ++i) {
+                        const int par = TOK == 2 ? i & 1 : 0, c = i / TOK;
+                        const uint32_t at = tS + par * 2 * Rp + 8 * c;
+                        const unsigned t = (unsigned)t0 + TOK * r + par;
+                        float s0[8], s1[8];
+                        tm_ld8x2(at, at + Rp, s0, s1);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (TOK == 2 && par == 1 && knan) s0[k] = __uint_as_float(0x7FFFFFFFu);
+                            const bool see = t < (unsigned)g.sees((8 * c + k) >> p.lgG);
+                            s0[k] = see ? s0[k] : -INFINITY;
+                            s1[k] = see ? s1[k] : 0.f;
+                        }
+                        tm_st8(at, s0);
+                        tm_st8(at + Rp, s1);
+                    }
+                    tc5_wait_st();
+                }
+                // Scores of eight rows at token par, in log2 units.
                 auto scores = [&](int c, int par, float (&x)[8]) {
                     float s0[8], s1[8];
                     const uint32_t at = tS + par * 2 * Rp + 8 * c;
@@ -570,21 +657,14 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         x[i + 2] = fmaf(s1[i + 2], 0.0625f, s0[i + 2]) * (q4.z * sc.x);
                         x[i + 3] = fmaf(s1[i + 3], 0.0625f, s0[i + 3]) * (q4.w * sc.x);
                     }
-                    if (!whole) {
-                        const unsigned t = (unsigned)t0 + TOK * r + par;
-#pragma unroll
-                        for (int i = 0; TOK == 2 && i < 8; ++i)
-                            if (par == 1 && knan) x[i] = __uint_as_float(0x7FFFFFFFu);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (t >= (unsigned)g.sees((8 * c + i) >> p.lgG)) x[i] = -INFINITY;
-                    }
                 };
-                // References at or above everything in this tile, rounded up to integers; O and l follow.
-                auto raise = [&] {
+                // References of the rows 8 c .. of each bit c of `which` at or above everything in this tile, rounded up to
+                // integers; O and l follow.
+                auto raise = [&](uint32_t which) {
                     const float la = (float)((int)((__float_as_uint(sc.y) >> 23) & 0xFFu) - 127);
 #pragma unroll 1
                     for (int c = 0; c < Rp / 8; ++c) {
+                        if (!(which >> c & 1)) continue;
                         float top[8], x[8];
                         scores(c, 0, top);
 #pragma unroll
@@ -601,7 +681,8 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         }
                     }
                     sync4();
-                    if (r < Rp) {
+                    if (r < Rp && !(which >> (r >> 3) & 1)) M.fl[r] = 1.f;
+                    if (r < Rp && (which >> (r >> 3) & 1)) {
                         float m = j == 0 ? -INFINITY : M.m[r], MM = j == 0 ? -INFINITY : M.M[r];
                         const float m0 = m, M0 = MM;
 #pragma unroll
@@ -611,17 +692,24 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         }
                         M.m[r] = m;
                         M.M[r] = MM;
-                        M.mu[r] = m == -INFINITY ? 0.f : m;
-                        M.b[r] = m == -INFINITY ? 1.f : pow2_of(m - MM + 7.f);
+                        M.mu[r] = m == -INFINITY ? 0.f : -m;
+                        M.b[r] = m == -INFINITY ? 1.f : pow2_of(m - MM + 8.f);
                         M.fl[r] = m0 == -INFINITY || m == m0 ? 1.f : m0 - m < -126.f ? 0.f : pow2_of(m0 - m);
                         M.fo[r] = M0 == -INFINITY || MM == M0 ? 1.f : M0 - MM < -126.f ? 0.f : pow2_of(M0 - MM);
                     }
                     sync4();
-                    l *= my_row < Rp ? M.fl[my_row] : 1.f;
+                    if (few) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ls[i] *= M.fl[i];
+                    } else {
+                        l *= my_row < Rp ? M.fl[my_row] : 1.f;
+                    }
                     if (j > 0) {
+                        // (weigh has waited for the products into O so far)
 #pragma unroll 1
                         for (int k = 0; k < 3 * Rp / 8; ++k) {
                             const int row0 = (8 * k) % Rp;
+                            if (!(which >> (row0 >> 3) & 1)) continue;
                             const uint32_t at = tO + own_par * 3 * Rp + 8 * k;
                             float o[8];
                             tc5_ld8(at, o);
@@ -632,75 +720,79 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         tc5_wait_st();
                     }
                 };
-                // The tile's weights; their sums by row; whether one is too large for its codes.
-                auto weigh = [&](float& lt) {
-                    bool over = false;
-                    lt = 0.f;
+                // The tile's weights of those rows; their sums by row; the groups with one too large for its terms.  (Pairs of rows: two
+                // products or sums are one instruction.)
+                bool free_w = false;
+                float lt = 0.f;
+                float2 lts[4];
+                auto weigh = [&](uint32_t which) {
+                    uint32_t over = 0;
+                    const float2 a2 = make_float2(sc.y, sc.y), k2 = make_float2(sc.x, sc.x), s16 = make_float2(0.0625f, 0.0625f);
 #pragma unroll 1
                     for (int c = 0; c < Rp / 8; ++c) {
-                        float sum[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+                        if (!(which >> c & 1)) continue;
+                        __half2 top = __float2half2_rn(0.f);
+                        float2 sum[4];
 #pragma unroll
                         for (int par = 0; par < TOK; ++par) {
-                            float x[8];
-                            scores(c, par, x);
-                            float w[8];
+                            float s0[8], s1[8];
+                            const uint32_t at = tS + par * 2 * Rp + 8 * c;
+                            tm_ld8x2(at, at + Rp, s0, s1);
+                            float2 e[4];
 #pragma unroll
-                            for (int i = 0; i < 8; i += 4) {
-                                const float4 mu = *reinterpret_cast<const float4*>(M.mu + 8 * c + i);
-                                const float4 b4 = *reinterpret_cast<const float4*>(M.b + 8 * c + i);
-                                const float e0 = fast_exp2(x[i] - mu.x), e1 = fast_exp2(x[i + 1] - mu.y);
-                                const float e2 = fast_exp2(x[i + 2] - mu.z), e3 = fast_exp2(x[i + 3] - mu.w);
-                                sum[i] += e0;
-                                sum[i + 1] += e1;
-                                sum[i + 2] += e2;
-                                sum[i + 3] += e3;
-                                w[i] = e0 * sc.y * b4.x;
-                                w[i + 1] = e1 * sc.y * b4.y;
-                                w[i + 2] = e2 * sc.y * b4.z;
-                                w[i + 3] = e3 * sc.y * b4.w;
+                            for (int i = 0; i < 4; i += 2) {
+                                const float4 q4 = *reinterpret_cast<const float4*>(qs + 8 * c + 2 * i);
+                                const float4 m4 = *reinterpret_cast<const float4*>(M.mu + 8 * c + 2 * i);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int n = 2 * (i + k);
+                                    const float2 f = __fmul2_rn(k ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), k2);
+                                    const float2 x = __ffma2_rn(make_float2(s1[n], s1[n + 1]), s16, make_float2(s0[n], s0[n + 1]));
+                                    e[i + k] = __ffma2_rn(x, f, k ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
+                                }
                             }
                             uint32_t u[3][4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                over |= fmaxf(w[2 * i], w[2 * i + 1]) > 256.f;
-                                const __half2 sixteen = __float2half2_rn(16.f);
-                                __half2 h = __floats2half2_rn(w[2 * i], w[2 * i + 1]);
-                                u[0][i] = e4m3x2_of(h);
-                                h = __hmul2(__hsub2(h, half2_of(u[0][i])), sixteen);
-                                u[1][i] = e4m3x2_of(h);
-                                h = __hmul2(__hsub2(h, half2_of(u[1][i])), sixteen);
-                                u[2][i] = e4m3x2_of(h);
+                            for (int i = 0; i < 4; i += 2) {
+                                const float4 b4 = *reinterpret_cast<const float4*>(M.b + 8 * c + 2 * i);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int n = i + k;
+                                    e[n] = make_float2(fast_exp2(e[n].x), fast_exp2(e[n].y));
+                                    sum[n] = par == 0 ? e[n] : __fadd2_rn(sum[n], e[n]);
+                                    const float2 w = __fmul2_rn(e[n], __fmul2_rn(k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), a2));
+                                    __half2 h = __floats2half2_rn(w.x, w.y);
+                                    top = __hmax2(top, h);
+                                    u[0][n] = half2_bits(h);
+                                    h = __hsub2(h, half2_from(u[0][n] & 0xFF00FF00u));
+                                    u[1][n] = half2_bits(h);
+                                    h = __hsub2(h, half2_from(u[1][n] & 0xFF00FF00u));
+                                    u[2][n] = half2_bits(h) + 0x00800080u;
+                                }
+                            }
+                            if (!free_w) {  // the product of the tile before has read its weights
+                                ok = (tile == 0 || wait_on(&M.odone, (tile - 1) & 1)) && ok;
+                                free_w = true;
                             }
 #pragma unroll
                             for (int term = 0; term < 3; ++term) {
                                 const int col = (par * 3 + term) * Rp + 8 * c;
                                 *reinterpret_cast<uint2*>(wop + (col >> 4) * 2048 + r * 16 + (col & 8)) =
-                                    make_uint2(u[term][0] | u[term][1] << 16, u[term][2] | u[term][3] << 16);
+                                    make_uint2(__byte_perm(u[term][0], u[term][1], 0x7531), __byte_perm(u[term][2], u[term][3], 0x7531));
                             }
                         }
-                        // Over the warp's positions: each halving exchanges the rows that the other half keeps, so lane i
-                        // ends with row i / 4 of the eight, four lanes alike.
-                        float h4[4], h2[2];
+                        const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                        if (all.x + all.y > 0x1p60f ||
+                            __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(0x1p15f)))
+                            over |= 1u << c;
+                        if (few) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool up = lane & 16;
-                            const float keep = up ? sum[4 + i] : sum[i], give = up ? sum[i] : sum[4 + i];
-                            h4[i] = keep + __shfl_xor_sync(ALL, give, 16);
+                            for (int i = 0; i < 4; ++i) lts[i] = sum[i];
+                        } else {
+                            const float flat[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
+                            const float v = rows_of_warp(flat, lane);
+                            if ((lane & 3) == c) lt = v;
                         }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const bool up = lane & 8;
-                            const float keep = up ? h4[2 + i] : h4[i], give = up ? h4[i] : h4[2 + i];
-                            h2[i] = keep + __shfl_xor_sync(ALL, give, 8);
-                        }
-                        const bool up = lane & 4;
-                        float v = (up ? h2[1] : h2[0]) + __shfl_xor_sync(ALL, up ? h2[0] : h2[1], 4);
-                        v += __shfl_xor_sync(ALL, v, 2);
-                        v += __shfl_xor_sync(ALL, v, 1);
-                        over |= v > 0x1p60f;
-                        if ((lane & 3) == c) lt = v;
                     }
                     return over;
                 };
@@ -729,26 +821,36 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         if (found) M.nonfinite = 1;
                     }
                 }
-                float lt;
-                if (j == 0) raise();
-                if (any_of(1, 128, weigh(lt) && j > 0)) {
-                    raise();
-                    weigh(lt);
+                if (j == 0) raise(15);
+                const uint32_t over = weigh(15);
+                if (j > 0 && over) atomicOr(&M.over[j & 1], over);
+                if (any_of(1, 128, j > 0 && over)) {
+                    const uint32_t which = *(volatile uint32_t*)&M.over[j & 1];
+                    raise(which);
+                    weigh(which);
                 }
-                l += lt;
+                // (read by all before raise's barriers; the next tile's votes go to the other word)
+                if (r == 0) M.over[j & 1] = 0;
+                if (few) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ls[2 * i] += lts[i].x;
+                        ls[2 * i + 1] += lts[i].y;
+                    }
+                } else {
+                    l += lt;
+                }
                 fence_async_smem();
                 tc5_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&M.pfull);
             }
             // ---- the next segment's rows, while this one's last product runs
-            Seg g2;
-            g2.n = 0;
-            live = !any_of(1, 128, !fetch(s + 1, g2));
-            if (live && g2.n > 0) write_q(g2, s + 1);
+            live = !any_of(1, 128, !known);
+            if (live && g2.n > 0) write_q(g2, s + 1, x2);
             // ---- the segment's state: written out, or left as a piece
-            M.red[sw][my_row].x = l;
-            ok = wait_on(&M.ofull, s & 1) && ok;
+            M.red[sw][my_row].x = few ? rows_of_warp(ls, lane) : l;  // (few: lane i has row i / 4)
+            ok = wait_on(&M.odone, (tile - 1) & 1) && ok;
             __syncwarp();
             tc5_fence_after();
             ok = !any_of(1, 128, !ok);
@@ -765,7 +867,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 const uint32_t at = tO + own_par * 3 * Rp + 8 * c;
                 tm_ld8x3(at, at + Rp, at + 2 * Rp, o, o1, o2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(fmaf(o2[i], 0.0625f, o1[i]), 0.0625f, o[i]) * M.fo[8 * c + i];
+                for (int i = 0; i < 8; ++i) o[i] = (o[i] + (o1[i] + o2[i])) * M.fo[8 * c + i];
             };
             if constexpr (TOK == 2) {
                 if (own_par == 1) {
