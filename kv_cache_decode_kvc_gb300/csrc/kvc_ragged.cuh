@@ -163,9 +163,12 @@ __host__ __device__ __forceinline__ unsigned ceil_sum(unsigned X, int lg) {
 // tensor-core kernel has them, and two workers per CTA for class 1; JOINT: the call has groups.
 // (A CTA starts with a cold instruction cache, where code costs several times its warm time:
 // the split's is kept short, and without groups their part is compiled out.)
-// START: (without PAIRS) key tiles that a stream's start costs as much as.
-template <int LRT, int LKT, bool PAIRS, bool JOINT, int START = 1>
+// MANY > 0 (without PAIRS): entries with more query rows per head are class 0 of a tile's other cost; a CTA's worker
+// walks its part of class 0, then that of class 1.  (At most one of its streams is cut at the end and one at the
+// start: where class 0 ends in a CTA, it ends with a stream.)
+template <int LRT, int LKT, bool PAIRS, bool JOINT, int MANY = 0>
 struct Ragged {
+    static constexpr bool CLASSES = PAIRS || MANY > 0;
     static constexpr int RT = 1 << LRT, KT = 1 << LKT;
     // scratch slots of a CTA: with PAIRS five of 128 rows (a shared stream's later piece takes 0-1,
     // its first piece 2-3 and then ends the range; set 0: 0 and 2, set 1: 3 and 4)
@@ -176,20 +179,22 @@ struct Ragged {
     // with up to 500 positions behind 16,384 common ones 181, 153, 162 us, 200 with 350 behind as many 132,
     // 139, 146: where the cuts happen to fall weighs as much as what a start costs, 3 is a middle; tiles of class 1 at
     // 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
-    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : 1; }
-    __host__ __device__ static constexpr int start_cost(int cl) { return !PAIRS ? START : cl == 0 ? 6 : 3; }
+    // (MANY, the kernel on codes: a tile of 32 rows takes 2.2 us, one of up to 8 that comes from memory 1.3; a stream's
+    // start some three tiles of the latter.)
+    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : MANY > 0 ? (cl == 0 ? 5 : 3) : 1; }
+    __host__ __device__ static constexpr int start_cost(int cl) { return PAIRS ? (cl == 0 ? 6 : 3) : MANY > 0 ? 9 : 1; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at
     // 500 positions 26.5 against 31.3 with the smaller).
-    __device__ static int lg_min(int W0) { return !PAIRS ? 0 : W0 > 0 ? 3 : 2; }
+    __device__ static int lg_min(int W0) { return MANY > 0 ? 3 : !PAIRS ? 0 : W0 > 0 ? 3 : 2; }
     __device__ static int groups(const RaggedParams& p) { return JOINT ? p.NG : 0; }
     __device__ static Entry entry_of(const RaggedParams& p, int e) {
         if (JOINT && e < p.NG) return group_entry(p, e);
         return seq_entry<JOINT>(p, e - groups(p));
     }
     __host__ __device__ static int cls(const RaggedParams& p, const Entry& s) {
-        return PAIRS && ((int64_t)s.T << p.lgG) > PAIR_ROWS ? 0 : 1;
+        return CLASSES && ((int64_t)s.T << p.lgG) > (PAIRS ? PAIR_ROWS : MANY) ? 0 : 1;
     }
     // Key tiles of a stream of an entry with S0 keys of its own before its new tokens, whose
     // last row is new token t1 - 1: positions [pfx, pfx + S0 + t1).
@@ -307,7 +312,7 @@ struct Ragged {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t1 = __shfl_up_sync(0xFFFFFFFFu, x[1], o);
-                const int t0 = PAIRS ? __shfl_up_sync(0xFFFFFFFFu, x[0], o) : 0;
+                const int t0 = CLASSES ? __shfl_up_sync(0xFFFFFFFFu, x[0], o) : 0;
                 if (lane >= o) {
                     x[0] += t0;
                     x[1] += t1;
@@ -317,7 +322,7 @@ struct Ragged {
                 c[e + 1] = carry[0] + x[0];
                 c[NE + 1 + e + 1] = carry[1] + x[1];
             }
-            carry[0] += PAIRS ? __shfl_sync(0xFFFFFFFFu, x[0], 31) : 0;
+            carry[0] += CLASSES ? __shfl_sync(0xFFFFFFFFu, x[0], 31) : 0;
             carry[1] += __shfl_sync(0xFFFFFFFFu, x[1], 31);
             bad = __any_sync(0xFFFFFFFFu, bad);
         }

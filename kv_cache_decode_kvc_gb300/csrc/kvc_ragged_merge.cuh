@@ -183,7 +183,9 @@ __device__ __forceinline__ void merge_two(const RaggedParams& p, int r0, int ste
     }
 }
 
-constexpr int MERGE_SLICES = 8;
+// Blocks that share the rows of a cut: a slot's rows for the warps of each.
+template <class R>
+constexpr int MERGE_SLICES = R::SLOT_ROWS < 8 * MERGE_WARPS ? R::SLOT_ROWS / MERGE_WARPS : 8;
 // Without groups: block (c, y) takes the c-th possible cut; if a stream was cut there first, its
 // warps merge the rows of the stream's tile from row 8 y on, every 64th eight of them.  With many pieces
 // the blocks of all its cuts take its rows in turn, one by one.
@@ -206,17 +208,17 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const Ragg
         };
     };
     if (a.x == 2) {
-        constexpr int STEP = MERGE_SLICES * MERGE_WARPS;
+        constexpr int STEP = MERGE_SLICES<R> * MERGE_WARPS;
         for (int r = blockIdx.y * MERGE_WARPS + warp; r < b.x; r += MERGE_ILP * STEP)
             merge_two<T>(p, r, STEP, b.x, lane, out_of, at_row);
         return;
     }
     if (a.x > MERGE_WIDE) {
-        for (int r = b.z * MERGE_SLICES + blockIdx.y; r < b.x; r += (a.x - 1) * MERGE_SLICES)
+        for (int r = b.z * MERGE_SLICES<R> + blockIdx.y; r < b.x; r += (a.x - 1) * MERGE_SLICES<R>)
             merge_row_wide<T>(p, a.x, out_of(r), warp, lane, at_row(r));
         return;
     }
-    for (int r = blockIdx.y * MERGE_WARPS + warp; r < b.x; r += MERGE_SLICES * MERGE_WARPS)
+    for (int r = blockIdx.y * MERGE_WARPS + warp; r < b.x; r += MERGE_SLICES<R> * MERGE_WARPS)
         merge_store<T>(p, merge_pieces(p, a.x, 0, 1, lane, at_row(r)), out_of(r), lane);
 }
 
@@ -295,7 +297,7 @@ inline int launch_merge(const RaggedParams& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e;
     if constexpr (!JOINT) {
-        cfg.gridDim = dim3((unsigned)(R::SLOTS > 2 ? 3 * p.P : p.P), MERGE_SLICES);
+        cfg.gridDim = dim3((unsigned)(R::SLOTS > 2 ? 3 * p.P : p.P), MERGE_SLICES<R>);
         cfg.blockDim = dim3(MERGE_WARPS * 32);
         e = cudaLaunchKernelEx(&cfg, merge_cuts_kernel<T, R>, p);
     } else {

@@ -38,7 +38,7 @@ namespace kvc {
 template <int TOK_, int LRT, bool JOINT>
 struct Q8Cfg {
     static constexpr int TOK = TOK_, D = 128 / TOK, RT = 1 << LRT, LKT = TOK == 2 ? 8 : 7, KT = 1 << LKT;
-    using R = Ragged<LRT, LKT, false, JOINT, 3>;
+    using R = Ragged<LRT, LKT, false, JOINT, 8>;
     using Seg = typename R::Seg;
     static constexpr int CTAS = TOK * RT > 32 ? 1 : 2;  // an SM
     static constexpr int TILE = 128 * 128;
@@ -300,7 +300,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         // The block's cuts start out empty (the warp that leaves them empties them).
         if (lane < 6) p.cuts[6 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
         __syncwarp();
-        if (lane == 0) wk = R::walk(p, sp, work, blockIdx.x, 1);
+        if (lane < 2) wk = R::walk(p, sp, work, blockIdx.x, lane);  // class 0, then class 1
         fence_async_smem();  // (the split's arrays are overwritten by copies)
     }
     __syncthreads();
@@ -310,15 +310,25 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
 
     if (warp == 2) {
         // ====================================================== streams
-        if (lane == 0) {
-            for (int s = 0;; ++s) {
-                const Seg g = R::next_seg(p, wk);
-                if (s >= C::NSEG && !wait_on(&M.segempty[s % C::NSEG], (s / C::NSEG - 1) & 1)) break;
-                M.seg[s % C::NSEG] = g;
-                mbar_arrive(&M.segfull[s % C::NSEG]);
-                if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, 1, g);
-                if (g.n == 0) break;
+        // Lane 0 leaves the segments of class 0, then lane 1 those of class 1 and the end.
+        int s = 0;
+        bool ok = true;
+        for (int cl = 0; cl < 2; ++cl) {
+            if (lane == cl) {
+                while (ok) {
+                    const Seg g = R::next_seg(p, wk);
+                    if (g.n == 0 && cl == 0) break;
+                    if (s >= C::NSEG) ok = wait_on(&M.segempty[s % C::NSEG], (s / C::NSEG - 1) & 1);
+                    if (!ok) break;
+                    M.seg[s % C::NSEG] = g;
+                    mbar_arrive(&M.segfull[s % C::NSEG]);
+                    if (wk.cut) R::leave_cut(p, sp, wk, blockIdx.x, 1, g);
+                    if (g.n == 0) break;
+                    ++s;
+                }
             }
+            s = __shfl_sync(ALL, s, 0);
+            ok = __shfl_sync(ALL, ok, 0);
         }
     } else if (warp == 3) {
         if (M.valid) ragged_zero_rows<__nv_bfloat16, JOINT>(p, lane, 32);
