@@ -8,14 +8,14 @@
 //   - S^T = K Q^T (A = a tile of codes, K-major, B = the rows): a query row is scaled by a power of two to
 //     [128, 256) and split into two codes, q = 2^e (t0 + t1 / 16).  Two 4-bit significands hold bf16's 8 bits:
 //     exact but for elements below 2^-13 of the row's largest (off by 2^-21 of that).  Each term has columns of its own.
-//   - O^T += V^T W (A = the same tile of V read MN-major, B = the weights): w_t = 2^{x_t - m} 2^{b_t} 2^{m - M + 8} as
-//     three E5M2 terms with columns of their own: the top byte of w in f16, that of what is left, and of what is
-//     then left, rounded: within 2^-9 of w.  (A byte mask and a subtraction each, where E4M3 terms took conversions,
-//     and E4M3's range left a weight 2 binades to grow and cut those below 2^-25 of the largest off; here 7, 2^-32.)
-//     m >= max x_t and M >= max(x_t + b_t) are integers: all factors between references are exact.  The
-//     denominator sums 2^{x_t - m} in fp32.
+//   - O^T += V^T W (A = the same tile of V read MN-major, B = the weights): w_t = 2^{x_t - m} 2^{b_t} 2^{m - M + 4} as
+//     three E5M2 terms with columns of their own, w = u0 + u1 / 8 + u2 / 64: the top byte of w in f16, that of 8 times what
+//     is left, and of 8 times what is then left, rounded: within 2^-9 of w, or 2^-23 absolute with the row's largest
+//     above 2^3.  (A byte mask, a subtraction and a product each; E4M3 terms took conversions, and a weight had 2 binades
+//     to grow until its reference had to be raised, here 10.)  m >= max x_t and M >= max(x_t + b_t) are integers: all
+//     factors between references are exact.  The denominator sums 2^{x_t - m} in fp32.
 // A thread is a key position (lane of S^T), its columns the rows.  The references are raised only if a weight
-// passes 2^15: per tile one vote over the four warps instead of a maximum over the positions.
+// passes 2^14: per tile one vote over the four warps instead of a maximum over the positions.
 // S has two places: the scores of the next tile are computed while this one's are weighed.
 //
 // D = 64: a 128-byte row of the tile holds two tokens, tile rows are token pairs.  The operand has columns for
@@ -88,23 +88,13 @@ struct Q8Attn {
     int once;  // every tile is read by one CTA: it leaves L2 first
 };
 
-// Waits for a barrier's phase, for at most WAIT_LIMIT_NS (false: gave up, see mbar_wait).  The hardware holds the
-// thread for up to the hint: polls without one were a fifth of the kernel's instructions.
-__device__ __forceinline__ bool q8_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
-}
-__device__ __noinline__ bool q8_poll(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+// Polls a barrier until the phase has completed, for at most WAIT_LIMIT_NS (false: gave up, see mbar_wait); ns: sleep
+// between polls.
+__device__ __noinline__ bool q8_poll(uint64_t* bar, uint32_t parity, uint32_t ns, volatile int* abort_flag, uint32_t* err) {
     const uint64_t t0 = global_ns();
     while (true) {
-        if (q8_try(bar, parity)) return true;
+        if (ns) __nanosleep(ns);
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (global_ns() - t0 > WAIT_LIMIT_NS) {
             *abort_flag = 1;
@@ -198,6 +188,12 @@ __device__ __forceinline__ float warp_max(float x) {
     const int r = __reduce_max_sync(0xFFFFFFFFu, o);
     return __int_as_float(r >= 0 ? r : r ^ 0x7FFFFFFF);
 }
+// The smaller of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // Eight values summed over the warp: each halving exchanges what the other half keeps, so lane i ends with sum i / 4.
 __device__ __forceinline__ float rows_of_warp(const float (&sum)[8], int lane) {
     float h4[4], h2[2];
@@ -244,9 +240,8 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = 1 << p.lgG;
     volatile int* ab = &M.abort;
-    auto wait_on = [&](uint64_t* bar, uint32_t parity) {
-        const uint32_t at = smem_addr(bar);
-        return q8_try(at, parity) || q8_poll(at, parity, ab, p.err);
+    auto wait_on = [&](uint64_t* bar, uint32_t parity, uint32_t ns = 0) {
+        return mbar_try_wait(bar, parity) || q8_poll(bar, parity, ns, ab, p.err);
     };
     if (smem_addr(q8_smem) & 1023) {  // (the swizzled tiles need it; the declaration asks for it)
         if (tid == 0) atomicOr(p.err, DEV_WAIT_TIMEOUT);
@@ -318,7 +313,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 while (ok) {
                     const Seg g = R::next_seg(p, wk);
                     if (g.n == 0 && cl == 0) break;
-                    if (s >= C::NSEG) ok = wait_on(&M.segempty[s % C::NSEG], (s / C::NSEG - 1) & 1);
+                    if (s >= C::NSEG) ok = wait_on(&M.segempty[s % C::NSEG], (s / C::NSEG - 1) & 1, 500);
                     if (!ok) break;
                     M.seg[s % C::NSEG] = g;
                     mbar_arrive(&M.segfull[s % C::NSEG]);
@@ -600,11 +595,14 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         for (int s = 0; live && g.n > 0; ++s) {
             const int nrow = g.ntok << p.lgG, Rp = nrow <= 8 ? 8 : nrow <= 16 ? 16 : 32;
             const float* qs = M.qs[s & 1];
-            // Denominators: of up to 8 rows, this thread's part of each; of more, row my_row's over the warp's positions.
-            float l = 0.f, ls[8];
+            // Denominators: this thread's part of each row, and of row my_row what raises have added up over the warp.
+            constexpr int NG8 = C::RT / 8;  // groups of eight rows
+            float l = 0.f;
+            float2 ls[NG8][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ls[i] = 0.f;
-            const bool few = Rp == 8;
+            for (int c = 0; c < NG8; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ls[c][i] = make_float2(0.f, 0.f);
             if (r == 0) M.nonfinite = M.over[0] = M.over[1] = 0;
             sync4();
             bool ok = true, known = false;
@@ -703,19 +701,14 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         M.m[r] = m;
                         M.M[r] = MM;
                         M.mu[r] = m == -INFINITY ? 0.f : -m;
-                        M.b[r] = m == -INFINITY ? 1.f : pow2_of(m - MM + 8.f);
+                        M.b[r] = m == -INFINITY ? 1.f : pow2_of(m - MM + 4.f);
                         M.fl[r] = m0 == -INFINITY || m == m0 ? 1.f : m0 - m < -126.f ? 0.f : pow2_of(m0 - m);
                         M.fo[r] = M0 == -INFINITY || MM == M0 ? 1.f : M0 - MM < -126.f ? 0.f : pow2_of(M0 - MM);
                     }
                     sync4();
-                    if (few) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) ls[i] *= M.fl[i];
-                    } else {
-                        l *= my_row < Rp ? M.fl[my_row] : 1.f;
-                    }
+                    l *= my_row < Rp ? M.fl[my_row] : 1.f;
                     if (j > 0) {
-                        // (weigh has waited for the products into O so far)
+                        // (the weights' first writes have waited for the products into O so far)
 #pragma unroll 1
                         for (int k = 0; k < 3 * Rp / 8; ++k) {
                             const int row0 = (8 * k) % Rp;
@@ -730,81 +723,58 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         tc5_wait_st();
                     }
                 };
-                // The tile's weights of those rows; their sums by row; the groups with one too large for its terms.  (Pairs of rows: two
-                // products or sums are one instruction.)
+                // Eight rows' weights: their terms into the operand, each pair of rows'
+                // 2^{x - m}, added to `sum`, and whether a weight is too large for its terms.  (Pairs of rows: two
+                // products or sums are one instruction.  2^{x - m} is held below 2^60, where it stays finite until a
+                // raise has taken it out again.)
                 bool free_w = false;
-                float lt = 0.f;
-                float2 lts[4];
-                auto weigh = [&](uint32_t which) {
-                    uint32_t over = 0;
+                auto weigh = [&](int c, float2 (&sum)[4]) {
+                    __half2 top = __float2half2_rn(0.f);
+                    const __half2 eight = __float2half2_rn(8.f);
                     const float2 a2 = make_float2(sc.y, sc.y), k2 = make_float2(sc.x, sc.x), s16 = make_float2(0.0625f, 0.0625f);
-#pragma unroll 1
-                    for (int c = 0; c < Rp / 8; ++c) {
-                        if (!(which >> c & 1)) continue;
-                        __half2 top = __float2half2_rn(0.f);
-                        float2 sum[4];
 #pragma unroll
-                        for (int par = 0; par < TOK; ++par) {
-                            float s0[8], s1[8];
-                            const uint32_t at = tS + par * 2 * Rp + 8 * c;
-                            tm_ld8x2(at, at + Rp, s0, s1);
-                            float2 e[4];
+                    for (int par = 0; par < TOK; ++par) {
+                        float s0[8], s1[8];
+                        const uint32_t at = tS + par * 2 * Rp + 8 * c;
+                        tm_ld8x2(at, at + Rp, s0, s1);
+                        uint32_t u[3][4];
 #pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                const float4 q4 = *reinterpret_cast<const float4*>(qs + 8 * c + 2 * i);
-                                const float4 m4 = *reinterpret_cast<const float4*>(M.mu + 8 * c + 2 * i);
+                        for (int i = 0; i < 4; i += 2) {
+                            const float4 q4 = *reinterpret_cast<const float4*>(qs + 8 * c + 2 * i);
+                            const float4 m4 = *reinterpret_cast<const float4*>(M.mu + 8 * c + 2 * i);
+                            const float4 b4 = *reinterpret_cast<const float4*>(M.b + 8 * c + 2 * i);
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int n = 2 * (i + k);
-                                    const float2 f = __fmul2_rn(k ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), k2);
-                                    const float2 x = __ffma2_rn(make_float2(s1[n], s1[n + 1]), s16, make_float2(s0[n], s0[n + 1]));
-                                    e[i + k] = __ffma2_rn(x, f, k ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
-                                }
-                            }
-                            uint32_t u[3][4];
-#pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                const float4 b4 = *reinterpret_cast<const float4*>(M.b + 8 * c + 2 * i);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int n = i + k;
-                                    e[n] = make_float2(fast_exp2(e[n].x), fast_exp2(e[n].y));
-                                    sum[n] = par == 0 ? e[n] : __fadd2_rn(sum[n], e[n]);
-                                    const float2 w = __fmul2_rn(e[n], __fmul2_rn(k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), a2));
-                                    __half2 h = __floats2half2_rn(w.x, w.y);
-                                    top = __hmax2(top, h);
-                                    u[0][n] = half2_bits(h);
-                                    h = __hsub2(h, half2_from(u[0][n] & 0xFF00FF00u));
-                                    u[1][n] = half2_bits(h);
-                                    h = __hsub2(h, half2_from(u[1][n] & 0xFF00FF00u));
-                                    u[2][n] = half2_bits(h) + 0x00800080u;
-                                }
-                            }
-                            if (!free_w) {  // the product of the tile before has read its weights
-                                ok = (tile == 0 || wait_on(&M.odone, (tile - 1) & 1)) && ok;
-                                free_w = true;
-                            }
-#pragma unroll
-                            for (int term = 0; term < 3; ++term) {
-                                const int col = (par * 3 + term) * Rp + 8 * c;
-                                *reinterpret_cast<uint2*>(wop + (col >> 4) * 2048 + r * 16 + (col & 8)) =
-                                    make_uint2(__byte_perm(u[term][0], u[term][1], 0x7531), __byte_perm(u[term][2], u[term][3], 0x7531));
+                            for (int k = 0; k < 2; ++k) {
+                                const int n = i + k;
+                                const float2 f = __fmul2_rn(k ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), k2);
+                                float2 e = __ffma2_rn(make_float2(s1[2 * n], s1[2 * n + 1]), s16, make_float2(s0[2 * n], s0[2 * n + 1]));
+                                e = __ffma2_rn(e, f, k ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
+                                e = make_float2(fast_exp2(min_nan(e.x, 60.f)), fast_exp2(min_nan(e.y, 60.f)));
+                                sum[n] = __fadd2_rn(sum[n], e);
+                                const float2 w = __fmul2_rn(e, __fmul2_rn(k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), a2));
+                                __half2 h = __floats2half2_rn(w.x, w.y);
+                                top = __hmax2(top, h);
+                                u[0][n] = half2_bits(h);
+                                h = __hmul2(__hsub2(h, half2_from(u[0][n] & 0xFF00FF00u)), eight);
+                                u[1][n] = half2_bits(h);
+                                h = __hmul2(__hsub2(h, half2_from(u[1][n] & 0xFF00FF00u)), eight);
+                                u[2][n] = half2_bits(h) + 0x00800080u;
                             }
                         }
-                        const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-                        if (all.x + all.y > 0x1p60f ||
-                            __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(0x1p15f)))
-                            over |= 1u << c;
-                        if (few) {
+                        if (!free_w) {  // the product of the tile before has read its weights
+                            ok = (tile == 0 || wait_on(&M.odone, (tile - 1) & 1)) && ok;
+                            free_w = true;
+                        }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) lts[i] = sum[i];
-                        } else {
-                            const float flat[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
-                            const float v = rows_of_warp(flat, lane);
-                            if ((lane & 3) == c) lt = v;
+                        for (int term = 0; term < 3; ++term) {
+                            const int col = (par * 3 + term) * Rp + 8 * c;
+                            *reinterpret_cast<uint2*>(wop + (col >> 4) * 2048 + r * 16 + (col & 8)) =
+                                make_uint2(__byte_perm(u[term][0], u[term][1], 0x7531), __byte_perm(u[term][2], u[term][3], 0x7531));
                         }
                     }
-                    return over;
+                    // (a sum of 2^59 is one whose value may have been held, or soon: that row's m is raised too)
+                    const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                    return all.x + all.y > 0x1p59f || __hgt(__hmax(__low2half(top), __high2half(top)), __float2half_rn(0x1p14f));
                 };
                 if (!whole) {
                     // A weight of 0 times NaN is NaN: V of tokens behind the end (stale, or never loaded) is zeroed, and
@@ -831,25 +801,49 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                         if (found) M.nonfinite = 1;
                     }
                 }
-                if (j == 0) raise(15);
-                const uint32_t over = weigh(15);
+                if (j == 0) raise((1u << NG8) - 1);
+                uint32_t over = 0;
+                auto weigh_all = [&](auto groups) {
+#pragma unroll
+                    for (int c = 0; c < decltype(groups)::value; ++c)
+                        if (weigh(c, ls[c])) over |= 1u << c;
+                };
+                if (Rp == 8) weigh_all(std::integral_constant<int, 1>{});
+                else if (Rp == 16) weigh_all(std::integral_constant<int, 2>{});
+                else if constexpr (C::RT == 32) weigh_all(std::integral_constant<int, 4>{});
                 if (j > 0 && over) atomicOr(&M.over[j & 1], over);
                 if (any_of(1, 128, j > 0 && over)) {
+                    // The groups' sums go to l, this tile's are taken out of them (their size is at most that of the sums to come,
+                    // and so is what rounding leaves of them), the references raised, the weights computed again.
                     const uint32_t which = *(volatile uint32_t*)&M.over[j & 1];
-                    raise(which);
-                    weigh(which);
+                    auto add_to_l = [&](int c, const float2 (&v)[4], float sign) {
+                        const float flat[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+                        const float x = rows_of_warp(flat, lane);
+                        if ((lane & 3) == c) l = fmaf(sign, x, l);
+                    };
+#pragma unroll
+                    for (int c = 0; c < NG8; ++c)
+                        if (which >> c & 1) {
+                            add_to_l(c, ls[c], 1.f);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) ls[c][i] = make_float2(0.f, 0.f);
+                        }
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (pass == 1) raise(which);
+#pragma unroll 1
+                        for (int c = 0; c < Rp / 8; ++c) {
+                            if (!(which >> c & 1)) continue;
+                            float2 sum[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+                            weigh(c, sum);
+                            add_to_l(c, sum, pass == 0 ? -1.f : 1.f);
+                        }
+                    }
                 }
                 // (read by all before raise's barriers; the next tile's votes go to the other word)
                 if (r == 0) M.over[j & 1] = 0;
-                if (few) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ls[2 * i] += lts[i].x;
-                        ls[2 * i + 1] += lts[i].y;
-                    }
-                } else {
-                    l += lt;
-                }
                 fence_async_smem();
                 tc5_fence_before();
                 __syncwarp();
@@ -859,7 +853,15 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
             live = !any_of(1, 128, !known);
             if (live && g2.n > 0) write_q(g2, s + 1, x2);
             // ---- the segment's state: written out, or left as a piece
-            M.red[sw][my_row].x = few ? rows_of_warp(ls, lane) : l;  // (few: lane i has row i / 4)
+#pragma unroll
+            for (int c = 0; c < NG8; ++c)
+                if (8 * c < Rp) {
+                    const float flat[8] = {ls[c][0].x, ls[c][0].y, ls[c][1].x, ls[c][1].y,
+                                           ls[c][2].x, ls[c][2].y, ls[c][3].x, ls[c][3].y};
+                    const float x = rows_of_warp(flat, lane);
+                    if ((lane & 3) == c) l += x;
+                }
+            M.red[sw][my_row].x = l;
             ok = wait_on(&M.odone, (tile - 1) & 1) && ok;
             __syncwarp();
             tc5_fence_after();
@@ -877,7 +879,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 const uint32_t at = tO + own_par * 3 * Rp + 8 * c;
                 tm_ld8x3(at, at + Rp, at + 2 * Rp, o, o1, o2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = (o[i] + (o1[i] + o2[i])) * M.fo[8 * c + i];
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(fmaf(o2[i], 0.125f, o1[i]), 0.125f, o[i]) * M.fo[8 * c + i];
             };
             if constexpr (TOK == 2) {
                 if (own_par == 1) {
