@@ -383,35 +383,39 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
     }
 }
 
-// Whole blocks of the batch's sequences as pools of the cache's dtype, at the same place, for the attention
-// kernels of plain pools.  A block that the sequence before has at the same place (a shared prefix) is left to it.
-template <typename T>
-__global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen p) {
+// The blocks that entries with more than `wide` rows read, as pools of the cache's dtype, at the same place, for the
+// attention kernels of plain pools.  Blocks (x, e) share entry e's: a group's prefix, a sequence's own part.  Bound by
+// memory, a byte read and two (four) written a value.
+template <typename T, bool JOINT>
+__global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
     constexpr int VEC = Elem<T>::VEC;
+    const RaggedParams& p = x.r;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.y;
-    auto blocks_of = [&](int q) {
-        const int n = __ldg(p.cu + q + 1) - __ldg(p.cu + q), L = __ldg(p.lens + q);
-        return n > 0 && L >= n && L <= p.T_max ? (L - 1) / p.bs + 1 : 0;
-    };
-    const int nb = blocks_of(b), before = b > 0 ? blocks_of(b - 1) : 0;
-    const int codes = p.H_kv * p.bs * p.D;  // (32-bit: a block's codes are bounded at creation)
-    for (int k = blockIdx.x; k < nb; k += gridDim.x) {
-        const int e = __ldg(p.table + (size_t)b * p.max_blocks + k);
-        if ((unsigned)e >= (unsigned)p.num_blocks) continue;
-        if (k < before && __ldg(p.table + (size_t)(b - 1) * p.max_blocks + k) == e) continue;
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(kv ? p.Vc : p.Kc) + (int64_t)e * codes);
-            T* dst = static_cast<T*>(kv ? p.V : p.K) + (int64_t)e * codes;
-            const float* sc = (kv ? p.Vsc : p.Ksc) + (int64_t)e * p.H_kv;
-#pragma unroll 4
-            for (int i = threadIdx.x; i < codes / 16; i += READ_THREADS) {
-                uint4 o[16 / VEC];
-                q8_widen16<T>(__ldg(src + i), __ldg(sc + i / (p.bs * p.D / 16)), o);
+    const int e = blockIdx.y;
+    Entry s;
+    if (JOINT && e < p.NG) {
+        const int b0 = __ldg(p.groups + e), b1 = __ldg(p.groups + e + 1);
+        if (b0 < 0 || b1 < b0 || b0 >= p.B || b1 > p.B) return;  // (the attention flags them)
+        s = group_entry(p, e);
+    } else {
+        s = seq_entry<JOINT>(p, e - (JOINT ? p.NG : 0));
+    }
+    if (!s.ok || ((int64_t)s.T << p.lgG) <= p.wide) return;
+    const int j0 = s.group ? 0 : s.pfx >> p.lgbs, j1 = ((s.group ? s.pfx : s.L) - 1) >> p.lgbs;
+    const int per = p.bs * p.D / 16, heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
+    const int64_t total = (int64_t)(j1 - j0 + 1) * heads * per;
+#pragma unroll 2
+    for (int64_t i = (int64_t)blockIdx.x * READ_THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * READ_THREADS) {
+        const int64_t g = i / per;
+        const int w = (int)(i - g * per), j = (int)(g / heads), hk = (int)(g - (int64_t)j * heads);
+        const int block = __ldg(p.table + (size_t)s.seq * p.max_blocks + j0 + j);
+        if ((unsigned)block >= (unsigned)p.num_blocks) continue;
+        const bool isv = hk >= p.H_kv;
+        const int64_t bh = (int64_t)block * p.H_kv + (isv ? hk - p.H_kv : hk), at = bh * per + w;
+        uint4 o[16 / VEC];
+        q8_widen16<T>(__ldg(static_cast<const uint4*>(isv ? p.V : p.K) + at), __ldg((isv ? x.Vsc : x.Ksc) + bh), o);
 #pragma unroll
-                for (int q = 0; q < 16 / VEC; ++q) reinterpret_cast<uint4*>(dst)[(int64_t)i * (16 / VEC) + q] = o[q];
-            }
-        }
+        for (int q = 0; q < 16 / VEC; ++q) static_cast<uint4*>(isv ? x.V : x.K)[at * (16 / VEC) + q] = o[q];
     }
 }
 
@@ -438,12 +442,16 @@ int launch_paged_read(int dtype, const Q8Read& p, cudaStream_t s) {
     return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 
-int launch_widen(int dtype, const Q8Widen& p, int sms, cudaStream_t s) {
+int launch_widen(int dtype, const Q8Widen& x, int sms, cudaStream_t s) {
+    const RaggedParams& p = x.r;
+    // CTAs of an entry: two an SM if there are few entries, some for each of many (most of which hold nothing)
+    const int NE = p.NG + p.B, want = 16 * sms / NE, most = 2 * sms;
     cudaLaunchAttribute attr[1];
-    const int want = (8 * sms + p.B - 1) / p.B;  // a few CTAs an SM, whatever the sequences hold
-    const cudaLaunchConfig_t cfg = dependent(attr, dim3(want < p.max_blocks ? want : p.max_blocks, p.B), READ_THREADS, s);
-    const cudaError_t e = dtype == 0 ? cudaLaunchKernelEx(&cfg, widen_kernel<__nv_bfloat16>, p)
-                                     : cudaLaunchKernelEx(&cfg, widen_kernel<float>, p);
+    const cudaLaunchConfig_t cfg = dependent(attr, dim3(want < 8 ? 8 : want > most ? most : want, NE), READ_THREADS, s);
+    const cudaError_t e = dtype == 0 ? (p.NG > 0 ? cudaLaunchKernelEx(&cfg, widen_kernel<__nv_bfloat16, true>, x)
+                                                 : cudaLaunchKernelEx(&cfg, widen_kernel<__nv_bfloat16, false>, x))
+                                     : (p.NG > 0 ? cudaLaunchKernelEx(&cfg, widen_kernel<float, true>, x)
+                                                 : cudaLaunchKernelEx(&cfg, widen_kernel<float, false>, x));
     return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 

@@ -37,19 +37,18 @@ struct Q8Read {
     int B, N, H_kv, D, bs, max_blocks, num_blocks, T_max;
 };
 struct Q8Widen {
-    const void *Kc, *Vc;
+    RaggedParams r;  // (K, V: the codes)
     const float *Ksc, *Vsc;
     void *K, *V;  // pools of the same shape in the cache's dtype
-    const int32_t *table, *cu, *lens;
-    int B, N, H_kv, D, bs, max_blocks, num_blocks, T_max;
 };
 
 // Attention on the codes (kvc_ragged_q8.cu; bf16, D = 64 or 128): maps of 128-byte rows (128 / D tokens) in boxes of
 // q8_box tokens, scratch for P = ctas an SM with 2 slots of `rows` rows.
 void q8_shape(int D, int G, int* rows, int* ctas);
 constexpr int q8_box(int D, int bs) { return bs < 16384 / D ? bs : 16384 / D; }
-int launch_ragged_q8(const RaggedParams& p, const float* Ksc, const float* Vsc, const CUtensorMap& k, const CUtensorMap& v,
-                     cudaStream_t s);
+// many: the call of the kernel of plain pools that attended the entries of many rows (p.part = 1), or nullptr.
+int launch_ragged_q8(const RaggedParams& p, const RaggedParams* many, const float* Ksc, const float* Vsc,
+                     const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 
 // Launchers (kvc_append8.cu); each returns a cudaError_t.
 int launch_append8(int dtype, const RopeParams& p, const RopeTable& t, int sms, cudaStream_t s);

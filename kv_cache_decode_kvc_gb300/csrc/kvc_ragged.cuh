@@ -62,6 +62,9 @@ struct RaggedParams {
     int bs, lgbs, max_blocks, num_blocks, T_max;
     int P;          // CTAs at most
     float qscale;   // log2(e) / sqrt(D)
+    // 8-bit caches: entries with more than `wide` query rows per head are attended by the kernel of plain pools, the
+    // others by that on codes.  part: 0 all entries, 1 those with few rows, 2 the others.
+    int wide, part;
 };
 
 // Scratch layout (bytes, 256-byte aligned parts), host side: P CTAs with `slots` slots of `rows` rows.
@@ -149,6 +152,11 @@ __device__ __forceinline__ Entry seq_entry(const RaggedParams& p, int b) {
 __device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
     const int b0 = __ldg(p.groups + g), b1 = __ldg(p.groups + g + 1), P = __ldg(p.prefix + g);
     return group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), prefix_used(p, b0, b1, P));
+}
+
+// Is the entry this call's?
+__device__ __forceinline__ bool in_part(const RaggedParams& p, const Entry& s) {
+    return p.part == 0 || (((int64_t)s.T << p.lgG) > p.wide) == (p.part == 2);
 }
 
 // sum of ceil(x / 2^lg) for x = 1 .. X, modulo 2^32 (of far positions only differences fit: unsigned
@@ -305,8 +313,10 @@ struct Ragged {
             int x[2] = {0, 0};
             if (fine && e < NE) {
                 const int cl = cls(p, s);
-                x[cl] = cost(p, s, cl);
-                about += cost_about(p, s, cl);
+                if (in_part(p, s)) {
+                    x[cl] = cost(p, s, cl);
+                    about += cost_about(p, s, cl);
+                }
                 k.ent[e] = make_int4(s.row0, s.T, s.L, s.pfx);
             }
 #pragma unroll
@@ -484,7 +494,7 @@ struct Ragged {
                 do {
                     if (++st.e == groups(p) + p.B) return false;
                     st.s = entry_of(p, st.e);
-                } while (!st.s.ok || cls(p, st.s) != cl);
+                } while (!st.s.ok || cls(p, st.s) != cl || !in_part(p, st.s));
             }
         }
         fill(p, st);
@@ -572,6 +582,10 @@ struct Ragged {
         p.cuts[2 * (3 * i + w) + 1] = make_int4(g.ntok << p.lgG, g.h, k.own - first, 0);
     }
 };
+
+// The split of the tensor-core kernel of plain pools.
+template <bool JOINT>
+using RaggedTc5 = Ragged<8, 7, true, JOINT>;
 
 // Zero output rows of the sequences that cannot be attended (CTA-strided over sequences, thread tid
 // of n).

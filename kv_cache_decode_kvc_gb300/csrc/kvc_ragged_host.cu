@@ -50,9 +50,55 @@ kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, Path path) {
     if (path == Path::Q8) kvc::q8_shape(h->D, h->G, &rows, &ctas);
     return kvc::ragged_scratch(h->B, N, NG, h->H_q, h->D, ragged_p(h, path), path == Path::TC5 ? 5 : 2, rows);
 }
-// Bytes of a widened pool (K or V) of an 8-bit cache's layer, which follow the ragged scratch.
-uint64_t widened(const kvc_cache* h, Path path) {
-    return h->quant && path == Path::CC ? ((uint64_t)h->layer_bytes * h->es + 255) / 256 * 256 : 0;
+// On an 8-bit cache, entries (sequences, shared prefixes) with more query rows per head than this are widened to bf16
+// and attended by the kernel of plain pools: per 32 rows it takes a quarter of the time of the kernel on codes, which
+// makes up for the widening at about a hundred rows.
+constexpr int MANY_ROWS = 128;
+// Is that worth its launches (three, some 8 us with nothing to do)?  The host knows how many rows an entry can have if every
+// sequence has a token, no more; a batch whose sequences have none, against that, is attended on codes all the same.
+bool many_rows(const kvc_cache* h, int N, int NG) {
+    const int64_t most = NG > 0 ? N : (int64_t)N - h->B + 1;
+    return most * h->G > 2 * MANY_ROWS;
+}
+// The parts of the scratch: the path's, that of the kernel of plain pools beside the one on codes, and the two
+// widened pools.
+struct Scratch {
+    kvc::RaggedScratch own, many;
+    uint64_t many_at, wide_at, wide_bytes, total;
+    bool split;  // entries of many rows are attended apart
+};
+Scratch scratch_of(const kvc_cache* h, int N, int NG, Path path) {
+    Scratch s{};
+    s.own = ragged_ws(h, N, NG, path);
+    s.split = path == Path::Q8 && many_rows(h, N, NG);
+    s.many_at = s.wide_at = s.total = s.own.total;
+    if (s.split) {
+        s.many = ragged_ws(h, N, NG, Path::TC5);
+        s.wide_at = s.total += s.many.total;
+    }
+    if (h->quant && (path == Path::CC || s.split)) {
+        s.wide_bytes = ((uint64_t)h->layer_bytes * h->es + 255) / 256 * 256;
+        s.total += 2 * s.wide_bytes;
+    }
+    return s;
+}
+void set_scratch(kvc::RaggedParams& p, char* w, const kvc::RaggedScratch& sc) {
+    p.plan = reinterpret_cast<int*>(w + sc.plan);
+    p.cuts = reinterpret_cast<int4*>(w + sc.cuts);
+    p.row_o = reinterpret_cast<float*>(w + sc.row_o);
+    p.row_ml = reinterpret_cast<float*>(w + sc.row_ml);
+    p.slot_o = reinterpret_cast<float*>(w + sc.slot_o);
+    p.slot_ml = reinterpret_cast<float*>(w + sc.slot_ml);
+}
+// The tensor-core kernel of plain pools, k / v: the pools' maps.
+int launch_tc5(const kvc_cache* h, const kvc::RaggedParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+    // boxes of 64 query rows, and of as few as one token's
+    CUtensorMap mq, m1;
+    const int few = h->G > 16 ? h->G : 16;
+    if (!kvc::make_q_tensor_map(&mq, p.q, p.N, h->H_q, h->D, p.q_ts, h->G, 64 / h->G) ||
+        !kvc::make_q_tensor_map(&m1, p.q, p.N, h->H_q, h->D, p.q_ts, h->G, few / h->G))
+        return KVC_ECUDA;
+    return kvc::launch_ragged_tc5(p, mq, m1, k, v, st) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
 int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* table,
@@ -64,9 +110,8 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     if (!packed_ok(q, q_stride, row, h->es) || !packed_ok(out, out_stride, row, h->es)) return KVC_EINVAL;
     if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(ws, 256)) return KVC_EINVAL;
     const Path path = ragged_path(h);
-    const kvc::RaggedScratch sc = ragged_ws(h, N, NG, path);
-    const uint64_t wide = widened(h, path);
-    if (ws_bytes < sc.total + 2 * wide) return KVC_EINVAL;
+    const Scratch sc = scratch_of(h, N, NG, path);
+    if (ws_bytes < sc.total) return KVC_EINVAL;
     const int rc = on_device(h);
     if (rc != KVC_OK) return rc;
     kvc::RaggedParams p{};
@@ -83,12 +128,7 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.prefix = NG > 0 ? prefix : nullptr;
     p.err = h->err;
     char* w = static_cast<char*>(ws);
-    p.plan = reinterpret_cast<int*>(w + sc.plan);
-    p.cuts = reinterpret_cast<int4*>(w + sc.cuts);
-    p.row_o = reinterpret_cast<float*>(w + sc.row_o);
-    p.row_ml = reinterpret_cast<float*>(w + sc.row_ml);
-    p.slot_o = reinterpret_cast<float*>(w + sc.slot_o);
-    p.slot_ml = reinterpret_cast<float*>(w + sc.slot_ml);
+    set_scratch(p, w, sc.own);
     p.B = h->B;
     p.N = N;
     p.H_q = h->H_q;
@@ -104,45 +144,42 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.P = ragged_p(h, path);
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (path == Path::Q8) {
-        const float* Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
-        const CUtensorMap* kv = &h->rmaps[2 * (size_t)layer];
-        return kvc::launch_ragged_q8(p, Ksc, Ksc + h->scale_stride, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
+    if (!h->quant) {
+        if (path == Path::CC) return kvc::launch_ragged_cc(h->dtype, p, st) == 0 ? KVC_OK : KVC_ECUDA;
+        const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
+        return launch_tc5(h, p, kv[0], kv[1], st);
     }
-    if (h->quant) {
-        kvc::Q8Widen x{};
-        x.Kc = p.K;
-        x.Vc = p.V;
-        x.Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
-        x.Vsc = x.Ksc + h->scale_stride;
-        x.K = w + sc.total;
-        x.V = w + sc.total + wide;
-        x.table = table;
-        x.cu = cu;
-        x.lens = lens;
-        x.B = h->B;
-        x.N = N;
-        x.H_kv = h->H_kv;
-        x.D = h->D;
-        x.bs = h->bs;
-        x.max_blocks = h->max_blocks;
-        x.num_blocks = h->num_blocks;
-        x.T_max = h->T_max;
-        p.K = x.K;
-        p.V = x.V;
+    const float* Ksc = h->scales + (size_t)(2 * layer) * h->scale_stride;
+    const float* Vsc = Ksc + h->scale_stride;
+    kvc::RaggedParams m = p;  // the call on widened blocks
+    m.K = w + sc.wide_at;
+    m.V = w + sc.wide_at + sc.wide_bytes;
+    m.wide = path == Path::CC ? -1 : MANY_ROWS;
+    if (path == Path::CC || sc.split) {
+        kvc::Q8Widen x{p, Ksc, Vsc, w + sc.wide_at, w + sc.wide_at + sc.wide_bytes};
+        x.r.wide = m.wide;
         if (kvc::launch_widen(h->dtype, x, h->sms, st) != 0) return KVC_ECUDA;
     }
-    if (path == Path::TC5) {
-        // boxes of 64 query rows, and of as few as one token's
-        CUtensorMap mq, m1;
-        const int few = h->G > 16 ? h->G : 16;
-        if (!kvc::make_q_tensor_map(&mq, q, N, h->H_q, h->D, q_stride, h->G, 64 / h->G) ||
-            !kvc::make_q_tensor_map(&m1, q, N, h->H_q, h->D, q_stride, h->G, few / h->G))
+    if (path == Path::CC) return kvc::launch_ragged_cc(h->dtype, m, st) == 0 ? KVC_OK : KVC_ECUDA;
+    if (sc.split) {
+        set_scratch(m, w + sc.many_at, sc.many);
+        m.row_o = p.row_o;  // (the rows of shared prefixes are merged together)
+        m.row_ml = p.row_ml;
+        m.P = ragged_p(h, Path::TC5);
+        m.part = 2;
+        p.wide = MANY_ROWS;
+        p.part = 1;
+        CUtensorMap mk, mv;
+        const uint64_t rows = h->layer_bytes / h->D;
+        const int box = h->bs < 128 ? h->bs : 128;
+        if (!kvc::make_pool_tensor_map(&mk, w + sc.wide_at, rows, h->D, box) ||
+            !kvc::make_pool_tensor_map(&mv, w + sc.wide_at + sc.wide_bytes, rows, h->D, box))
             return KVC_ECUDA;
-        const CUtensorMap* kv = h->D == 128 ? &h->tmaps[4 * (size_t)layer + 2] : &h->rmaps[2 * (size_t)layer];
-        return kvc::launch_ragged_tc5(p, mq, m1, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
+        const int e = launch_tc5(h, m, mk, mv, st);
+        if (e != KVC_OK) return e;
     }
-    return kvc::launch_ragged_cc(h->dtype, p, st) == 0 ? KVC_OK : KVC_ECUDA;
+    const CUtensorMap* kv = &h->rmaps[2 * (size_t)layer];
+    return kvc::launch_ragged_q8(p, sc.split ? &m : nullptr, Ksc, Vsc, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
 }  // namespace
@@ -291,7 +328,7 @@ int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes) {
     // enough for every path, whatever kvc_set_math does in between
     uint64_t most = 0;
     for (const Path path : {Path::CC, h->quant ? Path::Q8 : Path::TC5}) {
-        const uint64_t n = ragged_ws(h, N, NG, path).total + 2 * widened(h, path);
+        const uint64_t n = scratch_of(h, N, NG, path).total;
         if (n > most) most = n;
     }
     *bytes = most;

@@ -285,6 +285,94 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
     }
 }
 
+// With groups, where entries of many rows were attended by the kernel with split RA (parameters pa) and the others by
+// that with split RB (pb): as merge_rows_kernel, each of the row's two streams from its own kernel's pieces.  (The row
+// buffers are one.)
+template <typename T, class RA, class RB>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) merge_parts_kernel(const RaggedParams pa, const RaggedParams pb) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const RaggedParams& p = pb;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const typename RA::Split spa = RA::planned(pa);
+    const typename RB::Split spb = RB::planned(pb);
+    if (!spa.valid && !spb.valid) return;
+    const int row = blockIdx.x, h = blockIdx.y, G = 1 << p.lgG;
+    if (row >= __ldg(p.cu + p.B)) return;
+    const int lo = last_at(p.cu, p.B, row, lane);  // the sequence
+    const int a = last_at(p.groups, p.NG, lo, lane), b0 = __ldg(p.groups + a), b1 = __ldg(p.groups + a + 1);
+    const int P = __ldg(p.prefix + a), used = prefix_used(p, b0, b1, P);
+    // A stream's pieces: how many, the first one's owner, class, the row's place in its tile, which kernel's.
+    struct Pieces {
+        int n, first, cl, row;
+        bool many;
+    };
+    auto pieces = [&](int e, const Entry& s) {
+        Pieces x;
+        x.many = !in_part(pb, s);
+        auto find = [&](auto r, const auto& sp, const RaggedParams& q) {
+            using R = decltype(r);
+            const typename R::Stream st = R::of_row(q, sp, q.plan, e, s, h, row);
+            x.cl = R::cls(q, s);
+            x.first = R::owner_of(sp, st, x.cl, 0);
+            x.n = R::owner_of(sp, st, x.cl, st.n - 1) - x.first + 1;
+            x.row = ((row - s.row0) << p.lgG) & (R::RT - 1);
+        };
+        if (x.many) find(RA{}, spa, pa);
+        else find(RB{}, spb, pb);
+        return x;
+    };
+    const Entry own = seq_entry(p, lo, __ldg(p.cu + lo), __ldg(p.cu + lo + 1), __ldg(p.lens + lo), P, used);
+    if (!own.ok) return;
+    const Pieces po = pieces(p.NG + lo, own);
+    const bool joint = own.pfx > 0;
+    if (!joint && po.n == 1) return;  // written by its worker
+    Pieces pp;
+    pp.n = 0;
+    if (joint) pp = pieces(a, group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), used));
+    const int np = pp.n + po.n;
+    auto out_of = [&](int g) { return static_cast<T*>(p.out) + (int64_t)row * p.out_ts + (int64_t)(h * G + g) * p.D; };
+    auto at_head = [&](int g) {
+        return [&, g](int q, const float*& o, const float*& ml) {
+            const bool pre = q < pp.n;
+            const int c = pre ? q : q - pp.n;
+            if (c == 0 && joint) {
+                const int64_t at = ((int64_t)(pre ? 0 : 1) * p.N + row) * p.H_q + h * G + g;
+                o = p.row_o + at * p.D;
+                ml = p.row_ml + at * 2;
+                return;
+            }
+            const int cl = pre ? pp.cl : po.cl, owner = (pre ? pp.first : po.first) + c, r = (pre ? pp.row : po.row) + g;
+            const bool many = pre ? pp.many : po.many;
+            const RaggedParams& k = many ? pa : pb;
+            const int64_t at = (many ? (int64_t)RA::slot(cl, owner, c > 0) * RA::SLOT_ROWS
+                                     : (int64_t)RB::slot(cl, owner, c > 0) * RB::SLOT_ROWS) + r;
+            o = k.slot_o + at * p.D;
+            ml = k.slot_ml + at * 2;
+        };
+    };
+    const int g0 = blockIdx.z * MERGE_WARPS;
+    if (np > MERGE_WIDE) {
+        for (int g = g0; g < min(g0 + MERGE_WARPS, G); ++g) merge_row_wide<T>(p, np, out_of(g), warp, lane, at_head(g));
+    } else if (g0 + warp < G) {
+        merge_store<T>(p, merge_pieces(p, np, 0, 1, lane, at_head(g0 + warp)), out_of(g0 + warp), lane);
+    }
+}
+template <typename T, class RA, class RB>
+inline int launch_merge_parts(const RaggedParams& pa, const RaggedParams& pb, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int G = 1 << pb.lgG;
+    cfg.gridDim = dim3((unsigned)pb.N, (unsigned)pb.H_kv, (unsigned)((G + MERGE_WARPS - 1) / MERGE_WARPS));
+    cfg.blockDim = dim3((unsigned)((G < 4 ? 4 : (G < MERGE_WARPS ? G : MERGE_WARPS)) * 32));
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, merge_parts_kernel<T, RA, RB>, pa, pb);
+    return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
+}
+
 // Launch behind the attention kernel; starts as that one ends.
 template <typename T, class R, bool JOINT>
 inline int launch_merge(const RaggedParams& p, cudaStream_t s) {

@@ -958,7 +958,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
 }
 
 template <int TOK, int LRT, bool JOINT>
-static int launch_q8_as(const Q8Attn& pa, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+static int launch_q8_as(const Q8Attn& pa, const RaggedParams* many, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
     using C = Q8Cfg<TOK, LRT, JOINT>;
     static PerDeviceOnce once;
     const int e0 = once.run([] {
@@ -977,6 +977,8 @@ static int launch_q8_as(const Q8Attn& pa, const CUtensorMap& k, const CUtensorMa
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_q8_kernel<TOK, LRT, JOINT>, pa, k, v);
     if (e != cudaSuccess) return (int)e;
+    if constexpr (JOINT)
+        if (many) return launch_merge_parts<__nv_bfloat16, RaggedTc5<true>, typename C::R>(*many, pa.r, s);
     return launch_merge<__nv_bfloat16, typename C::R, JOINT>(pa.r, s);
 }
 
@@ -986,16 +988,21 @@ void q8_shape(int D, int G, int* rows, int* ctas) {
     *ctas = D == 64 && G > 16 ? 1 : 2;
 }
 
-int launch_ragged_q8(const RaggedParams& p, const float* Ksc, const float* Vsc, const CUtensorMap& k, const CUtensorMap& v,
-                     cudaStream_t s) {
+int launch_ragged_q8(const RaggedParams& p, const RaggedParams* many, const float* Ksc, const float* Vsc,
+                     const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
     int rows, ctas;
     q8_shape(p.D, 1 << p.lgG, &rows, &ctas);
     Q8Attn pa{p, Ksc, Vsc, 0};
     // (a batch of at most one tile of rows per sequence and no shared prefixes)
     pa.once = p.NG == 0 && ((int64_t)p.N << p.lgG) <= (int64_t)p.B * rows;
-    if (p.D == 128) return p.NG > 0 ? launch_q8_as<1, 5, true>(pa, k, v, s) : launch_q8_as<1, 5, false>(pa, k, v, s);
-    if (rows == 16) return p.NG > 0 ? launch_q8_as<2, 4, true>(pa, k, v, s) : launch_q8_as<2, 4, false>(pa, k, v, s);
-    return p.NG > 0 ? launch_q8_as<2, 5, true>(pa, k, v, s) : launch_q8_as<2, 5, false>(pa, k, v, s);
+    auto go = [&](auto tok, auto lrt) {
+        constexpr int TOK = decltype(tok)::value, LRT = decltype(lrt)::value;
+        return p.NG > 0 ? launch_q8_as<TOK, LRT, true>(pa, many, k, v, s) : launch_q8_as<TOK, LRT, false>(pa, many, k, v, s);
+    };
+    using std::integral_constant;
+    if (p.D == 128) return go(integral_constant<int, 1>{}, integral_constant<int, 5>{});
+    if (rows == 16) return go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    return go(integral_constant<int, 2>{}, integral_constant<int, 5>{});
 }
 
 }  // namespace kvc

@@ -62,7 +62,7 @@ struct Give {
 template <int D_, bool JOINT>
 struct RtCfg {
     static constexpr int D = D_;
-    using R = Ragged<8, 7, true, JOINT>;
+    using R = RaggedTc5<JOINT>;
     using Seg = typename R::Seg;
     static constexpr int KT = R::KT;
     static constexpr int CB = D / 64;                // 128-byte column blocks of a row
@@ -1137,6 +1137,7 @@ static int launch_rt(const RaggedParams& p, const CUtensorMap& q, const CUtensor
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, ragged_tc5_kernel<D, JOINT>, p, q, q1, k, v);
     if (e != cudaSuccess) return (int)e;
+    if (JOINT && p.part != 0) return 0;  // (merged with the pieces of the kernel on codes)
     return launch_merge<__nv_bfloat16, typename C::R, JOINT>(p, s);
 }
 
