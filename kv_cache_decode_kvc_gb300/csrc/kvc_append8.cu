@@ -383,39 +383,69 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
     }
 }
 
-// The blocks that entries with more than `wide` rows read, as pools of the cache's dtype, at the same place, for the
-// attention kernels of plain pools.  Blocks (x, e) share entry e's: a group's prefix, a sequence's own part.  Bound by
-// memory, a byte read and two (four) written a value.
+// The blocks that entries with more than `wide` rows read (a group's prefix, a sequence's own part), as pools of the
+// cache's dtype, at the same place, for the attention kernels of plain pools.  Every CTA finds these entries, 256 at a
+// time, and all share each one's pieces.  Bound by memory, a byte read and two (four) written a value.
 template <typename T, bool JOINT>
 __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
-    constexpr int VEC = Elem<T>::VEC;
+    constexpr int VEC = Elem<T>::VEC, ILP = 4;
     const RaggedParams& p = x.r;
+    __shared__ int found, seq_s[READ_THREADS], j0_s[READ_THREADS], nj_s[READ_THREADS];
+    const int tid = threadIdx.x, NE = p.B + (JOINT ? p.NG : 0);
+    const int lgper = 31 - __clz(p.bs * p.D / 16), heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int e = blockIdx.y;
-    Entry s;
-    if (JOINT && e < p.NG) {
-        const int b0 = __ldg(p.groups + e), b1 = __ldg(p.groups + e + 1);
-        if (b0 < 0 || b1 < b0 || b0 >= p.B || b1 > p.B) return;  // (the attention flags them)
-        s = group_entry(p, e);
-    } else {
-        s = seq_entry<JOINT>(p, e - (JOINT ? p.NG : 0));
-    }
-    if (!s.ok || ((int64_t)s.T << p.lgG) <= p.wide) return;
-    const int j0 = s.group ? 0 : s.pfx >> p.lgbs, j1 = ((s.group ? s.pfx : s.L) - 1) >> p.lgbs;
-    const int per = p.bs * p.D / 16, heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
-    const int64_t total = (int64_t)(j1 - j0 + 1) * heads * per;
-#pragma unroll 2
-    for (int64_t i = (int64_t)blockIdx.x * READ_THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * READ_THREADS) {
-        const int64_t g = i / per;
-        const int w = (int)(i - g * per), j = (int)(g / heads), hk = (int)(g - (int64_t)j * heads);
-        const int block = __ldg(p.table + (size_t)s.seq * p.max_blocks + j0 + j);
-        if ((unsigned)block >= (unsigned)p.num_blocks) continue;
-        const bool isv = hk >= p.H_kv;
-        const int64_t bh = (int64_t)block * p.H_kv + (isv ? hk - p.H_kv : hk), at = bh * per + w;
-        uint4 o[16 / VEC];
-        q8_widen16<T>(__ldg(static_cast<const uint4*>(isv ? p.V : p.K) + at), __ldg((isv ? x.Vsc : x.Ksc) + bh), o);
+    for (int e0 = 0; e0 < NE; e0 += READ_THREADS) {
+        const int e = e0 + tid;
+        Entry s;
+        s.ok = false;
+        if (JOINT && e < p.NG) {
+            const int b0 = __ldg(p.groups + e), b1 = __ldg(p.groups + e + 1);
+            if (b0 >= 0 && b0 < p.B && b1 >= b0 && b1 <= p.B) s = group_entry(p, e);  // (else the attention flags it)
+        } else if (e < NE) {
+            s = seq_entry<JOINT>(p, e - (JOINT ? p.NG : 0));
+        }
+        __syncthreads();
+        if (tid == 0) found = 0;
+        __syncthreads();
+        if (s.ok && ((int64_t)s.T << p.lgG) > p.wide) {
+            const int i = atomicAdd(&found, 1), j0 = s.group ? 0 : s.pfx >> p.lgbs;
+            seq_s[i] = s.seq;
+            j0_s[i] = j0;
+            nj_s[i] = (((s.group ? s.pfx : s.L) - 1) >> p.lgbs) + 1 - j0;
+        }
+        __syncthreads();
+        for (int k = 0; k < found; ++k) {
+            const int32_t* row = p.table + (size_t)seq_s[k] * p.max_blocks + j0_s[k];
+            const int64_t total = ((int64_t)nj_s[k] * heads) << lgper;
+            for (int64_t i0 = (int64_t)blockIdx.x * (ILP * READ_THREADS) + tid; i0 < total; i0 += (int64_t)gridDim.x * (ILP * READ_THREADS)) {
+                uint4 c[ILP];
+                float sc[ILP];
+                int64_t at[ILP];
+                bool isv[ILP];
 #pragma unroll
-        for (int q = 0; q < 16 / VEC; ++q) static_cast<uint4*>(isv ? x.V : x.K)[at * (16 / VEC) + q] = o[q];
+                for (int q = 0; q < ILP; ++q) {
+                    const int64_t i = i0 + q * READ_THREADS;
+                    at[q] = -1;
+                    if (i >= total) continue;
+                    const unsigned g = (unsigned)(i >> lgper), j = g / (unsigned)heads, hk = g - j * heads;
+                    const int block = __ldg(row + j);
+                    if ((unsigned)block >= (unsigned)p.num_blocks) continue;
+                    isv[q] = hk >= (unsigned)p.H_kv;
+                    const int64_t bh = (int64_t)block * p.H_kv + (isv[q] ? hk - p.H_kv : hk);
+                    at[q] = (bh << lgper) + (i & ((1 << lgper) - 1));
+                    c[q] = __ldg(static_cast<const uint4*>(isv[q] ? p.V : p.K) + at[q]);
+                    sc[q] = __ldg((isv[q] ? x.Vsc : x.Ksc) + bh);
+                }
+#pragma unroll
+                for (int q = 0; q < ILP; ++q) {
+                    if (at[q] < 0) continue;
+                    uint4 o[16 / VEC];
+                    q8_widen16<T>(c[q], sc[q], o);
+#pragma unroll
+                    for (int v = 0; v < 16 / VEC; ++v) static_cast<uint4*>(isv[q] ? x.V : x.K)[at[q] * (16 / VEC) + v] = o[v];
+                }
+            }
+        }
     }
 }
 
@@ -444,10 +474,8 @@ int launch_paged_read(int dtype, const Q8Read& p, cudaStream_t s) {
 
 int launch_widen(int dtype, const Q8Widen& x, int sms, cudaStream_t s) {
     const RaggedParams& p = x.r;
-    // CTAs of an entry: two an SM if there are few entries, some for each of many (most of which hold nothing)
-    const int NE = p.NG + p.B, want = 16 * sms / NE, most = 2 * sms;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = dependent(attr, dim3(want < 8 ? 8 : want > most ? most : want, NE), READ_THREADS, s);
+    const cudaLaunchConfig_t cfg = dependent(attr, dim3(4 * sms), READ_THREADS, s);
     const cudaError_t e = dtype == 0 ? (p.NG > 0 ? cudaLaunchKernelEx(&cfg, widen_kernel<__nv_bfloat16, true>, x)
                                                  : cudaLaunchKernelEx(&cfg, widen_kernel<__nv_bfloat16, false>, x))
                                      : (p.NG > 0 ? cudaLaunchKernelEx(&cfg, widen_kernel<float, true>, x)

@@ -71,6 +71,7 @@ struct Q8Cfg {
         alignas(16) float mu[32];
         alignas(16) float b[32];
         float m[32], M[32], fo[32], fl[32];
+        char* dst[32];  // where a row's output or piece goes
         float2 red[4][32];
         uint32_t knan[2][4];  // (TOK = 2, of two tiles in turn) second tokens whose key has NaN codes
         uint32_t over[2];  // (of two tiles in turn) groups of eight rows whose references have to be raised
@@ -217,6 +218,17 @@ __device__ __forceinline__ float rows_of_warp(const float (&sum)[8], int lane) {
 // 0xFF in the bytes that are NaN codes (0x7F, 0xFF).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t u) {
     return ((((u & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+}
+// NaN in column `dim` of the rows r0 .. that see a NaN code there which was taken out of V: of positions that not all
+// rows see, up to `end`, the last that the segment's tiles hold.
+template <class Seg>
+__device__ __noinline__ void add_nan(const RaggedParams& p, const Seg& g, int end, int r0, int dim, int D, float (&o)[8]) {
+    for (int t = max(g.lim0, g.kv0); t < end; ++t) {
+        const int64_t vr = cache_row_rd(p.table, p.bs, p.max_blocks, p.num_blocks, p.H_kv, p.T_max, g.seq, g.h, t, p.err);
+        if ((__ldg(static_cast<const uint8_t*>(p.V) + vr * D + dim) & 0x7F) != 0x7F) continue;
+        for (int i = 0; i < 8; ++i)
+            if (t < g.sees((r0 + i) >> p.lgG)) o[i] = __uint_as_float(0x7FFFFFFFu);
+    }
 }
 // 2^d for an integer-valued d, clamped to the normal floats.
 __device__ __forceinline__ float pow2_of(float d) { return exp2i((int)fminf(fmaxf(d, -126.f), 127.f)); }
@@ -532,12 +544,20 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                                                         (int64_t)(g.h * G + (rr & (G - 1))) * D) +
                          v);
         };
-        auto write_q = [&](const Seg& g, int s, uint4 x) {  // x: this thread's first vector
+        constexpr int QV = (C::RT * VPR + 127) / 128;  // a thread's vectors
+        auto write_q = [&](const Seg& g, int s, uint4 x0) {  // x0: this thread's first vector
             const int nrow = g.ntok << p.lgG, Rp = nrow <= 8 ? 8 : nrow <= 16 ? 16 : 32;
-#pragma unroll 1
-            for (int i = r; i < Rp * VPR; i += 128) {
+            uint4 xs[QV];
+            xs[0] = x0;
+#pragma unroll
+            for (int k = 1; k < QV; ++k)
+                if (r + 128 * k < Rp * VPR) xs[k] = load_q(g, r + 128 * k);
+#pragma unroll
+            for (int k = 0; k < QV; ++k) {
+                const int i = r + 128 * k;
+                if (i >= Rp * VPR) continue;
                 const int rr = i / VPR, v = i & (VPR - 1);
-                if (i != r) x = load_q(g, i);
+                const uint4 x = xs[k];
                 float f[8];
                 Elem<__nv_bfloat16>::unpack(x, f);
                 uint32_t top = 0;
@@ -670,6 +690,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 // integers; O and l follow.
                 auto raise = [&](uint32_t which) {
                     const float la = (float)((int)((__float_as_uint(sc.y) >> 23) & 0xFFu) - 127);
+                    const bool alike = __all_sync(ALL, la == __shfl_sync(ALL, la, 0));  // (one block's positions, mostly)
 #pragma unroll 1
                     for (int c = 0; c < Rp / 8; ++c) {
                         if (!(which >> c & 1)) continue;
@@ -684,7 +705,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float v = top[i] == top[i] ? top[i] : -INFINITY;
-                            const float mx = warp_max(v), Mx = warp_max(v + la);
+                            const float mx = warp_max(v), Mx = alike ? mx + la : warp_max(v + la);
                             if (lane == 0) M.red[sw][8 * c + i] = make_float2(mx, Mx);
                         }
                     }
@@ -868,8 +889,17 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
             ok = !any_of(1, 128, !ok);
             if (r < Rp) {
                 const float sum = (M.red[0][r].x + M.red[1][r].x) + (M.red[2][r].x + M.red[3][r].x);
-                M.fl[r] = sum;
                 M.fo[r] = 1.f / M.b[r] * (g.dst == -1 ? 1.f / sum : 1.f);
+                const int64_t row = g.row0 + (r >> p.lgG);
+                const int head = g.h * G + (r & (G - 1));
+                if (g.dst == -1) {
+                    M.dst[r] = static_cast<char*>(p.out) + (row * p.out_ts + (int64_t)head * D) * 2;
+                } else {
+                    float *po, *pml;
+                    ragged_dst(p, g.dst, R::SLOT_ROWS, r, row, head, po, pml);
+                    M.dst[r] = reinterpret_cast<char*>(po);
+                    if (r < nrow && ok) *reinterpret_cast<float2*>(pml) = make_float2(M.m[r], sum);
+                }
             }
             sync4();
             const bool nonfin = M.nonfinite != 0;
@@ -900,29 +930,15 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                     outputs(c, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int rr = 8 * c + i;
-                        if (rr >= nrow) continue;
-                        if constexpr (TOK == 2) o[i] += half[rr * 64 + dim];
-                        if (nonfin) {
-                            // NaN codes that were taken out of tiles this row sees part of
-                            const int end = min(g.sees(rr >> p.lgG), g.n > (g.kv_end - 1 - g.kv0) / C::KT ? g.kv_end : g.kv0 + g.n * C::KT);
-                            for (int t = max(g.lim0, g.kv0); t < end; ++t) {
-                                const int64_t vr = cache_row_rd(p.table, p.bs, p.max_blocks, p.num_blocks, p.H_kv, p.T_max,
-                                                                g.seq, g.h, t, p.err);
-                                if ((__ldg(static_cast<const uint8_t*>(p.V) + vr * D + dim) & 0x7F) == 0x7F)
-                                    o[i] = __uint_as_float(0x7FFFFFFFu);
-                            }
-                        }
-                        const int64_t row = g.row0 + (rr >> p.lgG);
-                        const int head = g.h * G + (rr & (G - 1));
-                        if (g.dst == -1) {
-                            static_cast<__nv_bfloat16*>(p.out)[row * p.out_ts + (int64_t)head * D + dim] = __float2bfloat16_rn(o[i]);
-                        } else {
-                            float *po, *pml;
-                            ragged_dst(p, g.dst, R::SLOT_ROWS, rr, row, head, po, pml);
-                            po[dim] = o[i];
-                            if (dim == 0) *reinterpret_cast<float2*>(pml) = make_float2(M.m[rr], M.fl[rr]);
-                        }
+                        if constexpr (TOK == 2) o[i] += half[(8 * c + i) * 64 + dim];
+                    }
+                    if (nonfin) add_nan(p, g, g.n > (g.kv_end - 1 - g.kv0) / C::KT ? g.kv_end : g.kv0 + g.n * C::KT, 8 * c, dim, D, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (8 * c + i >= nrow) continue;
+                        char* to = M.dst[8 * c + i];
+                        if (g.dst == -1) reinterpret_cast<__nv_bfloat16*>(to)[dim] = __float2bfloat16_rn(o[i]);
+                        else reinterpret_cast<float*>(to)[dim] = o[i];
                     }
                 }
             }
