@@ -385,13 +385,14 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
 
 // The blocks that entries with more than `wide` rows read (a group's prefix, a sequence's own part), as pools of the
 // cache's dtype, at the same place, for the attention kernels of plain pools.  Every CTA finds these entries, 256 at a
-// time, and all share each one's pieces.  Bound by memory, a byte read and two (four) written a value.
+// time, and all share their pieces laid end to end.  Bound by memory, a byte read and two (four) written a value.
 template <typename T, bool JOINT>
 __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
-    constexpr int VEC = Elem<T>::VEC, ILP = 4;
+    constexpr int VEC = Elem<T>::VEC, ILP = 4, WARPS = READ_THREADS / 32;
     const RaggedParams& p = x.r;
-    __shared__ int found, seq_s[READ_THREADS], j0_s[READ_THREADS], nj_s[READ_THREADS];
-    const int tid = threadIdx.x, NE = p.B + (JOINT ? p.NG : 0);
+    __shared__ int seq_s[READ_THREADS], j0_s[READ_THREADS], warps[WARPS];
+    __shared__ int64_t end_s[READ_THREADS], sums[WARPS];  // pieces up to and with an entry's
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NE = p.B + (JOINT ? p.NG : 0);
     const int lgper = 31 - __clz(p.bs * p.D / 16), heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int e0 = 0; e0 < NE; e0 += READ_THREADS) {
@@ -404,46 +405,70 @@ __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
         } else if (e < NE) {
             s = seq_entry<JOINT>(p, e - (JOINT ? p.NG : 0));
         }
-        __syncthreads();
-        if (tid == 0) found = 0;
-        __syncthreads();
-        if (s.ok && ((int64_t)s.T << p.lgG) > p.wide) {
-            const int i = atomicAdd(&found, 1), j0 = s.group ? 0 : s.pfx >> p.lgbs;
-            seq_s[i] = s.seq;
-            j0_s[i] = j0;
-            nj_s[i] = (((s.group ? s.pfx : s.L) - 1) >> p.lgbs) + 1 - j0;
+        const bool mine = s.ok && ((int64_t)s.T << p.lgG) > p.wide;
+        const int j0 = !mine || s.group ? 0 : s.pfx >> p.lgbs;
+        const int64_t n = !mine ? 0 : ((int64_t)((((s.group ? s.pfx : s.L) - 1) >> p.lgbs) + 1 - j0) * heads) << lgper;
+        int64_t end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(0xFFFFFFFFu, end, o);
+            if (lane >= o) end += t;
+        }
+        const uint32_t those = __ballot_sync(0xFFFFFFFFu, mine);
+        __syncthreads();  // (the entries before are done with)
+        if (lane == 31) {
+            sums[warp] = end;
+            warps[warp] = __popc(those);
         }
         __syncthreads();
-        for (int k = 0; k < found; ++k) {
-            const int32_t* row = p.table + (size_t)seq_s[k] * p.max_blocks + j0_s[k];
-            const int64_t total = ((int64_t)nj_s[k] * heads) << lgper;
-            for (int64_t i0 = (int64_t)blockIdx.x * (ILP * READ_THREADS) + tid; i0 < total; i0 += (int64_t)gridDim.x * (ILP * READ_THREADS)) {
-                uint4 c[ILP];
-                float sc[ILP];
-                int64_t at[ILP];
-                bool isv[ILP];
+        int found = 0, at = __popc(those & ((1u << lane) - 1));
+        int64_t total = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) {
+                at += warps[w];
+                end += sums[w];
+            }
+            found += warps[w];
+            total += sums[w];
+        }
+        if (mine) {
+            seq_s[at] = s.seq;
+            j0_s[at] = j0;
+            end_s[at] = end;
+        }
+        __syncthreads();
+        for (int64_t i0 = (int64_t)blockIdx.x * (ILP * READ_THREADS) + tid; i0 < total; i0 += (int64_t)gridDim.x * (ILP * READ_THREADS)) {
+            uint4 c[ILP];
+            float sc[ILP];
+            int64_t at_piece[ILP];
+            bool isv[ILP];
 #pragma unroll
-                for (int q = 0; q < ILP; ++q) {
-                    const int64_t i = i0 + q * READ_THREADS;
-                    at[q] = -1;
-                    if (i >= total) continue;
-                    const unsigned g = (unsigned)(i >> lgper), j = g / (unsigned)heads, hk = g - j * heads;
-                    const int block = __ldg(row + j);
-                    if ((unsigned)block >= (unsigned)p.num_blocks) continue;
-                    isv[q] = hk >= (unsigned)p.H_kv;
-                    const int64_t bh = (int64_t)block * p.H_kv + (isv[q] ? hk - p.H_kv : hk);
-                    at[q] = (bh << lgper) + (i & ((1 << lgper) - 1));
-                    c[q] = __ldg(static_cast<const uint4*>(isv[q] ? p.V : p.K) + at[q]);
-                    sc[q] = __ldg((isv[q] ? x.Vsc : x.Ksc) + bh);
+            for (int q = 0; q < ILP; ++q) {
+                const int64_t i = i0 + q * READ_THREADS;
+                at_piece[q] = -1;
+                if (i >= total) continue;
+                int k = 0, hi = found - 1;  // the first entry that ends behind the piece
+                while (k < hi) {
+                    const int mid = (k + hi) >> 1;
+                    if (end_s[mid] <= i) k = mid + 1; else hi = mid;
                 }
+                const int64_t w = i - (k > 0 ? end_s[k - 1] : 0);
+                const unsigned g = (unsigned)(w >> lgper), j = g / (unsigned)heads, hk = g - j * heads;
+                const int block = __ldg(p.table + (size_t)seq_s[k] * p.max_blocks + j0_s[k] + j);
+                if ((unsigned)block >= (unsigned)p.num_blocks) continue;
+                isv[q] = hk >= (unsigned)p.H_kv;
+                const int64_t bh = (int64_t)block * p.H_kv + (isv[q] ? hk - p.H_kv : hk);
+                at_piece[q] = (bh << lgper) + (w & ((1 << lgper) - 1));
+                c[q] = __ldg(static_cast<const uint4*>(isv[q] ? p.V : p.K) + at_piece[q]);
+                sc[q] = __ldg((isv[q] ? x.Vsc : x.Ksc) + bh);
+            }
 #pragma unroll
-                for (int q = 0; q < ILP; ++q) {
-                    if (at[q] < 0) continue;
-                    uint4 o[16 / VEC];
-                    q8_widen16<T>(c[q], sc[q], o);
+            for (int q = 0; q < ILP; ++q) {
+                if (at_piece[q] < 0) continue;
+                uint4 o[16 / VEC];
+                q8_widen16<T>(c[q], sc[q], o);
 #pragma unroll
-                    for (int v = 0; v < 16 / VEC; ++v) static_cast<uint4*>(isv[q] ? x.V : x.K)[at[q] * (16 / VEC) + v] = o[v];
-                }
+                for (int v = 0; v < 16 / VEC; ++v) static_cast<uint4*>(isv[q] ? x.V : x.K)[at_piece[q] * (16 / VEC) + v] = o[v];
             }
         }
     }

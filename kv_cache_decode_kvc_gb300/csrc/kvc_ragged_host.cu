@@ -52,8 +52,9 @@ kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, Path path) {
 }
 // On an 8-bit cache, entries (sequences, shared prefixes) with more query rows per head than this are widened to bf16
 // and attended by the kernel of plain pools: per 32 rows it takes a quarter of the time of the kernel on codes, which
-// makes up for the widening at about a hundred rows.
-constexpr int MANY_ROWS = 128;
+// has to make up for the widening and for merging its larger pieces (64 sequences of 32 to 160 rows on one KV head
+// take XXX us at 128, YYY at 256).
+constexpr int MANY_ROWS = 256;
 // Is that worth its launches (three, some 8 us with nothing to do)?  The host knows how many rows an entry can have if every
 // sequence has a token, no more; a batch whose sequences have none, against that, is attended on codes all the same.
 bool many_rows(const kvc_cache* h, int N, int NG) {

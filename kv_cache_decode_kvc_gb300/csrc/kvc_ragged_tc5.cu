@@ -855,6 +855,10 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + set * 128 + lanes, tO = tmem + 256 + set * D + half * C::HD + lanes;
         const float c = p.qscale;
+        // Binades that a row's maximum may grow by before its reference follows.  (Weights against a lower reference keep
+        // their relative precision; only the room for sums of large values shrinks.  An 8-bit cache's keys differ
+        // in size from block to block: with 8 there a chunk of 2048 tokens behind 12,288 positions took XXX us, with 16 YYY.)
+        const float slack = p.part == 2 ? 16.f : 8.f;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_ts * 2)) & 31) == 0;
         uint32_t ns = 0, no = 0;
         int sc = 0;  // segments of class 1 begun
@@ -900,7 +904,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     *mine = top;
                     named_bar_sync(bar, 64);
                     top = fmaxf(top, *other);
-                    const bool raise = (top - m) * c > 8.f;
+                    const bool raise = (top - m) * c > slack;
                     if (__any_sync(ALL, raise)) {
                         const float mn = raise ? top : m;
                         const float f = raise ? fast_exp2((m - mn) * c) : 1.f;

@@ -42,8 +42,8 @@ CASES = [
     ([1, 4, 70], [100, 333, 12], 32, 4, 2, 64, "bf16"),
     ([1] * 40, list(range(0, 800, 20)), 16, 8, 8, 64, "bf16"),
     ([1, 9], [70, 20], 64, 4, 1, 256, "bf16"),
-    ([1, 400, 2, 33, 32], [300, 100, 0, 60, 7], 32, 8, 2, 128, "bf16"),  # 129 and 128 rows a head: either side of a rule
-    ([1, 400, 2, 33, 32], [300, 100, 0, 60, 7], 128, 8, 2, 64, "bf16"),
+    ([1, 400, 2, 65, 64], [300, 100, 0, 60, 7], 32, 8, 2, 128, "bf16"),  # 260 and 256 rows a head: either side of a rule
+    ([1, 400, 2, 65, 64], [300, 100, 0, 60, 7], 128, 8, 2, 64, "bf16"),
     ([0] * 150 + [140] + [0] * 49, [3] * 150 + [500] + [9] * 49, 64, 4, 2, 128, "bf16"),  # a chunk alone in a wide batch
     ([1, 6, 40], [200, 0, 77], 32, 4, 2, 64, "f32"),
     ([2, 1], [0, 130], 16, 2, 1, 128, "f32"),
@@ -63,9 +63,9 @@ def test_against_64_bits(kvc, new, hist, bs, H_q, H_kv, D, dtype, math):
     ([1, 2, 1, 3], [200, 210, 64, 90], [0, 2, 4], [160, 64], 16, 8, 1, 128),
     ([1, 5, 1], [600, 513, 512], [0, 3], [512], 128, 32, 1, 64),
     ([40, 1, 1], [130, 129, 400], [0, 3], [128], 64, 8, 2, 128),
-    # prefixes and sequences of more than 128 rows a head, in every combination with fewer
-    ([1] * 40 + [60, 1], [300 + i for i in range(40)] + [70, 90], [0, 40, 42], [272, 64], 16, 8, 2, 128),
-    ([1] * 40 + [60, 1, 1], [300 + i for i in range(40)] + [70, 90, 3], [0, 40, 42, 43], [256, 0, 0], 32, 8, 2, 64),
+    # prefixes and sequences of more than 256 rows a head, in every combination with fewer
+    ([1] * 80 + [70, 1], [300 + i for i in range(80)] + [70, 90], [0, 80, 82], [272, 64], 16, 8, 2, 128),
+    ([1] * 80 + [70, 1, 1], [300 + i for i in range(80)] + [70, 90, 3], [0, 80, 82, 83], [256, 0, 0], 32, 8, 2, 64),
     ([3, 1, 2, 1, 1, 4], [2050, 2048, 3000, 2200, 2300, 2064], [0, 6], [2048], 64, 32, 1, 128),
 ])
 @pytest.mark.parametrize("math", [0, 1])
