@@ -115,9 +115,7 @@ def header_symbols() -> list[str]:
 
 # ----------------------------------------------------------------------------- marshalling
 def _ptr(x) -> int:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     return x.data_ptr()
 
@@ -556,20 +554,22 @@ class Rope:
 
 def _packed(t, heads, D, dtype, what, dev=None):
     """Elements between tokens of a packed [N, heads, D] tensor."""
-    sh, st = t.shape, t.stride()
+    st = t.stride()
     if dev is None:
         dev = _device() if t.is_cuda else 0
-    if len(sh) != 3 or sh[1] != heads or sh[2] != D or t.dtype != dtype or t.get_device() != dev:
+    sh = t.shape
+    if len(st) != 3 or sh[1] != heads or sh[2] != D or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{what}: want [N, {heads}, {D}] {dtype} on the GPU (the current device), got {tuple(sh)} {t.dtype} on {t.device}")
-    if st[2] != 1 or (st[1] != D and heads > 1):
+    s0, s1, s2 = st
+    if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous, got strides {st}")
-    return st[0] if sh[0] > 1 else max(st[0], heads * D)
+    return s0 if sh[0] > 1 else max(s0, heads * D)
 
 
 def _index(t, what, int32, *shape, dev=None):
     if dev is None:
         dev = _device() if t.is_cuda else 0
-    if t.dtype != int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+    if t.dtype is not int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{what}: want contiguous int32 {list(shape)} on the GPU (the current device), got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
 
@@ -606,9 +606,15 @@ class PagedKVCache(KVCache):
 
 
     def _batch(self, block_table, cu_seqlens, lens, int32, dev):
-        _index(block_table, "block_table", int32, self.B, self.max_blocks, dev=dev)
-        _index(cu_seqlens, "cu_seqlens", int32, self.B + 1, dev=dev)
-        _index(lens, "lens", int32, self.B, dev=dev)
+        # (checked in one go: the call by call checks below only say what is wrong)
+        B = self.B
+        if not (block_table.dtype is int32 and cu_seqlens.dtype is int32 and lens.dtype is int32 and
+                block_table.shape == (B, self.max_blocks) and cu_seqlens.shape == (B + 1,) and lens.shape == (B,) and
+                block_table.get_device() == cu_seqlens.get_device() == lens.get_device() == dev and
+                block_table.is_contiguous() and cu_seqlens.is_contiguous() and lens.is_contiguous()):
+            _index(block_table, "block_table", int32, B, self.max_blocks, dev=dev)
+            _index(cu_seqlens, "cu_seqlens", int32, B + 1, dev=dev)
+            _index(lens, "lens", int32, B, dev=dev)
 
     def append_rope(self, layer, rope, q, k, v, block_table, cu_seqlens, lens, q_out=None, positions=None,
                     stream=None, q_norm=None, k_norm=None, norm_eps=1e-6):
@@ -654,8 +660,7 @@ class PagedKVCache(KVCache):
             stream = _current_stream(dev)
         if q_norm is not None or k_norm is not None or rope is None:
             for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-                if t is not None and (tuple(t.shape) != (D,) or t.dtype != dt or not t.is_contiguous() or
-                                      t.get_device() != dev):
+                if t is not None and (t.shape != (D,) or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous()):
                     raise ValueError(f"{what}: want contiguous [{D}] {dt} on the GPU (the current device), got "
                                      f"{list(t.shape)} {t.dtype} on {t.device}")
             kvc_paged_append_norm_rope(self.h, layer, None if rope is None else rope.r, q_norm, k_norm, norm_eps, q, qs,
