@@ -7,8 +7,11 @@
 
 namespace kvc {
 
-// Two finite values, or any, as codes: infinite and NaN values are stored as NaN (E4M3 has no infinity).
-__device__ __forceinline__ uint32_t q8_codes2(float x, float y, float mul, float lim) {
+// Two values as codes.  (mul: 2^-e; out of range is the largest code.)
+__device__ __forceinline__ uint32_t q8_codes2(float x, float y, float mul) { return e4m3x2(x * mul, y * mul); }
+// The same where infinities occur, which are stored as NaN (E4M3 has none), or where the largest code would read back as
+// one.
+__device__ __forceinline__ uint32_t q8_codes2_any(float x, float y, float mul, float lim) {
     const float nan = __uint_as_float(0x7FFFFFFFu);
     const float a = isfinite(x) ? fminf(fmaxf(x * mul, -lim), lim) : nan;
     const float b = isfinite(y) ? fminf(fmaxf(y * mul, -lim), lim) : nan;
@@ -22,24 +25,36 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t c, float mul) {
 
 // The new rows of one block and some of its heads, K and V: a CTA's share of the keys' and values' append.
 // Sequence b's blocks are items cu[b] / bs + 2 b, .. (floor(T / bs) + 2 places hold the blocks that T rows
-// touch), so no sum over the sequences is needed.  The rows' pieces (two 16-byte vectors, as in append_rows)
-// are all read at once, up to Q8_HELD of a thread; the first pass finds each head's largest |x| of
-// K, normalised and rotated, and of V; then the scales are settled, and the second pass, from the same
-// registers, stores the codes.  A block that holds earlier rows and needs a larger scale has their codes
-// moved down.
-constexpr int Q8_HELD = 8;
+// touch), so no sum over the sequences is needed.  The angles of 4096 pairs (64 rows at D = 128) are turned into
+// cosines and sines at a time, once for the CTA's heads where that is all of them.  K or V of a head is a unit of one warp (of two or four where heads are few or blocks long), which goes
+// over its rows twice: first for the largest |x| of K, normalised and rotated, or of V, which settles the scale, then, from
+// L1, for the codes.  (Values held in registers between the passes spilled, or left too few warps: 9700 rows of 32 + 8
+// heads took 112 to 129 us so, and 81 us with a CTA's heads laid out as pieces and a maximum exchanged for each.)  A block
+// that holds earlier rows and needs a larger scale has their codes moved down.
+constexpr int APPEND8_THREADS = 256, APPEND8_WARPS = APPEND8_THREADS / 32;
+struct Append8Grid {
+    int nkv, groups, hg, rounds, wpu, chunk;  // CTAs of keys and values; groups of `rounds` times hg heads; warps of a unit; rows
+                                           // whose angles are held
+};
 
 template <typename T, bool NORM>
-__device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTable& rt, int item, int h_first, int nh,
-                                              bool table_fits, float2* trig) {
-    constexpr int VEC = Elem<T>::VEC, NT = ROPE_THREADS;
+__device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTable& rt, int item, int h_first, int h_count,
+                                              const Append8Grid& grid, float* trig) {
+    constexpr int VEC = Elem<T>::VEC, NT = APPEND8_THREADS;
     __shared__ int found;
-    __shared__ uint32_t amax[32];
-    __shared__ float mul_s[32], lim_s[32], down_s[32];
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ uint32_t amax[2][APPEND8_WARPS];  // of a round's units, of two rounds in turn
+    __shared__ uint64_t freq_s[128];  // (from the parameters, where each lane's is another, a warp's loads go one by one)
+    __shared__ uint8_t axis_s[128];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pairs = rt.rot_dim / 2, nrot = rt.rot_dim / (2 * VEC);
     if (tid == 0) found = 0;
-    if (tid < 32) amax[tid] = 0;
+    if (tid < 2 * APPEND8_WARPS) amax[tid / APPEND8_WARPS][tid % APPEND8_WARPS] = 0;
+    if (tid < pairs) {
+        freq_s[tid] = rt.freq[tid];
+        axis_s[tid] = rt.axis[tid];
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the queries' grid of the same append, see `late`)
     __syncthreads();
     bool bad = false;
     int cnt = 0;
@@ -70,224 +85,227 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
         if (tid == 0) atomicOr(p.err, DEV_BAD_BLOCK);
         return;
     }
-    const int per = p.D / (2 * VEC), lg = 31 - __clz(per);
-    const int half = nrow * per, total = 2 * nh * half;  // a head's K pieces, and its V pieces
-    const int pairs = rt.rot_dim / 2, nrot = rt.rot_dim / (2 * VEC);
-    auto piece = [&](int i, int& hk, int& row, int& u) {
-        const int g = i >> lg;
-        u = i & (per - 1);
-        hk = g / nrow;
-        row = g - hk * nrow;
-    };
-    auto vectors = [&](int hk, int u, int& v0, int& v1) {
-        const bool halves = !(hk & 1) && u < nrot && !rt.adjacent;
-        v0 = halves ? u : 2 * u;
-        v1 = halves ? u + nrot : 2 * u + 1;
-    };
-    auto load = [&](int i, uint4& a, uint4& bb) {
-        int hk, row, u, v0, v1;
-        piece(i, hk, row, u);
-        vectors(hk, u, v0, v1);
-        const int h = h_first + (hk >> 1);
-        const T* src = hk & 1 ? static_cast<const T*>(p.v) + (r0 + row) * p.v_ts + (int64_t)h * p.D
-                              : static_cast<const T*>(p.k) + (r0 + row) * p.k_ts + (int64_t)h * p.D;
-        a = __ldg(reinterpret_cast<const uint4*>(src) + v0);
-        bb = __ldg(reinterpret_cast<const uint4*>(src) + v1);
-    };
-    uint4 xa[Q8_HELD], xb[Q8_HELD];
-#pragma unroll
-    for (int q = 0; q < Q8_HELD; ++q)
-        if (tid + q * NT < total) load(tid + q * NT, xa[q], xb[q]);
-    auto angle = [&](int row, int pr) {
-        const int pos = p.positions ? __ldg(p.positions + (int64_t)rt.axis[pr] * p.pos_ts + r0 + row) : lo + row;
-        const uint64_t turn = (uint64_t)(int64_t)pos * rt.freq[pr];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-        return make_float2(c * rt.scale, s * rt.scale);
-    };
-    if (table_fits)
-        for (int i = tid; i < nrow * pairs; i += NT) {
-            const int row = i / pairs;
-            trig[i] = angle(row, i - row * pairs);
+    const int chunk = min(grid.chunk, nrow), nchunk = (nrow + grid.chunk - 1) / grid.chunk;
+    float* cosines = trig;
+    float* sines = trig + chunk * pairs;
+    // the angles of rows [row, row + chunk), by all threads
+    auto angles_of = [&](int row) {
+        __syncthreads();
+        for (int i = tid; i < min(chunk, nrow - row) * pairs; i += NT) {
+            const int t = i / pairs, pr = i - t * pairs;
+            const int pos = p.positions ? __ldg(p.positions + (int64_t)axis_s[pr] * p.pos_ts + r0 + row + t) : lo + row + t;
+            const uint64_t turn = (uint64_t)(int64_t)pos * freq_s[pr];
+            float s, c;
+            sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+            cosines[i] = c * rt.scale;
+            sines[i] = s * rt.scale;
         }
-    __syncthreads();
-    // the values that piece i stands for, in fp32
-    auto values = [&](int i, const uint4& a, const uint4& bb, float (&x)[VEC], float (&y)[VEC], int& hk, int& row, int& v0,
-                      int& v1) {
-        int u;
-        piece(i, hk, row, u);
-        vectors(hk, u, v0, v1);
-        Elem<T>::unpack(a, x);
-        Elem<T>::unpack(bb, y);
-        if (hk & 1) return;
-        if (NORM && p.k_norm) norm_piece<T>(x, y, p.k_norm, v0, v1, per, p.D, p.eps);
-        if (u >= nrot) return;
-        const float2* tr = trig + row * pairs + u * VEC;
-        auto at = [&](int q) { return table_fits ? tr[q] : angle(row, u * VEC + q); };
-        if (!rt.adjacent) {
+        __syncthreads();
+    };
+    if (nchunk == 1) angles_of(0);
+    // A unit's pieces: a lane's are at one place of the rows' heads, v0 and v1, rows `row0`, row0 + step, ..
+    const int per = p.D / (2 * VEC), lg = 31 - __clz(per), u = lane & (per - 1);
+    const int unit = warp / grid.wpu, part = warp - unit * grid.wpu;
+    const bool isv = unit & 1, halves = !isv && u < nrot && !rt.adjacent;
+    const int v0 = halves ? u : 2 * u, v1 = halves ? u + nrot : 2 * u + 1;
+    const int row0 = (part << (5 - lg)) + (lane >> lg), step = grid.wpu << (5 - lg);
+    const bool normed = NORM && p.k_norm && !isv, turned = !isv && u < nrot;
+    uint4 wx = make_uint4(0, 0, 0, 0), wy = wx;
+    if (normed) {
+        wx = __ldg(static_cast<const uint4*>(p.k_norm) + v0);
+        wy = __ldg(static_cast<const uint4*>(p.k_norm) + v1);
+    }
+    for (int rd = 0; rd < grid.rounds; ++rd) {
+        const int hl = rd * grid.hg + (unit >> 1);  // the unit's head, of this CTA's
+        const bool live = unit < 2 * grid.hg && hl < h_count;
+        const int h = h_first + hl;
+        const T* src = isv ? static_cast<const T*>(p.v) + r0 * p.v_ts + (int64_t)h * p.D
+                           : static_cast<const T*>(p.k) + r0 * p.k_ts + (int64_t)h * p.D;
+        const int64_t ts = isv ? p.v_ts : p.k_ts;
+        // Row `row`'s values at this lane's place; the angles held begin at row `from`.
+        auto values = [&](int row, int from, const uint4& a, const uint4& bb, float (&x)[VEC], float (&y)[VEC]) {
+            Elem<T>::unpack(a, x);
+            Elem<T>::unpack(bb, y);
+            if (normed)  // (alike in a warp, whose lanes stay together)
+                norm_piece<T>(x, y, wx, wy, norm_factor<VEC>(x, y, per, 1.f / (float)p.D, p.eps));
+            if (!turned) return;
+            const float *cr = cosines + (row - from) * pairs + u * VEC, *sr = sines + (row - from) * pairs + u * VEC;
+            float co[VEC], si[VEC];
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                const float2 t = at(q);
-                const float f = x[q], g = y[q];
-                x[q] = f * t.x - g * t.y;
-                y[q] = g * t.x + f * t.y;
+            for (int q = 0; q < VEC; q += 4) {
+                *reinterpret_cast<float4*>(co + q) = *reinterpret_cast<const float4*>(cr + q);
+                *reinterpret_cast<float4*>(si + q) = *reinterpret_cast<const float4*>(sr + q);
             }
-        } else {
+            turn_piece<VEC>(x, y, co, si, !rt.adjacent);
+        };
+        uint32_t* tops = amax[rd & 1];
+        char* codes = static_cast<char*>(isv ? p.Vc : p.Kc) + (((int64_t)e * p.H_kv + h) * p.bs) * p.D;
+        char* dst = codes + (lo - start) * p.D;
+        float mul = 0.f, lim = 0.f, down = 1.f;
+        bool infinite = false;
+        // Pass 0: the largest |x|; 1: the largest finite one, if that was none; 2: the codes.  (One copy of the code: with
+        // one for each pass the values did not fit the registers.)
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            if (pass == 1 && !infinite) continue;
+            float m = 0.f;
+            // this lane's rows, two loaded at once; all of the block come along for the angles
+            for (int from = 0; from < nrow; from += chunk) {
+                if (nchunk > 1) angles_of(from);
+                if (!live) continue;
+                const int end = min(from + chunk, nrow);
+                for (int first = from + row0 - (lane >> lg); first < end; first += 2 * step) {  // (the warp's first row)
+                    uint4 a[2], bb[2];
 #pragma unroll
-            for (int q = 0; q < VEC / 2; ++q) {
-                const float2 t = at(q), t2 = at(q + VEC / 2);
-                const float f = x[2 * q], g = x[2 * q + 1], f2 = y[2 * q], g2 = y[2 * q + 1];
-                x[2 * q] = f * t.x - g * t.y;
-                x[2 * q + 1] = g * t.x + f * t.y;
-                y[2 * q] = f2 * t2.x - g2 * t2.y;
-                y[2 * q + 1] = g2 * t2.x + f2 * t2.y;
+                    for (int q = 0; q < 2; ++q) {
+                        const int row = first + (lane >> lg) + q * step;
+                        a[q] = bb[q] = make_uint4(0, 0, 0, 0);
+                        if (row < end) {
+                            const uint4* at = reinterpret_cast<const uint4*>(src + row * ts);
+                            a[q] = __ldg(at + v0);
+                            bb[q] = __ldg(at + v1);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (first + q * step >= end) continue;
+                        const int row = min(first + (lane >> lg) + q * step, end - 1);
+                        float x[VEC], y[VEC];
+                        values(row, from, a[q], bb[q], x, y);
+                        if (first + (lane >> lg) + q * step >= end) continue;
+                        if (pass == 0) {  // (a maximum passes NaN over)
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
+                        } else if (pass == 1) {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) {
+                                m = isfinite(x[i]) ? fmaxf(m, fabsf(x[i])) : m;
+                                m = isfinite(y[i]) ? fmaxf(m, fabsf(y[i])) : m;
+                            }
+                        } else {
+                            uint32_t w[VEC / 4], z[VEC / 4];
+#pragma unroll
+                            for (int i = 0; i < VEC / 4; ++i) {
+                                const int k = 4 * i;
+                                if (lim == 0.f) {
+                                    w[i] = q8_codes2(x[k], x[k + 1], mul) | q8_codes2(x[k + 2], x[k + 3], mul) << 16;
+                                    z[i] = q8_codes2(y[k], y[k + 1], mul) | q8_codes2(y[k + 2], y[k + 3], mul) << 16;
+                                } else {
+                                    w[i] = q8_codes2_any(x[k], x[k + 1], mul, lim) | q8_codes2_any(x[k + 2], x[k + 3], mul, lim) << 16;
+                                    z[i] = q8_codes2_any(y[k], y[k + 1], mul, lim) | q8_codes2_any(y[k + 2], y[k + 3], mul, lim) << 16;
+                                }
+                            }
+                            char* to = dst + row * p.D;
+                            if constexpr (VEC == 8) {
+                                *reinterpret_cast<uint2*>(to + v0 * VEC) = make_uint2(w[0], w[1]);
+                                *reinterpret_cast<uint2*>(to + v1 * VEC) = make_uint2(z[0], z[1]);
+                            } else {
+                                *reinterpret_cast<uint32_t*>(to + v0 * VEC) = w[0];
+                                *reinterpret_cast<uint32_t*>(to + v1 * VEC) = z[0];
+                            }
+                        }
+                    }
+                }
             }
+            if (pass == 2) break;
+            uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+            if (live && lane == 0) atomicMax(&tops[unit], top);
+            __syncthreads();
+            if (live) top = tops[unit];
+            if (pass == 0) {
+                if (tid < APPEND8_WARPS) amax[(rd & 1) ^ 1][tid] = 0;
+                infinite = __syncthreads_or(live && top >= 0x7F800000u) != 0;
+                if (infinite) {
+                    if (tid < APPEND8_WARPS) tops[tid] = 0;
+                    __syncthreads();
+                    continue;
+                }
+            }
+            float* sc = (isv ? p.Vsc : p.Ksc) + (int64_t)e * p.H_kv + h;
+            int x = q8_exponent(top);
+            if (live && held > 0) {
+                const int old = q8_stored(__float_as_uint(*sc));
+                if (old >= x) x = old;
+                else down = exp2i(max(old - x, -60));
+            }
+            // (a unit's warps have all read the old scale before one of them stores the new one)
+            if (grid.wpu > 1) __syncthreads();
+            if (live && part == 0 && lane == 0) *sc = exp2i(x);
+            mul = exp2i(-x);
+            if (infinite || x == Q8_EMAX) lim = x == Q8_EMAX ? 240.f : 448.f;  // (256 2^120 is past the largest float)
         }
-    };
-    auto largest = [&](int i, const uint4& a, const uint4& bb) {
-        float x[VEC], y[VEC];
-        int hk, row, v0, v1;
-        values(i, a, bb, x, y, hk, row, v0, v1);
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            const uint32_t f = __float_as_uint(x[q]) & 0x7FFFFFFFu, g = __float_as_uint(y[q]) & 0x7FFFFFFFu;
-            if (f < 0x7F800000u) m = max(m, f);
-            if (g < 0x7F800000u) m = max(m, g);
-        }
-        const uint32_t mask = (per == 32 ? 0xFFFFFFFFu : (1u << per) - 1u) << (lane & ~(per - 1));
-        for (int off = per >> 1; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(mask, m, off));
-        if ((lane & (per - 1)) == 0) atomicMax(&amax[hk], m);
-    };
-#pragma unroll
-    for (int q = 0; q < Q8_HELD; ++q)
-        if (tid + q * NT < total) largest(tid + q * NT, xa[q], xb[q]);
-    for (int i = tid + Q8_HELD * NT; i < total; i += NT) {
-        uint4 a, bb;
-        load(i, a, bb);
-        largest(i, a, bb);
-    }
-    __syncthreads();
-    if (tid < 2 * nh) {
-        float* sc = (tid & 1 ? p.Vsc : p.Ksc) + (int64_t)e * p.H_kv + h_first + (tid >> 1);
-        int x = q8_exponent(amax[tid]);
-        float down = 1.f;
-        if (held > 0) {
-            const int old = q8_stored(__float_as_uint(*sc));
-            if (old >= x) x = old;
-            else down = exp2i(max(old - x, -60));
-        }
-        *sc = exp2i(x);
-        mul_s[tid] = exp2i(-x);
-        lim_s[tid] = x == Q8_EMAX ? 240.f : 448.f;  // (256 2^120 is past the largest float)
-        down_s[tid] = down;
-    }
-    __syncthreads();
-    auto codes_of = [&](int hk) {
-        char* pool = static_cast<char*>(hk & 1 ? p.Vc : p.Kc);
-        return pool + (((int64_t)e * p.H_kv + h_first + (hk >> 1)) * p.bs) * p.D;
-    };
-    auto store = [&](int i, const uint4& a, const uint4& bb) {
-        float x[VEC], y[VEC];
-        int hk, row, v0, v1;
-        values(i, a, bb, x, y, hk, row, v0, v1);
-        const float mul = mul_s[hk], lim = lim_s[hk];
-        char* dst = codes_of(hk) + (lo - start + row) * p.D;
-        uint32_t w[VEC / 4], z[VEC / 4];
-#pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) {
-            w[q] = q8_codes2(x[4 * q], x[4 * q + 1], mul, lim) | q8_codes2(x[4 * q + 2], x[4 * q + 3], mul, lim) << 16;
-            z[q] = q8_codes2(y[4 * q], y[4 * q + 1], mul, lim) | q8_codes2(y[4 * q + 2], y[4 * q + 3], mul, lim) << 16;
-        }
-        if constexpr (VEC == 8) {
-            *reinterpret_cast<uint2*>(dst + v0 * VEC) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(dst + v1 * VEC) = make_uint2(z[0], z[1]);
-        } else {
-            *reinterpret_cast<uint32_t*>(dst + v0 * VEC) = w[0];
-            *reinterpret_cast<uint32_t*>(dst + v1 * VEC) = z[0];
-        }
-    };
-#pragma unroll
-    for (int q = 0; q < Q8_HELD; ++q)
-        if (tid + q * NT < total) store(tid + q * NT, xa[q], xb[q]);
-    for (int i = tid + Q8_HELD * NT; i < total; i += NT) {
-        uint4 a, bb;
-        load(i, a, bb);
-        store(i, a, bb);
-    }
-    if (held > 0)
-        for (int hk = 0; hk < 2 * nh; ++hk) {
-            const float down = down_s[hk];
-            if (down == 1.f) continue;
-            uint4* c = reinterpret_cast<uint4*>(codes_of(hk));
-            for (int i = tid; i < held * (p.D / 16); i += NT) {
+        if (live && down != 1.f) {
+            uint4* c = reinterpret_cast<uint4*>(codes);
+            for (int i = part * 32 + lane; i < held * (p.D / 16); i += 32 * grid.wpu) {
                 const uint4 w = c[i];
                 c[i] = make_uint4(q8_rescale4(w.x, down), q8_rescale4(w.y, down), q8_rescale4(w.z, down),
                                   q8_rescale4(w.w, down));
             }
         }
-}
-
-// Blocks [0, nkv) append keys and values (nkv / groups items, heads in groups of hg), the others rotate the
-// queries, TB rows each.
-struct Append8Grid {
-    int nkv, groups, hg, table_fits;
-};
-template <typename T, int TB, bool NORM>
-__global__ void __launch_bounds__(ROPE_THREADS, 2)
-append8_kernel(const RopeParams p, const __grid_constant__ RopeTable rt, const Append8Grid g) {
-    extern __shared__ __align__(16) float2 trig8[];
-    if (blockIdx.x < g.nkv) {
-        const int item = blockIdx.x / g.groups, h = (blockIdx.x - item * g.groups) * g.hg;
-        append8_block<T, NORM>(p, rt, item, h, min(g.hg, p.H_kv - h), g.table_fits != 0, trig8);
-    } else {
-        RopeParams q = p;  // the queries alone
-        q.H_kv = 0;
-        append_rows<T, TB, true, NORM>(q, rt, blockIdx.x - g.nkv);
     }
 }
 
-template <typename T, int TB, bool NORM>
-static int launch_append8_as(const RopeParams& p, const RopeTable& t, cudaStream_t s) {
-    constexpr int VEC = Elem<T>::VEC, TABLE = 64 << 10;
+// Blocks [0, nkv) append keys and values (nkv / groups items), the others rotate the queries, a row each (none in the
+// launch of many rows, where the queries have a kernel of their own, with more blocks an SM).
+template <typename T, bool NORM>
+__global__ void __launch_bounds__(APPEND8_THREADS, 2)
+append8_kernel(const RopeParams p, const __grid_constant__ RopeTable rt, const Append8Grid g) {
+    extern __shared__ __align__(16) float trig8[];
+    if (blockIdx.x < g.nkv) {
+        const int item = blockIdx.x / g.groups, each = g.hg * g.rounds, h = (blockIdx.x - item * g.groups) * each;
+        append8_block<T, NORM>(p, rt, item, h, min(each, p.H_kv - h), g, trig8);
+    } else {
+        RopeParams q = p;  // the queries alone
+        q.H_kv = 0;
+        append_rows<T, 1, true, NORM>(q, rt, blockIdx.x - g.nkv);
+    }
+}
+
+template <typename T, bool NORM>
+static int launch_append8_as(const RopeParams& p, const RopeTable& t, int sms, bool many, cudaStream_t s) {
     Append8Grid g;
-    const int per_head = 2 * p.bs * (p.D / (2 * VEC));
-    g.hg = Q8_HELD * ROPE_THREADS / per_head;
-    g.hg = g.hg < 1 ? 1 : g.hg > 16 ? 16 : g.hg;
-    if (g.hg > p.H_kv) g.hg = p.H_kv;
-    g.groups = (p.H_kv + g.hg - 1) / g.hg;
-    const int64_t items = p.N / p.bs + 2 * (int64_t)p.B, nkv = items * g.groups;
-    const int64_t nq = p.q ? ((int64_t)p.N + TB - 1) / TB : 0;
+    // heads at a time: a unit's warp gets some 64 rows at most
+    const int most = p.bs <= 64 ? 4 : p.bs == 128 ? 2 : 1;
+    g.hg = most;
+    while (g.hg > p.H_kv) g.hg /= 2;
+    g.wpu = APPEND8_WARPS / (2 * g.hg);
+    // the angles are shared by a CTA's heads: as many as leave the GPU some CTAs an SM
+    g.rounds = 1;
+    while (g.rounds * g.hg * 2 <= p.H_kv && (int64_t)(p.N / p.bs) * ((p.H_kv + 2 * g.rounds * g.hg - 1) / (2 * g.rounds * g.hg)) >= 4 * sms)
+        g.rounds *= 2;
+    g.groups = (p.H_kv + g.hg * g.rounds - 1) / (g.hg * g.rounds);
+    const int64_t nkv = (p.N / p.bs + 2 * (int64_t)p.B) * g.groups;
+    const int64_t nq = p.q && !many ? p.N : 0;
     if (nkv + nq > 0x7FFFFFFF) return (int)cudaErrorInvalidValue;
     g.nkv = (int)nkv;
-    const int table = p.bs * (t.rot_dim / 2) * (int)sizeof(float2);
-    g.table_fits = table <= TABLE;
-    static PerDeviceOnce once;
-    const int e0 = once.run([] {
-        return (int)cudaFuncSetAttribute(append8_kernel<T, TB, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, TABLE);
-    });
-    if (e0 != 0) return e0;
+    // rows whose angles are held: 4096 cosines and as many sines, 32 KB
+    const int pairs = t.rot_dim > 0 ? t.rot_dim / 2 : 1;
+    g.chunk = 4096 / pairs < p.bs ? 4096 / pairs : p.bs;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(nkv + nq));
-    cfg.blockDim = dim3(ROPE_THREADS);
-    cfg.dynamicSmemBytes = g.table_fits ? table : 0;
+    cfg.blockDim = dim3(APPEND8_THREADS);
+    cfg.dynamicSmemBytes = g.chunk * pairs * 2 * sizeof(float);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, append8_kernel<T, TB, NORM>, p, t, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, append8_kernel<T, NORM>, p, t, g);
     return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 int launch_append8(int dtype, const RopeParams& p, const RopeTable& t, int sms, cudaStream_t s) {
-    const bool norm = p.q_norm || p.k_norm, many = p.N >= 8 * sms;  // (as in kvc_rope.cu)
+    const bool norm = p.q_norm || p.k_norm, many = p.N >= 8 * sms;
     auto go = [&](auto tp) {
         using T = decltype(tp);
-        return many ? (norm ? launch_append8_as<T, 4, true>(p, t, s) : launch_append8_as<T, 4, false>(p, t, s))
-                    : (norm ? launch_append8_as<T, 1, true>(p, t, s) : launch_append8_as<T, 1, false>(p, t, s));
+        return norm ? launch_append8_as<T, true>(p, t, sms, many, s) : launch_append8_as<T, false>(p, t, sms, many, s);
     };
-    return dtype == 0 ? go(__nv_bfloat16()) : go(float());
+    const int e = dtype == 0 ? go(__nv_bfloat16()) : go(float());
+    if (e != 0 || !many || !p.q) return e;
+    RopeParams q = p;
+    q.H_kv = 0;
+    q.late = 1;
+    return launch_append_rope(dtype, q, t, sms, s);
 }
 
 // ------------------------------------------------------------------ reading back

@@ -26,12 +26,11 @@ constexpr int ROPE_THREADS = 256;
 // Bytes in flight decide: 16,000 bf16 rows of 80 heads take 105 us (5.9 TB/s, 0.89 of a copy's
 // rate) with two pieces ahead and 4 blocks an SM; 115 us with one piece, 110 with three (fewer
 // blocks fit), 131 with 5 blocks of fewer registers.
-// The norm of a head whose `per` pieces lie in neighbouring lanes, all of them here: this lane's are vectors v0 (x)
-// and v1 (y).
-template <typename T>
-__device__ __forceinline__ void norm_piece(float (&x)[Elem<T>::VEC], float (&y)[Elem<T>::VEC], const void* weight, int v0,
-                                           int v1, int per, int D, float eps) {
-    constexpr int VEC = Elem<T>::VEC;
+// 1 / sqrt(mean x^2 + eps) of a head whose `per` pieces lie in neighbouring lanes: this lane's two vectors x and
+// y.  rD = 1 / D (a power of two).  All lanes of the warp come along (shuffles of a part of them, found at run time,
+// cost the compiler's search for it: 14,000 rows of 80 heads took 105 to 120 us so).
+template <int VEC>
+__device__ __forceinline__ float norm_factor(const float (&x)[VEC], const float (&y)[VEC], int per, float rD, float eps) {
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -39,17 +38,91 @@ __device__ __forceinline__ void norm_piece(float (&x)[Elem<T>::VEC], float (&y)[
         s1 = fmaf(y[e], y[e], s1);
     }
     float sum = s0 + s1;
-    const int lane = threadIdx.x & 31;
-    const uint32_t mask = (per == 32 ? 0xFFFFFFFFu : (1u << per) - 1u) << (lane & ~(per - 1));
-    for (int off = per >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(mask, sum, off);
-    const float inv = rsqrtf(sum / (float)D + eps);
-    float w[VEC];
-    Elem<T>::unpack(__ldg(static_cast<const uint4*>(weight) + v0), w);
+    for (int off = per >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    return rsqrtf(fmaf(sum, rD, eps));
+}
+// The two vectors times that factor and their weights, 16-byte vectors at wx and wy.
+template <typename T>
+__device__ __forceinline__ void norm_piece(float (&x)[Elem<T>::VEC], float (&y)[Elem<T>::VEC], const uint4& wx, const uint4& wy,
+                                           float inv) {
+    float w[Elem<T>::VEC];
+    Elem<T>::unpack(wx, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] *= inv * w[e];
-    Elem<T>::unpack(__ldg(static_cast<const uint4*>(weight) + v1), w);
+    for (int e = 0; e < Elem<T>::VEC; ++e) x[e] *= inv * w[e];
+    Elem<T>::unpack(wy, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) y[e] *= inv * w[e];
+    for (int e = 0; e < Elem<T>::VEC; ++e) y[e] *= inv * w[e];
+}
+
+// The places of packed rows [r0, r0 + n), n at most the block's warps, which find one each: position in the sequence (-1:
+// skip the row) and pool row of head 0 (-1: not stored).  Checks cu as well.  Returns DEV_BAD_SEQ to all threads, or
+// to this one the error of its warp's row.  Ends with a barrier.
+__device__ __forceinline__ uint32_t find_rows(const RopeParams& p, int r0, int n, int64_t* krow, int* slots) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bool bad = false;
+    uint32_t flag = 0;  // (speaks of a row only once cu is known to be sound)
+    for (int b = tid; b <= p.B; b += ROPE_THREADS) {
+        const int c = __ldg(p.cu + b);
+        bad |= (b == 0 ? c != 0 : c < __ldg(p.cu + b - 1)) || c > p.N;
+    }
+    if (warp < n) {
+        // the row's sequence: the number of b with cu[b + 1] <= row
+        const int row = r0 + warp;
+        int b = 0;
+        for (int i = 0; i < p.B; i += 32)
+            b += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < p.B && __ldg(p.cu + i + lane + 1) <= row));
+        if (lane == 0) {
+            int slot = -1;
+            int64_t kr = -1;
+            if (b < p.B && row < p.N) {
+                const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
+                if (c0 >= 0 && c0 <= row && row < c1 && c1 <= p.N) {  // (else cu does not ascend within 0 .. N)
+                    if (L < c1 - c0 || L > p.T_max) {
+                        flag = DEV_BAD_LENS;
+                    } else {
+                        slot = L - (c1 - c0) + (row - c0);
+                        const int e = __ldg(p.table + (size_t)b * p.max_blocks + slot / p.bs);
+                        if ((unsigned)e >= (unsigned)p.num_blocks) flag = DEV_BAD_BLOCK;
+                        else kr = (int64_t)e * p.H_kv * p.bs + slot % p.bs;
+                    }
+                }
+            }
+            slots[warp] = slot;
+            krow[warp] = kr;
+        }
+    }
+    return __syncthreads_or(bad) ? DEV_BAD_SEQ : flag;
+}
+// Cosine and sine of pair j of packed row `row`, at `slot` of its sequence.
+__device__ __forceinline__ void row_angle(const RopeParams& p, const RopeTable& rt, int row, int slot, int j, float& c, float& s) {
+    const int pos = p.positions ? __ldg(p.positions + (int64_t)rt.axis[j] * p.pos_ts + row) : slot;
+    const uint64_t turn = (uint64_t)(int64_t)pos * rt.freq[j];
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    c *= rt.scale;
+    s *= rt.scale;
+}
+
+// A vector's pairs turned, with the vector of their other halves (halves) or each with its neighbour.
+template <int VEC>
+__device__ __forceinline__ void turn_piece(float (&x)[VEC], float (&y)[VEC], const float* co, const float* si, bool halves) {
+    if (halves) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float f = x[e], g = y[e];
+            x[e] = f * co[e] - g * si[e];
+            y[e] = g * co[e] + f * si[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const float c = co[e], s = si[e], c2 = co[e + VEC / 2], s2 = si[e + VEC / 2];
+            const float f = x[2 * e], g = x[2 * e + 1], f2 = y[2 * e], g2 = y[2 * e + 1];
+            x[2 * e] = f * c - g * s;
+            x[2 * e + 1] = g * c + f * s;
+            y[2 * e] = f2 * c2 - g2 * s2;
+            y[2 * e + 1] = g2 * c2 + f2 * s2;
+        }
+    }
 }
 
 // NORM: the heads of q and k are first divided by the root of their mean square (plus eps) and multiplied by a
@@ -107,57 +180,21 @@ __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable
         b = src[v1];
     };
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (VECTOR) {
 #pragma unroll
         for (int k = 0; k < PRE; ++k) load(tid + k * ROPE_THREADS, xa[k], xb[k]);
     }
-    bool bad = false;
-    uint32_t flag = 0;  // of this warp's row: set once cu is known to be sound, else it speaks of no row
-    for (int b = tid; b <= p.B; b += ROPE_THREADS) {
-        const int c = __ldg(p.cu + b);
-        bad |= (b == 0 ? c != 0 : c < __ldg(p.cu + b - 1)) || c > p.N;
-    }
-    if (warp < TB) {
-        // the row's sequence: the number of b with cu[b + 1] <= row
-        const int row = r0 + warp;
-        int b = 0;
-        for (int i = 0; i < p.B; i += 32)
-            b += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < p.B && __ldg(p.cu + i + lane + 1) <= row));
-        if (lane == 0) {
-            int slot = -1;
-            int64_t kr = -1;
-            if (b < p.B && row < p.N) {
-                const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.lens + b);
-                if (c0 >= 0 && c0 <= row && row < c1 && c1 <= p.N) {  // (else cu does not ascend within 0 .. N)
-                    if (L < c1 - c0 || L > p.T_max) {
-                        flag = DEV_BAD_LENS;
-                    } else {
-                        slot = L - (c1 - c0) + (row - c0);
-                        const int e = __ldg(p.table + (size_t)b * p.max_blocks + slot / p.bs);
-                        if ((unsigned)e >= (unsigned)p.num_blocks) flag = DEV_BAD_BLOCK;
-                        else kr = (int64_t)e * p.H_kv * p.bs + slot % p.bs;
-                    }
-                }
-            }
-            slot_s[warp] = slot;
-            krow[warp] = kr;
-        }
-    }
-    if (__syncthreads_or(bad)) {
+    const uint32_t flag = find_rows(p, r0, TB, krow, slot_s);
+    if (flag == DEV_BAD_SEQ) {
         if (bid == 0 && tid == 0) atomicOr(p.err, DEV_BAD_SEQ);
+        if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     if (flag) atomicOr(p.err, flag);
     for (int i = tid; i < TB * pairs; i += ROPE_THREADS) {
         const int t = i / pairs, j = i - t * pairs;
-        if (slot_s[t] < 0) continue;
-        const int pos = p.positions ? __ldg(p.positions + (int64_t)rt.axis[j] * p.pos_ts + r0 + t) : slot_s[t];
-        const uint64_t turn = (uint64_t)(int64_t)pos * rt.freq[j];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-        cs[t][j] = c * rt.scale;
-        sn[t][j] = s * rt.scale;
+        if (slot_s[t] >= 0) row_angle(p, rt, r0 + t, slot_s[t], j, cs[t][j], sn[t][j]);
     }
     __syncthreads();
 
@@ -171,51 +208,75 @@ __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable
                           : static_cast<T*>(p.Vc) + (krow[t] + (int64_t)(h - p.H_kv) * p.bs) * p.D;
     };
     if constexpr (VECTOR) {
-        for (int i0 = tid; i0 < total; i0 += PRE * ROPE_THREADS) {
+        // (NORM: a warp's lanes stay together for the norms' sums)
+        for (int i0 = tid; (NORM ? i0 - lane : i0) < total; i0 += PRE * ROPE_THREADS) {
 #pragma unroll
             for (int k = 0; k < PRE; ++k) {
                 const int i = i0 + k * ROPE_THREADS;
-                if (i >= total) continue;
+                if ((NORM ? i - lane : i) >= total) continue;
                 int t, head, u;
-                piece(i, t, head, u);
+                piece(NORM ? min(i, total - 1) : i, t, head, u);
                 T* dst = place(t, head);
                 uint4 a = xa[k], b = xb[k];
                 load(i + PRE * ROPE_THREADS, xa[k], xb[k]);
-                if (!dst) continue;
+                if (!NORM && !dst) continue;
                 int v0, v1;
                 vectors(u, v0, v1);
-                const void* weight = nullptr;
-                if constexpr (NORM) weight = head < h0 ? p.q_norm : head < h0 + p.H_kv ? p.k_norm : nullptr;
-                if ((head < h0 + p.H_kv && u < nrot) || weight) {
+                if constexpr (NORM) {
+                    const bool rot = head < h0 + p.H_kv && u < nrot;
+                    const void* weight = head < h0 ? p.q_norm : head < h0 + p.H_kv ? p.k_norm : nullptr;
                     float x[VEC], y[VEC];
                     Elem<T>::unpack(a, x);
                     Elem<T>::unpack(b, y);
-                    if (weight) norm_piece<T>(x, y, weight, v0, v1, per, p.D, p.eps);
-                    if (u < nrot) {
-                        float co[VEC], si[VEC];
+                    const float inv = norm_factor<VEC>(x, y, per, 1.f / (float)p.D, p.eps);
+                    if (!dst || i >= total) continue;
+                    if (rot || weight) {
+                        if (weight)
+                            norm_piece<T>(x, y, __ldg(static_cast<const uint4*>(weight) + v0),
+                                          __ldg(static_cast<const uint4*>(weight) + v1), inv);
+                        if (rot) {
+                            float co[VEC], si[VEC];
 #pragma unroll
-                        for (int e = 0; e < VEC; e += 4) {
-                            *reinterpret_cast<float4*>(co + e) = *reinterpret_cast<const float4*>(&cs[t][u * VEC + e]);
-                            *reinterpret_cast<float4*>(si + e) = *reinterpret_cast<const float4*>(&sn[t][u * VEC + e]);
+                            for (int e = 0; e < VEC; e += 4) {
+                                *reinterpret_cast<float4*>(co + e) = *reinterpret_cast<const float4*>(&cs[t][u * VEC + e]);
+                                *reinterpret_cast<float4*>(si + e) = *reinterpret_cast<const float4*>(&sn[t][u * VEC + e]);
+                            }
+                            turn_piece<VEC>(x, y, co, si, !rt.adjacent);
                         }
-                        if (!rt.adjacent) {
+                        a = Elem<T>::pack(x);
+                        b = Elem<T>::pack(y);
+                    }
+                    *(reinterpret_cast<uint4*>(dst) + v0) = a;
+                    *(reinterpret_cast<uint4*>(dst) + v1) = b;
+                    continue;
+                }
+                if (head < h0 + p.H_kv && u < nrot) {
+                    float x[VEC], y[VEC];
+                    Elem<T>::unpack(a, x);
+                    Elem<T>::unpack(b, y);
+                    float co[VEC], si[VEC];
 #pragma unroll
-                            for (int e = 0; e < VEC; ++e) {
-                                const float c = co[e], s = si[e];
-                                const float f = x[e], g = y[e];
-                                x[e] = f * c - g * s;
-                                y[e] = g * c + f * s;
-                            }
-                        } else {
+                    for (int e = 0; e < VEC; e += 4) {
+                        *reinterpret_cast<float4*>(co + e) = *reinterpret_cast<const float4*>(&cs[t][u * VEC + e]);
+                        *reinterpret_cast<float4*>(si + e) = *reinterpret_cast<const float4*>(&sn[t][u * VEC + e]);
+                    }
+                    if (!rt.adjacent) {
 #pragma unroll
-                            for (int e = 0; e < VEC / 2; ++e) {
-                                const float c = co[e], s = si[e], c2 = co[e + VEC / 2], s2 = si[e + VEC / 2];
-                                const float f = x[2 * e], g = x[2 * e + 1], f2 = y[2 * e], g2 = y[2 * e + 1];
-                                x[2 * e] = f * c - g * s;
-                                x[2 * e + 1] = g * c + f * s;
-                                y[2 * e] = f2 * c2 - g2 * s2;
-                                y[2 * e + 1] = g2 * c2 + f2 * s2;
-                            }
+                        for (int e = 0; e < VEC; ++e) {
+                            const float c = co[e], s = si[e];
+                            const float f = x[e], g = y[e];
+                            x[e] = f * c - g * s;
+                            y[e] = g * c + f * s;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC / 2; ++e) {
+                            const float c = co[e], s = si[e], c2 = co[e + VEC / 2], s2 = si[e + VEC / 2];
+                            const float f = x[2 * e], g = x[2 * e + 1], f2 = y[2 * e], g2 = y[2 * e + 1];
+                            x[2 * e] = f * c - g * s;
+                            x[2 * e + 1] = g * c + f * s;
+                            y[2 * e] = f2 * c2 - g2 * s2;
+                            y[2 * e + 1] = g2 * c2 + f2 * s2;
                         }
                     }
                     a = Elem<T>::pack(x);
@@ -300,6 +361,7 @@ __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable
             }
         }
     }
+    if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace kvc
