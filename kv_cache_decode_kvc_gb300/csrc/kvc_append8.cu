@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
     __shared__ int block_s[READ_ROWS], off_s[READ_ROWS];  // block: -1 zeros, -2 not a row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = blockIdx.x * READ_ROWS;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool bad = false;
     uint32_t flag = 0;
     for (int b = tid; b <= p.B; b += READ_THREADS) {
@@ -413,6 +414,7 @@ __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NE = p.B + (JOINT ? p.NG : 0);
     const int lgper = 31 - __clz(p.bs * p.D / 16), heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e0 = 0; e0 < NE; e0 += READ_THREADS) {
         const int e = e0 + tid;
         Entry s;

@@ -189,8 +189,8 @@ struct Ragged {
     // 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
     // (MANY, the kernel on codes: a tile of 32 rows takes 2.2 us, one of up to 8 that comes from memory 1.3; a stream's
     // start some three tiles of the latter.)
-    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : MANY > 0 ? (cl == 0 ? 5 : 3) : 1; }
-    __host__ __device__ static constexpr int start_cost(int cl) { return PAIRS ? (cl == 0 ? 6 : 3) : MANY > 0 ? 9 : 1; }
+    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : MANY > 0 ? (cl == 0 ? 7 : 3) : 1; }
+    __host__ __device__ static constexpr int start_cost(int cl) { return PAIRS ? (cl == 0 ? 6 : 3) : MANY > 0 ? (cl == 0 ? 24 : 7) : 1; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at

@@ -183,15 +183,17 @@ __device__ __forceinline__ void merge_two(const RaggedParams& p, int r0, int ste
     }
 }
 
-// Blocks that share the rows of a cut: a slot's rows for the warps of each.
+// Blocks that share the rows of a cut.  (One for 16 or 32 rows, which its warps hold at once: all cuts' blocks then run
+// in one go.)
 template <class R>
-constexpr int MERGE_SLICES = R::SLOT_ROWS < 8 * MERGE_WARPS ? R::SLOT_ROWS / MERGE_WARPS : 8;
+constexpr int MERGE_SLICES = R::SLOT_ROWS < 8 * MERGE_WARPS ? 1 : 8;
 // Without groups: block (c, y) takes the c-th possible cut; if a stream was cut there first, its
 // warps merge the rows of the stream's tile from row 8 y on, every 64th eight of them.  With many pieces
 // the blocks of all its cuts take its rows in turn, one by one.
 template <typename T, class R>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_cuts_kernel(const RaggedParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = R::SLOTS > 2 ? blockIdx.x : 3 * blockIdx.x + 1;
     const int4 a = __ldcg(p.cuts + 2 * e), b = __ldcg(p.cuts + 2 * e + 1);
@@ -235,6 +237,7 @@ __device__ __forceinline__ int last_at(const int* a, int n, int x, int lane) {
 template <typename T, class R>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const RaggedParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const typename R::Split sp = R::planned(p);
     if (!sp.valid) return;
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_rows_kernel(const Ragg
 template <typename T, class RA, class RB>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_parts_kernel(const RaggedParams pa, const RaggedParams pb) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const RaggedParams& p = pb;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const typename RA::Split spa = RA::planned(pa);
@@ -373,7 +377,9 @@ inline int launch_merge_parts(const RaggedParams& pa, const RaggedParams& pb, cu
     return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 
-// Launch behind the attention kernel; starts as that one ends.
+// Launch behind the attention kernel; starts as that one ends.  (The kernels here and around release their dependents
+// as soon as they have waited for their own predecessor: at most two grids of a stream are then under way, so a kernel
+// that reads ahead of its wait still has only the one before it to think of.)
 template <typename T, class R, bool JOINT>
 inline int launch_merge(const RaggedParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};

@@ -290,9 +290,8 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         const CUtensorMap* m = lane == 0 ? &tmK : &tmV;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
-    // (the merge's blocks wait for this grid's end in their places)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     typename R::Split sp;
     typename R::Walk wk;
     if (warp == 2) {
