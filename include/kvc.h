@@ -99,7 +99,8 @@ int kvc_decode_attn(kvc_t h, int layer, const void* q, void* out, const int32_t*
 int kvc_decode_step(kvc_t h, int layer, const void* q, const void* k_new, const void* v_new,
                     void* out, const int32_t* lens, void* stream);
 
-/* Allocated payload of the handle: 2 * layers * H_kv * D * B * T_max * elem_bytes. */
+/* Allocated payload of the handle: 2 * layers * H_kv * D * B * T_max * elem_bytes (paged: the pools; 8-bit caches: the
+ * codes, a byte each, without the scales). */
 uint64_t kvc_bytes(kvc_t h);
 
 /* The closed form 2 * L * H_kv * D * (B * T) * elem_bytes (no allocation, host only).
@@ -136,6 +137,7 @@ int kvc_set_combine_mode(kvc_t h, int mode);
  *   2 warp-level mma.sync tensor instructions (bf16 caches);
  *   3 tcgen05 tensor cores with tensor-memory accumulators (bf16 caches, D = 128).
  * Paths 2 and 3 need B*H_kv*T_max < 2^31 (tensor-map coordinates), else KVC_EUNSUPPORTED.
+ * A paged 8-bit cache takes 0, 1 and, for bf16 with D = 64 or 128, 3 (what 0 takes there).
  * All paths agree within the bf16 tolerance.  kvc_get_math returns the path the next call
  * takes (1, 2 or 3). */
 int kvc_set_math(kvc_t h, int mode);
@@ -356,12 +358,19 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * Values at positions a row does not see never reach it, whatever they are.  bf16 caches with D =
  * 64 or 128 run on the tcgen05 tensor cores: softmax weights enter the second product as two bf16
  * terms (within 2^-15 of a weight) for sequences, and shared prefixes, of up to 64 query rows per
- * KV head (tokens x H_q / H_kv, of a prefix all its group's), as one (2^-8) for larger ones.  Every other shape, or math mode 1, runs on CUDA cores in fp32.  ws is device scratch of at least
+ * KV head (tokens x H_q / H_kv, of a prefix all its group's), as one (2^-8) for larger ones.  Every other shape, or math
+ * mode 1, runs on CUDA cores in fp32.  On a paged 8-bit cache the tensor cores take the codes as they are: q as two E4M3
+ * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights as three
+ * E5M2 terms (within 2^-9 of a weight, or 2^-26 of the row's largest), and a row whose q has an infinity or a NaN is NaN;
+ * sequences and prefixes of more than 256 query rows per KV head are attended as on a bf16 cache, over blocks
+ * widened (exactly) in the scratch, where the call's N leaves room for more than 512; where the CUDA cores attend an
+ * 8-bit cache, all blocks are widened.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each.
  * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on
  * CUDA cores) by 128 positions (CUDA cores: 64 for D <= 64, else 32) that its last row sees.  A
- * call of more than 10^9 tiles (2 10^9 on CUDA cores; some 12 and 30 s of work) may be refused:
+ * call of more than 10^9 tiles (2 10^9 on CUDA cores; some 12 and 30 s of work; on an 8-bit cache's codes, in tiles of
+ * 32 rows by 128 positions, 256 for D = 64, 3 10^8) may be refused:
  * KVC_DEV_TOO_LARGE is set and nothing is written; give it fewer sequences or shorter chunks. */
 int kvc_paged_attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,
                           int64_t out_stride, const int32_t* block_table, const int32_t* cu_seqlens,
@@ -384,7 +393,9 @@ int kvc_paged_attn_shared(kvc_t h, int layer, const void* q, int64_t q_stride, v
                           void* stream);
 
 /* Scratch of the two attention calls for N rows and NG groups (NG = 0: kvc_paged_attn_ragged), at
- * the handle's present kvc_set_ctas setting. */
+ * the handle's present kvc_set_ctas setting; on an 8-bit cache, also its present kvc_set_math setting: where blocks are
+ * widened (above) the scratch holds a layer's pools in the cache's dtype besides, where not, it does not.  It does
+ * not shrink as N or NG grow. */
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes);
 
 /* Shape query: writes layers, B, H_q, H_kv, D, T_max, dtype (any pointer may be NULL). */

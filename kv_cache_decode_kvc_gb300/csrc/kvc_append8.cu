@@ -28,9 +28,10 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t c, float mul) {
 // touch), so no sum over the sequences is needed.  The angles of 4096 pairs (64 rows at D = 128) are turned into
 // cosines and sines at a time, once for the CTA's heads where that is all of them.  K or V of a head is a unit of one warp (of two or four where heads are few or blocks long), which goes
 // over its rows twice: first for the largest |x| of K, normalised and rotated, or of V, which settles the scale, then, from
-// L1, for the codes.  (Values held in registers between the passes spilled, or left too few warps: 9700 rows of 32 + 8
-// heads took 112 to 129 us so, and 81 us with a CTA's heads laid out as pieces and a maximum exchanged for each.)  A block
-// that holds earlier rows and needs a larger scale has their codes moved down.
+// L1, for the codes.  Bound by its chain of lookups, first pass, maximum and second pass, beside the memory's: 9700 rows of
+// 32 + 8 heads take 76 us with the queries' grid beside it, 2.9 TB/s.  (Values held in registers between the passes
+// spilled, or left too few warps: 112 to 129 us, and 81 with a CTA's heads laid out as pieces and a maximum exchanged
+// for each.)  A block that holds earlier rows and needs a larger scale has their codes moved down.
 constexpr int APPEND8_THREADS = 256, APPEND8_WARPS = APPEND8_THREADS / 32;
 struct Append8Grid {
     int nkv, groups, hg, rounds, wpu, chunk;  // CTAs of keys and values; groups of `rounds` times hg heads; warps of a unit; rows
@@ -332,8 +333,9 @@ __device__ __forceinline__ void q8_widen16(const uint4& c, float scale, uint4 (&
 
 // Positions of the sequences as packed rows: a block takes READ_ROWS consecutive rows, a warp each finds
 // the row's place, then all threads copy its heads.  Bound by memory: every code is read, every value
-// written once.
-constexpr int READ_THREADS = 256, READ_ROWS = 4;
+// written once.  (38,000 bf16 rows of 8 heads 47.2 us, 5.0 TB/s, with 8 rows, 50.3 with 4; in blocks of 16 and three times
+// as many 123 against 134, 5.4 TB/s.  32 bytes a store make no difference.)
+constexpr int READ_THREADS = 256, READ_ROWS = 8;
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p) {
     constexpr int VEC = Elem<T>::VEC, PIECE = Q8 ? 16 : VEC;
@@ -404,7 +406,8 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
 
 // The blocks that entries with more than `wide` rows read (a group's prefix, a sequence's own part), as pools of the
 // cache's dtype, at the same place, for the attention kernels of plain pools.  Every CTA finds these entries, 256 at a
-// time, and all share their pieces laid end to end.  Bound by memory, a byte read and two (four) written a value.
+// time, and all share their pieces laid end to end.  Bound by memory, a byte read and two (four) written a value: 4
+// sequences of 4500 positions of 8 heads 20 us.  (By entries, a CTA each, one long entry took as long as all.)
 template <typename T, bool JOINT>
 __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
     constexpr int VEC = Elem<T>::VEC, ILP = 4, WARPS = READ_THREADS / 32;

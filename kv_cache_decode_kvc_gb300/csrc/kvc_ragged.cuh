@@ -187,10 +187,11 @@ struct Ragged {
     // with up to 500 positions behind 16,384 common ones 181, 153, 162 us, 200 with 350 behind as many 132,
     // 139, 146: where the cuts happen to fall weighs as much as what a start costs, 3 is a middle; tiles of class 1 at
     // 1/2, 1 and 3/2 of class 0's: a batch of chunks and tokens 176, 133, 168.)
-    // (MANY, the kernel on codes: a tile of 32 rows takes 2.2 us, one of up to 8 that comes from memory 1.3; a stream's
-    // start some three tiles of the latter.)
-    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : MANY > 0 ? (cl == 0 ? 7 : 3) : 1; }
-    __host__ __device__ static constexpr int start_cost(int cl) { return PAIRS ? (cl == 0 ? 6 : 3) : MANY > 0 ? (cl == 0 ? 24 : 7) : 1; }
+    // (MANY, the kernel on codes: a tile of 32 rows takes 1.7 to 2.2 us, one of up to 8, which comes from memory, 1.3.  Tiles of
+    // 5 : 3, 7 : 3, 7 : 4 with starts of 9 : 9, 24 : 7, 24 : 9: 24 tokens behind 2048 common positions 59.3, 53.2, 51.4 us, 128
+    // with 10 to 100 of their own 72.9, 69.4, 66.4; 24 tokens alone 47.0, 46.2, 46.5.)
+    __host__ __device__ static constexpr int tile_cost(int cl) { return PAIRS ? 2 : MANY > 0 ? (cl == 0 ? 7 : 4) : 1; }
+    __host__ __device__ static constexpr int start_cost(int cl) { return PAIRS ? (cl == 0 ? 6 : 3) : MANY > 0 ? (cl == 0 ? 24 : 9) : 1; }
     // log2 of the units a CTA takes at least: a worker between two pieces of a stream then holds a tile
     // of it (a worker's share, half of that in class 1, is a tile's cost or more).  With class 0 twice that,
     // a stream's start (one of 1 x 4000 positions 18.3 us against 20.6 with the larger share, 200 tokens at

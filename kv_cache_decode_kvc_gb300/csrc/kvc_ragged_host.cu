@@ -52,8 +52,10 @@ kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, Path path) {
 }
 // On an 8-bit cache, entries (sequences, shared prefixes) with more query rows per head than this are widened to bf16
 // and attended by the kernel of plain pools: per 32 rows it takes a quarter of the time of the kernel on codes, which
-// has to make up for the widening and for merging its larger pieces (64 sequences of 32 to 160 rows on one KV head
-// take XXX us at 128, YYY at 256).
+// has to make up for the widening and for merging its larger pieces.  (At 64, 128, 256, 512 rows: 64 sequences of 32 to
+// 160 rows on one KV head of 64 121, 131, 110, 110 us, of 128 162, 146, 110, 110; 24 sequences, 4 of them with chunks of
+// 4 x 300 rows at most, 171, 171, 171, 181, of 4 x 100 146, 146, 145, 115; 8 of 4 x 100 each 146 at 256 and
+// 222 on codes.  A rule on the device, by these entries' work, gained on no more cases than it lost on.)
 constexpr int MANY_ROWS = 256;
 // Is that worth its launches (three, some 8 us with nothing to do)?  The host knows how many rows an entry can have if every
 // sequence has a token, no more; a batch whose sequences have none, against that, is attended on codes all the same.
@@ -326,9 +328,11 @@ int kvc_paged_read(kvc_t h, int layer, void* k_out, int64_t k_stride, void* v_ou
 
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes) {
     if (!h || !bytes || !h->paged || N < 1 || NG < 0 || NG > h->B) return KVC_EINVAL;
-    // enough for every path, whatever kvc_set_math does in between
+    // enough for every path, whatever kvc_set_math does in between; on an 8-bit cache for the present one (that on CUDA
+    // cores holds a layer's widened pools, which a decode step on codes would never touch)
     uint64_t most = 0;
-    for (const Path path : {Path::CC, h->quant ? Path::Q8 : Path::TC5}) {
+    for (const Path path : {Path::CC, Path::TC5, Path::Q8}) {
+        if (h->quant ? path != ragged_path(h) : path == Path::Q8) continue;
         const uint64_t n = scratch_of(h, N, NG, path).total;
         if (n > most) most = n;
     }

