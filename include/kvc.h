@@ -371,7 +371,8 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * CUDA cores) by 128 positions (CUDA cores: 64 for D <= 64, else 32) that its last row sees.  A
  * call of more than 10^9 tiles (2 10^9 on CUDA cores; some 12 and 30 s of work; on an 8-bit cache's codes, in tiles of
  * 32 rows by 128 positions, 256 for D = 64, 3 10^8) may be refused:
- * KVC_DEV_TOO_LARGE is set and nothing is written; give it fewer sequences or shorter chunks. */
+ * KVC_DEV_TOO_LARGE is set and nothing is written (on an 8-bit cache, whose two kernels' entries are counted apart, nothing
+ * of the entries that were too many); give it fewer sequences or shorter chunks. */
 int kvc_paged_attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out,
                           int64_t out_stride, const int32_t* block_table, const int32_t* cu_seqlens,
                           const int32_t* lens, int N, void* ws, uint64_t ws_bytes, void* stream);

@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
                     if (end_s[mid] <= i) k = mid + 1; else hi = mid;
                 }
                 const int64_t w = i - (k > 0 ? end_s[k - 1] : 0);
-                const unsigned g = (unsigned)(w >> lgper), j = g / (unsigned)heads, hk = g - j * heads;
+                const int64_t g = w >> lgper;  // (past 32 bits for 16 KV heads at 2^31 positions)
+                const unsigned j = g >> 32 ? (unsigned)(g / heads) : (unsigned)g / (unsigned)heads, hk = (unsigned)g - j * heads;
                 const int block = __ldg(p.table + (size_t)seq_s[k] * p.max_blocks + j0_s[k] + j);
                 if ((unsigned)block >= (unsigned)p.num_blocks) continue;
                 isv[q] = hk >= (unsigned)p.H_kv;

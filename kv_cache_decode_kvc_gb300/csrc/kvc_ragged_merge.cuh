@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_parts_kernel(const Rag
     auto pieces = [&](int e, const Entry& s) {
         Pieces x;
         x.many = !in_part(pb, s);
+        x.n = 0;
         auto find = [&](auto r, const auto& sp, const RaggedParams& q) {
+            if (!sp.valid) return;  // (a part that was refused as too large has left no split)
             using R = decltype(r);
             const typename R::Stream st = R::of_row(q, sp, q.plan, e, s, h, row);
             x.cl = R::cls(q, s);
@@ -339,10 +341,13 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) merge_parts_kernel(const Rag
     if (!own.ok) return;
     const Pieces po = pieces(p.NG + lo, own);
     const bool joint = own.pfx > 0;
-    if (!joint && po.n == 1) return;  // written by its worker
+    if (po.n == 0 || (!joint && po.n == 1)) return;  // (written by its worker)
     Pieces pp;
     pp.n = 0;
-    if (joint) pp = pieces(a, group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), used));
+    if (joint) {
+        pp = pieces(a, group_entry(b0, __ldg(p.cu + b0), __ldg(p.cu + b1), used));
+        if (pp.n == 0) return;
+    }
     const int np = pp.n + po.n;
     auto out_of = [&](int g) { return static_cast<T*>(p.out) + (int64_t)row * p.out_ts + (int64_t)(h * G + g) * p.D; };
     auto at_head = [&](int g) {

@@ -387,7 +387,9 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
         auto scales_of = [&](const At& a, int e) {
             if (!there(a)) return make_float2(1.f, 1.f);  // (-inf times it stays that)
             const int64_t at = (int64_t)((unsigned)e < (unsigned)p.num_blocks ? e : 0) * p.H_kv + a.g.h;
-            return make_float2(__ldg(pa.Ksc + at), __ldg(pa.Vsc + at));
+            // (Blocks never written have scales of 0, whose logarithm the weights cannot take, and codes of 0.)
+            const float k = __ldg(pa.Ksc + at), v = __ldg(pa.Vsc + at), least = exp2i(Q8_EMIN);
+            return make_float2(k < least ? least : k, v < least ? least : v);
         };
         At a, b, c;  // block numbers, scales, copies
         a.g.n = 0;
