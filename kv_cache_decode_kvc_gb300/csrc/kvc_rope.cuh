@@ -28,7 +28,9 @@ __device__ __forceinline__ float norm_factor(const float (&x)[VEC], const float 
         s1 = fmaf(y[e], y[e], s1);
     }
     float sum = s0 + s1;
-    for (int off = per >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        if (off < per) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
     return rsqrtf(fmaf(sum, rD, eps));
 }
 // The two vectors times that factor and their weights, 16-byte vectors at wx and wy.
@@ -128,7 +130,7 @@ __device__ __forceinline__ void turn_piece(float (&x)[VEC], float (&y)[VEC], con
 //
 // NORM: the heads of q and k are first divided by the root of their mean square (plus eps) and multiplied by a
 // weight per dimension, y = x w / sqrt(mean x^2 + eps), all in fp32: a head's threads are neighbours in a warp and
-// add their squares by shuffles.  The same bytes: 12,400 rows of 80 heads take 99 us with norms (5.15 TB/s).
+// add their squares by shuffles.  The same bytes: 12,400 rows of 80 heads take 97 us with norms (5.2 TB/s), which the lanes' issue bounds as much (0.8 of its slots).
 template <typename T, int TB, bool VECTOR, bool NORM>
 __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable& rt, int bid) {
     constexpr int VEC = Elem<T>::VEC;
