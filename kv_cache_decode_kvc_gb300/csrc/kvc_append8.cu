@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t c, float mul) {
 // cosines and sines at a time, once for the CTA's heads where that is all of them.  K or V of a head is a unit of one warp (of two or four where heads are few or blocks long), which goes
 // over its rows twice: first for the largest |x| of K, normalised and rotated, or of V, which settles the scale, then, from
 // L1, for the codes.  Bound by its chain of lookups, first pass, maximum and second pass, beside the memory's: 9700 rows of
-// 32 + 8 heads take 76 us with the queries' grid beside it, 2.9 TB/s.  (Values held in registers between the passes
+// 32 + 8 heads take 75 us with the queries' grid beside it, 2.9 TB/s.  (Values held in registers between the passes
 // spilled, or left too few warps: 112 to 129 us, and 81 with a CTA's heads laid out as pieces and a maximum exchanged
 // for each.)  A block that holds earlier rows and needs a larger scale has their codes moved down.
 constexpr int APPEND8_THREADS = 256, APPEND8_WARPS = APPEND8_THREADS / 32;
@@ -46,6 +46,7 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
     __shared__ uint32_t amax[2][APPEND8_WARPS];  // of a round's units, of two rounds in turn
     __shared__ uint64_t freq_s[128];  // (from the parameters, where each lane's is another, a warp's loads go one by one)
     __shared__ uint8_t axis_s[128];
+    __shared__ float inv_s[256];  // norms of the rows of a round's heads (4 of 64 rows, 2 of 128, or 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pairs = rt.rot_dim / 2, nrot = rt.rot_dim / (2 * VEC);
     if (tid == 0) found = 0;
@@ -124,11 +125,15 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
                            : static_cast<const T*>(p.k) + r0 * p.k_ts + (int64_t)h * p.D;
         const int64_t ts = isv ? p.v_ts : p.k_ts;
         // Row `row`'s values at this lane's place; the angles held begin at row `from`.
-        auto values = [&](int row, int from, const uint4& a, const uint4& bb, float (&x)[VEC], float (&y)[VEC]) {
+        auto values = [&](int pass, bool there, int row, int from, const uint4& a, const uint4& bb, float (&x)[VEC], float (&y)[VEC]) {
             Elem<T>::unpack(a, x);
             Elem<T>::unpack(bb, y);
-            if (normed)  // (alike in a warp, whose lanes stay together)
-                norm_piece<T>(x, y, wx, wy, norm_factor<VEC>(x, y, per, 1.f / (float)p.D, p.eps));
+            if (normed) {  // (alike in a warp, whose lanes stay together)
+                float* kept = &inv_s[(unit >> 1) * p.bs + row];
+                const float inv = pass == 0 ? norm_factor<VEC>(x, y, per, 1.f / (float)p.D, p.eps) : *kept;
+                if (pass == 0 && there) *kept = inv;
+                norm_piece<T>(x, y, wx, wy, inv);
+            }
             if (!turned) return;
             const float *cr = cosines + (row - from) * pairs + u * VEC, *sr = sines + (row - from) * pairs + u * VEC;
             float co[VEC], si[VEC];
@@ -172,8 +177,9 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
                         if (first + q * step >= end) continue;
                         const int row = min(first + (lane >> lg) + q * step, end - 1);
                         float x[VEC], y[VEC];
-                        values(row, from, a[q], bb[q], x, y);
-                        if (first + (lane >> lg) + q * step >= end) continue;
+                        const bool there = first + (lane >> lg) + q * step < end;
+                        values(pass, there, row, from, a[q], bb[q], x, y);
+                        if (!there) continue;
                         if (pass == 0) {  // (a maximum passes NaN over)
 #pragma unroll
                             for (int i = 0; i < VEC; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
