@@ -100,7 +100,7 @@ int kvc_decode_step(kvc_t h, int layer, const void* q, const void* k_new, const 
                     void* out, const int32_t* lens, void* stream);
 
 /* Allocated payload of the handle: 2 * layers * H_kv * D * B * T_max * elem_bytes (paged: the pools; 8-bit caches: the
- * codes, a byte each, without the scales). */
+ * codes, a byte each, and their scales). */
 uint64_t kvc_bytes(kvc_t h);
 
 /* The closed form 2 * L * H_kv * D * (B * T) * elem_bytes (no allocation, host only).
@@ -109,7 +109,7 @@ uint64_t kvc_bytes_formula(int64_t L, int64_t B, int64_t H_kv, int64_t D, int64_
                            int64_t elem_bytes);
 
 /* Ragged payload 2 * layers * H_kv * D * elem_bytes * sum_b lens_host[b] (lens in HOST memory,
- * B entries). */
+ * B entries; 8-bit caches: codes and scales, of a paged one those of every block begun). */
 uint64_t kvc_payload_bytes(kvc_t h, const int32_t* lens_host);
 
 /* Device pointers of layer `layer`'s K and V caches ([B, H_kv, T_max, D], owned by h). */
@@ -360,11 +360,11 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * terms (within 2^-15 of a weight) for sequences, and shared prefixes, of up to 64 query rows per
  * KV head (tokens x H_q / H_kv, of a prefix all its group's), as one (2^-8) for larger ones.  Every other shape, or math
  * mode 1, runs on CUDA cores in fp32.  On a paged 8-bit cache the tensor cores take the codes as they are: q as two E4M3
- * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights as three
- * E5M2 terms (within 2^-9 of a weight, or 2^-26 of the row's largest), and a row whose q has an infinity or a NaN is NaN;
- * sequences and prefixes of more than 256 query rows per KV head are attended as on a bf16 cache, over blocks
- * widened (exactly) in the scratch, where the call's N leaves room for more than 512; where the CUDA cores attend an
- * 8-bit cache, all blocks are widened.  ws is device scratch of at least
+ * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights, times
+ * their block's scale of V, as three E5M2 terms (within 2^-9 of one, or 2^-26 of the row's largest such product); a row
+ * whose q has an infinity or a NaN is NaN; sequences and prefixes of many query rows per KV head (more than 256, fewer where N, B and D tell that most have
+ * many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N leaves room for
+ * more than 512; where the CUDA cores attend an 8-bit cache, all blocks are widened.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each.
  * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on

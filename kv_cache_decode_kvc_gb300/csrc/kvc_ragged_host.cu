@@ -52,16 +52,22 @@ kvc::RaggedScratch ragged_ws(const kvc_cache* h, int N, int NG, Path path) {
 }
 // On an 8-bit cache, entries (sequences, shared prefixes) with more query rows per head than this are widened to bf16
 // and attended by the kernel of plain pools: per 32 rows it takes a quarter of the time of the kernel on codes, which
-// has to make up for the widening and for merging its larger pieces.  (At 64, 128, 256, 512 rows: 64 sequences of 32 to
-// 160 rows on one KV head of 64 121, 131, 110, 110 us, of 128 162, 146, 110, 110; 24 sequences, 4 of them with chunks of
-// 4 x 300 rows at most, 171, 171, 171, 181, of 4 x 100 146, 146, 145, 115; 8 of 4 x 100 each 146 at 256 and
-// 222 on codes.  A rule on the device, by these entries' work, gained on no more cases than it lost on.)
-constexpr int MANY_ROWS = 256;
-// Is that worth its launches (three, some 8 us with nothing to do)?  The host knows how many rows an entry can have if every
+// has to make up for the widening, for merging its larger pieces, and for two kernels one after the other where a batch
+// has both kinds.  So what matters besides an entry's rows is whether the others go the same way, and of that the host knows
+// the mean.  (24 sequences of 3000 to 6000 positions with 30 to 40, 40 to 60, 56 to 64 tokens, D = 128, 32 heads on 8: all on codes
+// 258, 355, 412 us, all widened 255, 269, 273; 64 sequences of 5 tokens of 32 heads on 1 141, 145, of 7 179, 150.  D = 64, where
+// the kernel on codes has one CTA an SM: 64 sequences of 1 to 5 such tokens 111 and 100, of 2 on 2 KV heads 70 and 80, 24 of 40
+// to 60 tokens 393 and 176; with 20 of those 24 single tokens 124 at 256 rows, 100 at 128 and 64; 64 sequences of 20 to 80 rows 96 at
+// 128, 112 at 64.  D = 128, 4 of 24 sequences with chunks of 4 x 300 rows at most: 171 at 64 to 256, 181 at 512.)
+int many_rows(const kvc_cache* h, int N) {
+    const int64_t mean = (int64_t)N * h->G / h->B;
+    return h->D == 64 ? (mean >= 80 ? 16 : 128) : mean >= 160 ? 32 : 256;
+}
+// Is that worth its launches (some 17 us with nothing to do)?  The host knows how many rows an entry can have if every
 // sequence has a token, no more; a batch whose sequences have none, against that, is attended on codes all the same.
-bool many_rows(const kvc_cache* h, int N, int NG) {
+bool split_rows(const kvc_cache* h, int N, int NG) {
     const int64_t most = NG > 0 ? N : (int64_t)N - h->B + 1;
-    return most * h->G > 2 * MANY_ROWS;
+    return most * h->G > 512;
 }
 // The parts of the scratch: the path's, that of the kernel of plain pools beside the one on codes, and the two
 // widened pools.
@@ -73,7 +79,7 @@ struct Scratch {
 Scratch scratch_of(const kvc_cache* h, int N, int NG, Path path) {
     Scratch s{};
     s.own = ragged_ws(h, N, NG, path);
-    s.split = path == Path::Q8 && many_rows(h, N, NG);
+    s.split = path == Path::Q8 && split_rows(h, N, NG);
     s.many_at = s.wide_at = s.total = s.own.total;
     if (s.split) {
         s.many = ragged_ws(h, N, NG, Path::TC5);
@@ -157,7 +163,7 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     kvc::RaggedParams m = p;  // the call on widened blocks
     m.K = w + sc.wide_at;
     m.V = w + sc.wide_at + sc.wide_bytes;
-    m.wide = path == Path::CC ? -1 : MANY_ROWS;
+    m.wide = path == Path::CC ? -1 : many_rows(h, N);
     if (path == Path::CC || sc.split) {
         kvc::Q8Widen x{p, Ksc, Vsc, w + sc.wide_at, w + sc.wide_at + sc.wide_bytes};
         x.r.wide = m.wide;
@@ -170,7 +176,7 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
         m.row_ml = p.row_ml;
         m.P = ragged_p(h, Path::TC5);
         m.part = 2;
-        p.wide = MANY_ROWS;
+        p.wide = m.wide;
         p.part = 1;
         CUtensorMap mk, mv;
         const uint64_t rows = h->layer_bytes / h->D;

@@ -27,7 +27,7 @@
 // for more the softmax warps: 2.2 us a tile of 32 rows by 128 positions (256 of D = 64), two CTAs an SM at work, of
 // which the products take a tenth; conversions, three terms a weight and the exponentials are its chain (64 sequences of
 // 32 to 160 rows on one KV head of 64: 110 us against 7 of memory).  Two groups of softmax warps a CTA took as long.
-// So entries of more than 256 rows go to the kernel of plain pools (kvc_ragged_host.cu).
+// So entries of many rows go to the kernel of plain pools (kvc_ragged_host.cu).
 //
 // The streams, their split over the CTAs and the merge are those of kvc_ragged.cuh (tiles of RT rows, all of
 // class 1, one worker a CTA).  Warps: 0 copies, 1 issues the products, 2 computes the split and walks the

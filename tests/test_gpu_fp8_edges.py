@@ -126,6 +126,27 @@ def test_splits_over_few_and_many_ctas(kvc, ctas, D, shared):
     check_attention(out, bt, attention64(bt), tensor_cores=True)
 
 
+MIXES = [  # new, H_q, H_kv, D: which rows are attended on codes and which on widened blocks depends on D and on their mean
+    ([1] * 11 + [140], 8, 2, 128),            # one chunk beside single tokens
+    ([1] * 11 + [140], 8, 2, 64),
+    ([1] * 11 + [140], 8, 1, 64),             # (more rows to a token)
+    ([1, 2, 3, 5, 4, 5, 1, 1, 5], 32, 1, 64),  # drafts, all of them
+    ([1, 2, 3, 5, 4, 5, 1, 1, 5], 32, 1, 128),
+    ([7, 8, 9, 8, 1, 9, 8], 32, 1, 128),
+    ([40, 60, 0, 50, 33], 4, 1, 128),
+    ([40, 60, 0, 50, 33], 4, 1, 64),
+]
+
+
+@pytest.mark.parametrize("new,H_q,H_kv,D", MIXES)
+@pytest.mark.parametrize("shared", [False, True])
+def test_rows_on_codes_beside_widened_blocks(kvc, new, H_q, H_kv, D, shared):
+    hist = [(211 * i) % 300 + 40 for i in range(len(new))]
+    kw = dict(start=[0, 2, len(new)], prefix=[40, 32]) if shared else {}
+    bt = Batch8(new, hist, 16, H_q, H_kv, D, pad=3, mag=2, **kw)
+    check_attention(attend(kvc, bt, shared), bt, attention64(bt), tensor_cores=True)
+
+
 @pytest.mark.parametrize("math", [0, 1])
 @pytest.mark.parametrize("D", [64, 128])
 def test_many_kv_heads(kvc, D, math):
