@@ -34,8 +34,8 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t c, float mul) {
 // for each.)  A block that holds earlier rows and needs a larger scale has their codes moved down.
 constexpr int APPEND8_THREADS = 256, APPEND8_WARPS = APPEND8_THREADS / 32;
 struct Append8Grid {
-    int nkv, groups, hg, rounds, wpu, chunk;  // CTAs of keys and values; groups of `rounds` times hg heads; warps of a unit; rows
-                                           // whose angles are held
+    int nkv, groups, hg, rounds, wpu, chunk, two;  // CTAs of keys and values; groups of `rounds` times hg heads; warps of a unit; rows
+                                           // whose angles are held; do the queries follow as a grid of their own?
 };
 
 template <typename T, bool NORM>
@@ -56,7 +56,7 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
         axis_s[tid] = rt.axis[tid];
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the queries' grid of the same append, see `late`)
+    if (grid.two) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (see `late`: 74 us against 79.5)
     __syncthreads();
     bool bad = false;
     int cnt = 0;
@@ -285,6 +285,7 @@ static int launch_append8_as(const RopeParams& p, const RopeTable& t, int sms, b
     const int64_t nq = p.q && !many ? p.N : 0;
     if (nkv + nq > 0x7FFFFFFF) return (int)cudaErrorInvalidValue;
     g.nkv = (int)nkv;
+    g.two = many && p.q;
     // rows whose angles are held: 4096 cosines and as many sines, 32 KB
     const int pairs = t.rot_dim > 0 ? t.rot_dim / 2 : 1;
     g.chunk = 4096 / pairs < p.bs ? 4096 / pairs : p.bs;
@@ -348,7 +349,6 @@ __global__ void __launch_bounds__(READ_THREADS) paged_read_kernel(const Q8Read p
     __shared__ int block_s[READ_ROWS], off_s[READ_ROWS];  // block: -1 zeros, -2 not a row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = blockIdx.x * READ_ROWS;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool bad = false;
     uint32_t flag = 0;
     for (int b = tid; b <= p.B; b += READ_THREADS) {
@@ -423,7 +423,6 @@ __global__ void __launch_bounds__(READ_THREADS) widen_kernel(const Q8Widen x) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NE = p.B + (JOINT ? p.NG : 0);
     const int lgper = 31 - __clz(p.bs * p.D / 16), heads = 2 * p.H_kv;  // 16-code pieces of a head's block; K and V heads
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e0 = 0; e0 < NE; e0 += READ_THREADS) {
         const int e = e0 + tid;
         Entry s;

@@ -433,7 +433,6 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
     if (warp != 2) named_bar_arrive(9, C::THREADS);
     // Before any wait: a kernel that releases its dependents early may run for longer than a wait's limit.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // A role's segment s of set q, as soon as it is known (the caller releases the place).
     auto fetch_seg = [&](int q, int s, Seg& g) {

@@ -183,10 +183,7 @@ __device__ __forceinline__ void append_rows(const RopeParams& p, const RopeTable
         b = src[v1];
     };
 
-    if (!p.late) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
+    if (!p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (VECTOR) {
 #pragma unroll
         for (int k = 0; k < PRE; ++k) load(tid + k * ROPE_THREADS, xa[k], xb[k]);
