@@ -399,6 +399,17 @@ int kvc_paged_attn_shared(kvc_t h, int layer, const void* q, int64_t q_stride, v
  * not shrink as N or NG grow. */
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes);
 
+/* The calls of a serving step on one block of arguments, for bindings that pay for every argument (ctypes: 21 of them 2.5
+ * us, a block 0.5): `call` names one of these, args [n] holds its arguments in order, 8 bytes each and 8-byte aligned (HOST
+ * memory): pointers and integers as int64_t, floats as double.  The call's own status and meaning; KVC_EINVAL also for an unknown call,
+ * another n than its arguments', or an int argument that does not fit. */
+#define KVC_CALL_PAGED_APPEND_ROPE 0      /* 18 arguments */
+#define KVC_CALL_PAGED_APPEND_NORM_ROPE 1 /* 21 */
+#define KVC_CALL_PAGED_READ 2             /* 11 */
+#define KVC_CALL_PAGED_ATTN_RAGGED 3      /* 13 */
+#define KVC_CALL_PAGED_ATTN_SHARED 4      /* 16 */
+int kvc_call(int call, const void* args, int n);
+
 /* Shape query: writes layers, B, H_q, H_kv, D, T_max, dtype (any pointer may be NULL). */
 int kvc_get_shape(kvc_t h, int* layers, int* B, int* H_q, int* H_kv, int* D, int* T_max,
                   int* dtype);

@@ -191,6 +191,25 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     return kvc::launch_ragged_q8(p, sc.split ? &m : nullptr, Ksc, Vsc, kv[0], kv[1], st) == 0 ? KVC_OK : KVC_ECUDA;
 }
 
+// The arguments of kvc_call, one after the other.
+struct Words {
+    const int64_t* w;
+    bool ok = true;
+    template <class T>
+    T* ptr() { return reinterpret_cast<T*>((uintptr_t)*w++); }
+    int64_t i64() { return *w++; }
+    int i32() {
+        const int64_t x = *w++;
+        ok = ok && x == (int)x;
+        return (int)x;
+    }
+    float f32() {
+        double x;
+        memcpy(&x, w++, 8);
+        return (float)x;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -361,6 +380,93 @@ int kvc_paged_attn_shared(kvc_t h, int layer, const void* q, int64_t q_stride, v
     if (!aligned(groups, 4) || !aligned(prefix_lens, 4)) return KVC_EINVAL;
     return attn_ragged(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, groups, prefix_lens, NG,
                        ws, ws_bytes, stream);
+}
+
+int kvc_call(int call, const void* args, int n) {
+    if (!args || !aligned(args, 8)) return KVC_EINVAL;
+    Words a{static_cast<const int64_t*>(args)};
+    switch (call) {
+        case KVC_CALL_PAGED_APPEND_ROPE:
+        case KVC_CALL_PAGED_APPEND_NORM_ROPE: {
+            const bool norm = call == KVC_CALL_PAGED_APPEND_NORM_ROPE;
+            if (n != (norm ? 21 : 18)) return KVC_EINVAL;
+            kvc_cache* h = a.ptr<kvc_cache>();
+            const int layer = a.i32();
+            kvc_rope* rope = a.ptr<kvc_rope>();
+            const void *qn = nullptr, *kn = nullptr;
+            float eps = 0.f;
+            if (norm) {
+                qn = a.ptr<const void>();
+                kn = a.ptr<const void>();
+                eps = a.f32();
+            }
+            const void* q = a.ptr<const void>();
+            const int64_t qs = a.i64();
+            void* qo = a.ptr<void>();
+            const int64_t qos = a.i64();
+            const void* k = a.ptr<const void>();
+            const int64_t ks = a.i64();
+            const void* v = a.ptr<const void>();
+            const int64_t vs = a.i64();
+            const int32_t* pos = a.ptr<const int32_t>();
+            const int64_t ps = a.i64();
+            const int32_t* table = a.ptr<const int32_t>();
+            const int32_t* cu = a.ptr<const int32_t>();
+            const int32_t* lens = a.ptr<const int32_t>();
+            const int N = a.i32();
+            void* stream = a.ptr<void>();
+            if (!a.ok) return KVC_EINVAL;
+            return norm ? kvc_paged_append_norm_rope(h, layer, rope, qn, kn, eps, q, qs, qo, qos, k, ks, v, vs, pos, ps, table,
+                                                     cu, lens, N, stream)
+                        : kvc_paged_append_rope(h, layer, rope, q, qs, qo, qos, k, ks, v, vs, pos, ps, table, cu, lens, N,
+                                                stream);
+        }
+        case KVC_CALL_PAGED_READ: {
+            if (n != 11) return KVC_EINVAL;
+            kvc_cache* h = a.ptr<kvc_cache>();
+            const int layer = a.i32();
+            void* k = a.ptr<void>();
+            const int64_t ks = a.i64();
+            void* v = a.ptr<void>();
+            const int64_t vs = a.i64();
+            const int32_t* table = a.ptr<const int32_t>();
+            const int32_t* cu = a.ptr<const int32_t>();
+            const int32_t* lens = a.ptr<const int32_t>();
+            const int N = a.i32();
+            void* stream = a.ptr<void>();
+            return a.ok ? kvc_paged_read(h, layer, k, ks, v, vs, table, cu, lens, N, stream) : KVC_EINVAL;
+        }
+        case KVC_CALL_PAGED_ATTN_RAGGED:
+        case KVC_CALL_PAGED_ATTN_SHARED: {
+            const bool shared = call == KVC_CALL_PAGED_ATTN_SHARED;
+            if (n != (shared ? 16 : 13)) return KVC_EINVAL;
+            kvc_cache* h = a.ptr<kvc_cache>();
+            const int layer = a.i32();
+            const void* q = a.ptr<const void>();
+            const int64_t qs = a.i64();
+            void* out = a.ptr<void>();
+            const int64_t os = a.i64();
+            const int32_t* table = a.ptr<const int32_t>();
+            const int32_t* cu = a.ptr<const int32_t>();
+            const int32_t* lens = a.ptr<const int32_t>();
+            const int N = a.i32();
+            const int32_t *groups = nullptr, *prefix = nullptr;
+            int NG = 0;
+            if (shared) {
+                groups = a.ptr<const int32_t>();
+                prefix = a.ptr<const int32_t>();
+                NG = a.i32();
+            }
+            void* ws = a.ptr<void>();
+            const uint64_t ws_bytes = (uint64_t)a.i64();
+            void* stream = a.ptr<void>();
+            if (!a.ok) return KVC_EINVAL;
+            return shared ? kvc_paged_attn_shared(h, layer, q, qs, out, os, table, cu, lens, N, groups, prefix, NG, ws, ws_bytes,
+                                                  stream)
+                          : kvc_paged_attn_ragged(h, layer, q, qs, out, os, table, cu, lens, N, ws, ws_bytes, stream);
+        }
+    }
+    return KVC_EINVAL;
 }
 
 }  // extern "C"

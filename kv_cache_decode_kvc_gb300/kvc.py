@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkvc.so")
@@ -97,6 +98,7 @@ def load() -> ctypes.CDLL:
         "kvc_paged_attn_ragged": (I, [P, I, P, I64, P, I64, P, P, P, I, P, U64, P]),
         "kvc_paged_attn_shared": (I, [P, I, P, I64, P, I64, P, P, P, I, P, P, I, P, U64, P]),
         "kvc_paged_attn_workspace": (I, [P, I, I, ctypes.POINTER(U64)]),
+        "kvc_call": (I, [I, P, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -300,39 +302,52 @@ def kvc_rope_destroy(r) -> None:
     _check(load().kvc_rope_destroy(r), "kvc_rope_destroy")
 
 
+# The calls of a serving step go through kvc_call: their arguments as one block of 8-byte words.
+def _addr(x) -> int:
+    return 0 if x is None else x if type(x) is int else x.data_ptr()
+
+
+_APPEND, _APPEND_NORM = struct.Struct("=18q").pack, struct.Struct("=5qd15q").pack
+_READ, _ATTN, _SHARED = (struct.Struct(f"={n}q").pack for n in (11, 13, 16))
+
+
+def _call(call, words, n, what):
+    status = (_lib or load()).kvc_call(call, words, n)
+    if status:
+        raise KvcError(status, what)
+
+
 def kvc_paged_append_rope(h, layer, rope, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, positions,
                           pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _check(load().kvc_paged_append_rope(h, layer, rope, _ptr(q), q_stride, _ptr(q_out), q_out_stride, _ptr(k),
-                                        k_stride, _ptr(v), v_stride, _ptr(positions), pos_stride,
-                                        _ptr(block_table), _ptr(cu_seqlens), _ptr(lens), N, _stream(stream)),
-           "kvc_paged_append_rope")
+    _call(0, _APPEND(h or 0, layer, rope or 0, _addr(q), q_stride, _addr(q_out), q_out_stride, _addr(k), k_stride,
+                     _addr(v), v_stride, _addr(positions), pos_stride, _addr(block_table), _addr(cu_seqlens), _addr(lens),
+                     N, _stream(stream)), 18, "kvc_paged_append_rope")
 
 
 def kvc_paged_append_norm_rope(h, layer, rope, q_norm, k_norm, eps, q, q_stride, q_out, q_out_stride, k, k_stride, v,
                                v_stride, positions, pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _check(load().kvc_paged_append_norm_rope(h, layer, rope, _ptr(q_norm), _ptr(k_norm), eps, _ptr(q), q_stride,
-                                             _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(v), v_stride,
-                                             _ptr(positions), pos_stride, _ptr(block_table), _ptr(cu_seqlens),
-                                             _ptr(lens), N, _stream(stream)), "kvc_paged_append_norm_rope")
+    _call(1, _APPEND_NORM(h or 0, layer, rope or 0, _addr(q_norm), _addr(k_norm), eps, _addr(q), q_stride, _addr(q_out),
+                          q_out_stride, _addr(k), k_stride, _addr(v), v_stride, _addr(positions), pos_stride,
+                          _addr(block_table), _addr(cu_seqlens), _addr(lens), N, _stream(stream)), 21,
+          "kvc_paged_append_norm_rope")
 
 
 def kvc_paged_read(h, layer, k_out, k_stride, v_out, v_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _check(load().kvc_paged_read(h, layer, _ptr(k_out), k_stride, _ptr(v_out), v_stride, _ptr(block_table),
-                                 _ptr(cu_seqlens), _ptr(lens), N, _stream(stream)), "kvc_paged_read")
+    _call(2, _READ(h or 0, layer, _addr(k_out), k_stride, _addr(v_out), v_stride, _addr(block_table), _addr(cu_seqlens),
+                   _addr(lens), N, _stream(stream)), 11, "kvc_paged_read")
 
 
 def kvc_paged_attn_ragged(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, ws, ws_bytes,
                           stream=None) -> None:
-    _check(load().kvc_paged_attn_ragged(h, layer, _ptr(q), q_stride, _ptr(out), out_stride, _ptr(block_table),
-                                        _ptr(cu_seqlens), _ptr(lens), N, _ptr(ws), ws_bytes, _stream(stream)),
-           "kvc_paged_attn_ragged")
+    _call(3, _ATTN(h or 0, layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
+                   _addr(lens), N, _addr(ws), ws_bytes, _stream(stream)), 13, "kvc_paged_attn_ragged")
 
 
 def kvc_paged_attn_shared(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, groups,
                           prefix_lens, NG, ws, ws_bytes, stream=None) -> None:
-    _check(load().kvc_paged_attn_shared(h, layer, _ptr(q), q_stride, _ptr(out), out_stride, _ptr(block_table),
-                                        _ptr(cu_seqlens), _ptr(lens), N, _ptr(groups), _ptr(prefix_lens), NG,
-                                        _ptr(ws), ws_bytes, _stream(stream)), "kvc_paged_attn_shared")
+    _call(4, _SHARED(h or 0, layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
+                     _addr(lens), N, _addr(groups), _addr(prefix_lens), NG, _addr(ws), ws_bytes, _stream(stream)), 16,
+          "kvc_paged_attn_shared")
 
 
 def kvc_paged_attn_workspace(h, N, NG=0) -> int:

@@ -1,5 +1,6 @@
 """The 8-bit paged cache: host-side refusals, and the definition that the GPU tests compare with."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -29,6 +30,20 @@ def test_null_arguments_are_refused(lib):
                          ((1, 4, 256, 2, 4, 1 << 15, 1 << 15, 256, 0), kvc.KVC_ERANGE)):
         out = ctypes.c_void_p(5)
         assert lib.kvc_create_paged_fp8(ctypes.byref(out), *args) == status and out.value is None
+
+
+def test_calls_by_a_block_of_arguments_are_refused(lib):
+    # an unknown call, another number of arguments, none, not aligned, an int past 32 bits; the calls' own refusals (no handle)
+    counts = {0: 18, 1: 21, 2: 11, 3: 13, 4: 16}
+    for call, n in counts.items():
+        words = struct.pack(f"={n + 1}q", *[0] * (n + 1))
+        for c, w, m in ((call, words, n), (call, words, n - 1), (call, words, n + 1), (call, None, n), (-1, words, n), (5, words, n)):
+            assert lib.kvc_call(c, w, m) == kvc.KVC_EINVAL
+        buf = ctypes.create_string_buffer(8 * n + 8)
+        assert lib.kvc_call(call, ctypes.addressof(buf) + 4, n) == kvc.KVC_EINVAL
+        wide = [0] * n
+        wide[1] = 1 << 32
+        assert lib.kvc_call(call, struct.pack(f"={n}q", *wide), n) == kvc.KVC_EINVAL
 
 
 @pytest.mark.parametrize("amax,e", [(448.0, 0), (449.0, 1), (448 * 2.0 ** -64, -64), (0.0, -64), (1e-30, -64), (1.0, -8),
