@@ -400,7 +400,7 @@ int kvc_paged_attn_shared(kvc_t h, int layer, const void* q, int64_t q_stride, v
 int kvc_paged_attn_workspace(kvc_t h, int N, int NG, uint64_t* bytes);
 
 /* The calls of a serving step on one block of arguments, for bindings that pay for every argument (ctypes: 21 of them 2.5
- * us, a block 0.5): `call` names one of these, args [n] holds its arguments in order, 8 bytes each and 8-byte aligned (HOST
+ * us, a block 0.8): `call` names one of these, args [n] holds its arguments in order, 8 bytes each and 8-byte aligned (HOST
  * memory): pointers and integers as int64_t, floats as double.  The call's own status and meaning; KVC_EINVAL also for an unknown call,
  * another n than its arguments', or an int argument that does not fit. */
 #define KVC_CALL_PAGED_APPEND_ROPE 0      /* 18 arguments */

@@ -23,7 +23,7 @@
 // (token of the pair, d), each lane uses its own token's columns; the two halves are added at the end.
 //
 // What bounds it: for few rows the memory's bytes, half of a bf16 cache's (24 sequences of 3000 to 6000 positions on 8 KV
-// heads of 128 take 46 to 49 us, 4.7 to 5.0 TB/s; of 12,000 to 24,000 145 us, 6.2 TB/s: 6 us of start, 4 to 8 of merge and end),
+// heads of 128 take 45 to 48 us, 4.7 to 5.0 TB/s; of 12,000 to 24,000 144 us, 6.3 TB/s: 6 us of start, 4 to 8 of merge and end),
 // for more the softmax warps: 2.2 us a tile of 32 rows by 128 positions (256 of D = 64), two CTAs an SM at work, of
 // which the products take a tenth; conversions, three terms a weight and the exponentials are its chain (64 sequences of
 // 32 to 160 rows on one KV head of 64: 110 us against 7 of memory).  Two groups of softmax warps a CTA took as long.
