@@ -93,6 +93,65 @@ def test_axes_that_share_a_row_of_positions(kvc):
     assert all(torch.equal(a, b) for a, b in zip(*views))
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [900, 1, 600]])  # (queries in the keys' launch, or in one of their own beside it)
+def test_steps_captured_and_side_by_side(kvc, new):
+    # append and attention in one graph, replayed on other lengths, rows and positions; then two layers on two streams at
+    # once: all as one call after the other
+    D, H_q, H_kv, bs, mb, n = 128, 8, 2, 32, 64, sum(new)
+    g = torch.Generator().manual_seed(n)
+    table = torch.randperm(3 * mb, generator=g).view(3, mb).to(torch.int32).cuda()
+    rope = kvc.Rope([10000.0 ** (-i / 64) for i in range(64)])
+    cu = i32([0] + [sum(new[:b + 1]) for b in range(3)])
+    w = [(1 + 0.3 * torch.randn(D, generator=g)).bfloat16().cuda() for _ in range(2)]
+
+    def rows():
+        return [torch.randn(n, h, D, generator=g).bfloat16().cuda() for h in (H_q, H_kv, H_kv)]
+
+    def step(c, layer, x, out, lens, ws, stream=None):
+        c.append_rope(layer, rope, x[0], x[1], x[2], table, cu, lens, q_norm=w[0], k_norm=w[1], norm_eps=EPS, stream=stream)
+        c.attn_ragged(layer, x[0], out, table, cu, lens, workspace=ws, stream=stream)
+
+    steps = [(rows(), i32([h + T for h, T in zip(hist, new)])) for hist in ([0, 0, 0], [900, 40, 600], [100, 1, 33])]
+    want, views = [], []
+    c = kvc.PagedFP8KVCache(2, 3 * mb, bs, 3, mb, H_q, H_kv, D)
+    ws = torch.empty(c.attn_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+    for x, lens in steps:
+        out = torch.zeros(n, H_q, D, dtype=torch.bfloat16, device="cuda")
+        step(c, 0, [t.clone() for t in x], out, lens, ws)
+        torch.cuda.synchronize()
+        want.append(out)
+    views = [t.clone() for t in c.layer_views(0)]
+    assert c.last_error() == (kvc.KVC_OK, 0)
+
+    c = kvc.PagedFP8KVCache(2, 3 * mb, bs, 3, mb, H_q, H_kv, D)
+    x, lens, out = [t.clone() for t in steps[0][0]], steps[0][1].clone(), torch.zeros_like(want[0])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(c, 0, x, out, lens, ws)
+    for (rows_, lens_), o in zip(steps, want):
+        for t, r in zip(x, rows_):
+            t.copy_(r)
+        lens.copy_(lens_)
+        graph.replay()
+        assert torch.equal(out, o)
+    assert all(torch.equal(a, b) for a, b in zip(c.layer_views(0), views))
+
+    c = kvc.PagedFP8KVCache(2, 3 * mb, bs, 3, mb, H_q, H_kv, D)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs, wss = [torch.zeros_like(out) for _ in range(2)], [torch.empty_like(ws) for _ in range(2)]
+    for (rows_, lens_), o in zip(steps, want):
+        xs = [[t.clone() for t in rows_] for _ in range(2)]
+        torch.cuda.synchronize()
+        for layer, s in enumerate(streams):
+            step(c, layer, xs[layer], outs[layer], lens_, wss[layer], stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], o) and torch.equal(outs[1], o)
+    for layer in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(c.layer_views(layer), views))
+    assert c.last_error() == (kvc.KVC_OK, 0)
+
+
 def attend(kvc, bt, shared=False, ctas=None, math=0):
     c, d = bt.cache(kvc), bt.dev()
     c.set_math(math)
