@@ -325,3 +325,23 @@ def test_more_work_than_a_call_takes_is_refused(kvc, D, shared):
     c.attn_shared(*a, i32([0, 1]), i32([BS]), workspace=ws) if shared else c.attn_ragged(*a, workspace=ws)
     assert c.last_error() == (kvc.KVC_EDEVICE, kvc.KVC_DEV_TOO_LARGE)
     assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("N", [3, 1400])
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "bf16"), (128, "f32")])
+def test_a_batch_of_padding_alone(kvc, N, D, dtype):
+    # no sequence has a new token: every call returns, and leaves all as it was
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    c = kvc.PagedFP8KVCache(1, 6, 16, 2, 3, 8, 2, D, dtype)
+    for x in c.layer_views(0):
+        x.fill_(3)
+    table, cu, lens = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3), i32([0, 0, 0]), i32([20, 0])
+    q, k = torch.randn(N, 8, D, device="cuda").to(dt), torch.randn(N, 2, D, device="cuda").to(dt)
+    w = torch.ones(D, dtype=dt, device="cuda")
+    out, k_out = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    c.append_rope(0, kvc.Rope([1.0] * (D // 2)), q, k, k, table, cu, lens, q_out=out, q_norm=w, k_norm=w)
+    c.read(0, k_out, k_out.clone(), table, cu, lens)
+    c.attn_ragged(0, q, out, table, cu, lens)
+    c.attn_shared(0, q, out, table, cu, lens, i32([0, 2]), i32([0]))
+    assert c.last_error() == (kvc.KVC_OK, 0)
+    assert (out == 7).all() and (k_out == 7).all() and all((x == 3).all() for x in c.layer_views(0))
