@@ -363,8 +363,8 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights, times
  * their block's scale of V, as three E5M2 terms (within 2^-9 of one, or 2^-26 of the row's largest such product); a row
  * whose q has an infinity or a NaN is NaN; sequences and prefixes of many query rows per KV head (more than 256, fewer where N, B and D tell that most have
- * many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N leaves room for
- * more than 512; where the CUDA cores attend an 8-bit cache, all blocks are widened.  ws is device scratch of at least
+ * many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N and the
+ * cache's T_max leave room for much work; where the CUDA cores attend an 8-bit cache, all blocks are widened.  ws is device scratch of at least
  * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each.
  * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on

@@ -63,11 +63,18 @@ int many_rows(const kvc_cache* h, int N) {
     const int64_t mean = (int64_t)N * h->G / h->B;
     return h->D == 64 ? (mean >= 80 ? 16 : 128) : mean >= 160 ? 32 : 256;
 }
-// Is that worth its launches (some 17 us with nothing to do)?  The host knows how many rows an entry can have if every
-// sequence has a token, no more; a batch whose sequences have none, against that, is attended on codes all the same.
+// Is that worth its launches (13 to 16 us with nothing to do)?  The host knows how many rows an entry can have if every
+// sequence has a token, no more (a batch whose sequences have none, against that, is attended on codes all the same), and
+// how many positions it can see: where a CTA gets few tiles even then, codes are as quick.  (D = 128: up to 32, some 65 us:
+// one chunk of 200 tokens of 32 heads on 8 beside 23 single ones, all of 3000 to 6000 positions, 95 us on codes, 116 widened, of 300
+// 116 and 119; 64 sequences of 1 to 5 tokens on one KV head 90 and, with nothing widened, 106.)
 bool split_rows(const kvc_cache* h, int N, int NG) {
-    const int64_t most = NG > 0 ? N : (int64_t)N - h->B + 1;
-    return most * h->G > 512;
+    const int64_t most = (NG > 0 ? N : (int64_t)N - h->B + 1) * h->G;
+    if (most <= 512) return false;
+    int rows, ctas;
+    kvc::q8_shape(h->D, h->G, &rows, &ctas);
+    const int64_t tiles = (most + rows - 1) / rows * (((int64_t)h->T_max * h->D + 16383) / 16384) * h->H_kv;
+    return tiles > (int64_t)(ctas == 1 ? 24 : 64) * h->sms;
 }
 // The parts of the scratch: the path's, that of the kernel of plain pools beside the one on codes, and the two
 // widened pools.

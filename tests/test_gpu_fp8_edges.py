@@ -197,12 +197,20 @@ MIXES = [  # new, H_q, H_kv, D: which rows are attended on codes and which on wi
 ]
 
 
+def with_room(bt, blocks):
+    """The batch in a cache whose sequences may grow to that many blocks (what is widened depends on it)."""
+    bt.table = torch.cat([bt.table, torch.full((bt.B, blocks - bt.max_blocks), -1, dtype=torch.int32)], 1)
+    bt.max_blocks = blocks
+    return bt
+
+
 @pytest.mark.parametrize("new,H_q,H_kv,D", MIXES)
 @pytest.mark.parametrize("shared", [False, True])
-def test_rows_on_codes_beside_widened_blocks(kvc, new, H_q, H_kv, D, shared):
+@pytest.mark.parametrize("blocks", [64, 1 << 16])
+def test_rows_on_codes_beside_widened_blocks(kvc, new, H_q, H_kv, D, shared, blocks):
     hist = [(211 * i) % 300 + 40 for i in range(len(new))]
     kw = dict(start=[0, 2, len(new)], prefix=[40, 32]) if shared else {}
-    bt = Batch8(new, hist, 16, H_q, H_kv, D, pad=3, mag=2, **kw)
+    bt = with_room(Batch8(new, hist, 16, H_q, H_kv, D, pad=3, mag=2, **kw), blocks)
     check_attention(attend(kvc, bt, shared), bt, attention64(bt), tensor_cores=True)
 
 
@@ -229,6 +237,28 @@ def test_wide_batches(kvc, shared):
     check_attention(attend(kvc, bt, shared), bt, attention64(bt), tensor_cores=True)
 
 
+@pytest.mark.parametrize("new,hist,start,prefix,bs,H_q,H_kv,D", [
+    ([300, 1, 129], [0, 50, 200], None, None, 256, 16, 2, 128),
+    ([1, 400, 2, 65, 64], [300, 100, 0, 60, 7], None, None, 32, 8, 2, 128),   # a rule's either side: 260 and 256 rows
+    ([1, 400, 2, 65, 64], [300, 100, 0, 60, 7], None, None, 128, 8, 2, 64),
+    ([0, 600, 0, 0], [5, 0, 90, 0], None, None, 16, 2, 1, 128),
+    ([2] * 90 + [300], [70] * 90 + [3], None, None, 16, 4, 2, 128),
+    # prefixes and sequences of many rows, in every combination with few
+    ([300, 2, 1], [200, 180, 150], [0, 2, 3], [128, 64], 32, 8, 2, 128),
+    ([30] * 12, [97] * 12, [0, 12], [96], 32, 4, 2, 64),
+    ([400, 500], [300, 280], [0, 1, 2], [256, 0], 64, 4, 2, 64),
+    ([1] * 300, [50 + i % 7 for i in range(300)], [0, 150, 300], [48, 32], 16, 4, 2, 128),
+])
+@pytest.mark.parametrize("ctas", [None, 7])
+def test_widened_entries(kvc, new, hist, start, prefix, bs, H_q, H_kv, D, ctas):
+    kw = dict(start=start, prefix=prefix) if start else {}
+    bt = with_room(Batch8(new, hist, bs, H_q, H_kv, D, pad=2, mag=2, q_scale=1.5, **kw), (1 << 21) // bs)
+    c = bt.cache(kvc)
+    assert c.attn_workspace_bytes(bt.rows, len(start) - 1 if start else 0) > 2 * 2 * bt.K8.numel()  # (two pools in bf16)
+    out = attend(kvc, bt, start is not None, ctas)
+    check_attention(out, bt, attention64(bt), tensor_cores=True)
+
+
 def test_math_modes(kvc):
     for dtype, D, tensor in (("bf16", 128, True), ("bf16", 64, True), ("bf16", 256, False), ("f32", 128, False)):
         c = kvc.PagedFP8KVCache(1, 2, 16, 1, 2, 8, 2, D, dtype)
@@ -245,8 +275,9 @@ def test_math_modes(kvc):
         assert c.attn_workspace_bytes(1) == before
 
 
-def test_scratch_grows_with_rows_and_groups(kvc):
-    c = kvc.PagedFP8KVCache(1, 8, 16, 6, 8, 8, 2, 128)
+@pytest.mark.parametrize("blocks", [8, 1 << 16])
+def test_scratch_grows_with_rows_and_groups(kvc, blocks):
+    c = kvc.PagedFP8KVCache(1, 8, 16, 6, blocks, 8, 2, 128)
     for groups in (0, 1, 6):
         sizes = [c.attn_workspace_bytes(n, groups) for n in (1, 6, 64, 128, 129, 130, 134, 135, 500)]
         assert sizes == sorted(sizes)
