@@ -682,6 +682,10 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                     }
                     tc5_wait_st();
                 }
+                // What a score's factor, (a row's scale) (a block's scale), is at least, added to it: the product of two tiny scales
+                // is 0, and a masked score of -inf times 0 NaN.  (Nothing for factors from 2^-101 on; below, scores of up to 2^24
+                // times it are 0 next to 1 with and without it.)
+                constexpr float LEAST = 0x1p-126f;
                 // Scores of eight rows at token par, in log2 units.
                 auto scores = [&](int c, int par, float (&x)[8]) {
                     float s0[8], s1[8];
@@ -690,10 +694,10 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
 #pragma unroll
                     for (int i = 0; i < 8; i += 4) {
                         const float4 q4 = *reinterpret_cast<const float4*>(qs + 8 * c + i);
-                        x[i] = fmaf(s1[i], 0.0625f, s0[i]) * (q4.x * sc.x);
-                        x[i + 1] = fmaf(s1[i + 1], 0.0625f, s0[i + 1]) * (q4.y * sc.x);
-                        x[i + 2] = fmaf(s1[i + 2], 0.0625f, s0[i + 2]) * (q4.z * sc.x);
-                        x[i + 3] = fmaf(s1[i + 3], 0.0625f, s0[i + 3]) * (q4.w * sc.x);
+                        x[i] = fmaf(s1[i], 0.0625f, s0[i]) * fmaf(q4.x, sc.x, LEAST);
+                        x[i + 1] = fmaf(s1[i + 1], 0.0625f, s0[i + 1]) * fmaf(q4.y, sc.x, LEAST);
+                        x[i + 2] = fmaf(s1[i + 2], 0.0625f, s0[i + 2]) * fmaf(q4.z, sc.x, LEAST);
+                        x[i + 3] = fmaf(s1[i + 3], 0.0625f, s0[i + 3]) * fmaf(q4.w, sc.x, LEAST);
                     }
                 };
                 // References of the rows 8 c .. of each bit c of `which` at or above everything in this tile, rounded up to
@@ -762,7 +766,8 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                 auto weigh = [&](int c, float2 (&sum)[4]) {
                     __half2 top = __float2half2_rn(0.f);
                     const __half2 eight = __float2half2_rn(8.f);
-                    const float2 a2 = make_float2(sc.y, sc.y), k2 = make_float2(sc.x, sc.x), s16 = make_float2(0.0625f, 0.0625f);
+                    const float2 a2 = make_float2(sc.y, sc.y), k2 = make_float2(sc.x, sc.x), s16 = make_float2(0.0625f, 0.0625f),
+                                 least = make_float2(LEAST, LEAST);
 #pragma unroll
                     for (int par = 0; par < TOK; ++par) {
                         float s0[8], s1[8];
@@ -777,7 +782,7 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int n = i + k;
-                                const float2 f = __fmul2_rn(k ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), k2);
+                                const float2 f = __ffma2_rn(k ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), k2, least);
                                 float2 e = __ffma2_rn(make_float2(s1[2 * n], s1[2 * n + 1]), s16, make_float2(s0[2 * n], s0[2 * n + 1]));
                                 e = __ffma2_rn(e, f, k ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
                                 e = make_float2(fast_exp2(min_nan(e.x, 60.f)), fast_exp2(min_nan(e.y, 60.f)));
