@@ -787,7 +787,9 @@ ragged_q8_kernel(const Q8Attn pa, const __grid_constant__ CUtensorMap tmK, const
                                 e = __ffma2_rn(e, f, k ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y));
                                 e = make_float2(fast_exp2(min_nan(e.x, 60.f)), fast_exp2(min_nan(e.y, 60.f)));
                                 sum[n] = __fadd2_rn(sum[n], e);
-                                const float2 w = __fmul2_rn(e, __fmul2_rn(k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), a2));
+                                // (in this order: 2^{b_t} of a block with large values times b may pass the largest float, which 0, the
+                                // weight of a position that a row does not see, must not meet)
+                                const float2 w = __fmul2_rn(__fmul2_rn(e, k ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y)), a2);
                                 __half2 h = __floats2half2_rn(w.x, w.y);
                                 top = __hmax2(top, h);
                                 u[0][n] = half2_bits(h);

@@ -41,3 +41,56 @@ def test_tiny_queries_before_zero_keys(kvc, D, size, keys, shared):
     bt.Ks[some] = 0.0 if keys == "never written" else 2.0 ** -64
     bt.K = values(bt.K8, bt.Ks)
     check_attention(attend(kvc, bt, shared), bt, attention64(bt), tensor_cores=True)
+
+
+def smallest_weights(bt):
+    """What the outputs may be off by where weights are small: a weight times its block's scale of V, scaled so that a row's largest
+    is above 2^3, is cut into f16, off by half of 2^-24 there, and its third term, 1/64 of an E5M2 value, by half of 2^-16 / 64:
+    2^-23 + 2^-25 together, at most (2^-26 + 2^-28) of the row's largest.  It meets the code."""
+    out = torch.zeros(bt.rows, bt.H_q, bt.D, dtype=torch.float64)
+    G = bt.H_q // bt.H_kv
+    for b in range(bt.B):
+        for h in range(bt.H_kv):
+            t = torch.arange(bt.lens[b])
+            e = bt.table[b, t // bt.bs].long()
+            K, V, s = bt.K[e, h, t % bt.bs], bt.V[e, h, t % bt.bs], bt.Vs[e, h].double().clamp(min=2.0 ** -64)
+            for i in range(bt.new[b]):
+                n, r = bt.hist[b] + i + 1, bt.cu[b] + i
+                p = torch.softmax(bt.q[r, h * G:(h + 1) * G].double() @ K[:n].T / bt.D ** 0.5, -1)
+                codes = (V[:n].abs() / s[:n, None]).sum(0)
+                out[r, h * G:(h + 1) * G] = (2.0 ** -26 + 2.0 ** -28) * (p * s[:n]).amax(-1, keepdim=True) * codes
+    return out
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("math", [0, 1])
+@pytest.mark.parametrize("value", [2.0 ** 60, 3e20, 5e37, 3e38])
+@pytest.mark.parametrize("before", ["ordinary", "zero"])
+def test_a_large_value_of_a_later_token(kvc, D, math, value, before):
+    # token 1 begins a block, which token 0 does not see: in token 0's tile, and in a tile of its own
+    for hist in ([15, 255], [143, 15]):
+        bt = Batch8([6, 3], hist, 16, 8, 2, D, pad=1)
+        bt.K *= 0.25
+        if before == "zero":
+            bt.V.zero_()
+        for b in (0, 1):
+            bt.V[int(bt.table[b, (hist[b] + 1) // 16]), 1, 0, 9] = value
+        bt.requantize()
+        out = attend(kvc, bt, math=math)
+        ref, tol, A = attention64(bt)
+        if math == 0:
+            tol = tol + smallest_weights(bt)
+        check_attention(out, bt, (ref, tol, A), tensor_cores=math == 0)
+        assert before != "zero" or ((out[0] == 0).all() and (out[6] == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_and_small_values_seen_together(kvc, D):
+    # scales of V 2^140 and more apart in one sequence, the large ones first, last and in between; every weight finite
+    for at in ([0], [18], [0, 9, 18]):
+        bt = Batch8([2, 1], [300, 40], 16, 8, 2, D)
+        bt.V *= 2.0 ** -50
+        for j in at:
+            bt.V[int(bt.table[0, j])] *= 2.0 ** 150
+        bt.requantize()
+        check_attention(attend(kvc, bt), bt, attention64(bt), tensor_cores=True)
