@@ -141,8 +141,9 @@ __device__ __forceinline__ void merge_row_wide(const RaggedParams& p, int np, T*
     __syncthreads();
 }
 
-// NP pieces, two to four, the common cuts: a warp merges ILP rows at once (all their loads in flight), in the order of
-// merge_pieces.  (Three and four pieces taken so as well: 24 sequences, 4 with chunks of up to 300 tokens, over an 8-bit
+// NP pieces, two to four, the common cuts: a warp merges ILP rows at once (all their loads in flight).  Three and four in
+// the order and with the roundings of merge_pieces; of two, the second denominator is added to the first by one fma (products
+// and sums are written out: left to the compiler, which of them become one fma is its choice).  (Three and four pieces taken so as well: 24 sequences, 4 with chunks of up to 300 tokens, over an 8-bit
 // cache 165 -> 156 us.)
 template <int NP, int ILP, typename T, class Out, class At>
 __device__ __forceinline__ void merge_few(const RaggedParams& p, int r0, int step, int rows, int lane, Out&& out_of, At&& at_row) {
@@ -175,7 +176,7 @@ __device__ __forceinline__ void merge_few(const RaggedParams& p, int r0, int ste
         for (int q = 0; q < NP; ++q) {
             if (s[k][q].y == 0.f) continue;
             const float w = fast_exp2(s[k][q].x - mu);
-            l[q] = w * s[k][q].y;
+            l[q] = NP == 2 && q == 1 ? fmaf(w, s[k][q].y, l[0]) : __fmul_rn(w, s[k][q].y);
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 if (lane * 4 + v * 128 >= p.D) continue;
@@ -185,7 +186,8 @@ __device__ __forceinline__ void merge_few(const RaggedParams& p, int r0, int ste
                 a.o[v].w = fmaf(w, x[k][q][v].w, a.o[v].w);
             }
         }
-        a.l = (l[0] + l[2]) + (l[1] + l[3]);
+        if constexpr (NP == 2) a.l = s[k][1].y == 0.f ? l[0] : l[1];
+        else a.l = (l[0] + l[2]) + (l[1] + l[3]);
         merge_store<T>(p, a, out_of(r0 + k * step), lane);
     }
 }
