@@ -56,7 +56,7 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
         axis_s[tid] = rt.axis[tid];
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (grid.two) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (see `late`: 74 us against 79.5)
+    if (grid.two) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (see LATE: 74 us against 79.5)
     __syncthreads();
     bool bad = false;
     int cnt = 0;
@@ -312,8 +312,7 @@ int launch_append8(int dtype, const RopeParams& p, const RopeTable& t, int sms, 
     if (e != 0 || !many || !p.q) return e;
     RopeParams q = p;
     q.H_kv = 0;
-    q.late = 1;
-    return launch_append_rope(dtype, q, t, sms, s);
+    return launch_late_queries(dtype, q, t, s);
 }
 
 // ------------------------------------------------------------------ reading back

@@ -659,10 +659,9 @@ struct RopeParams {
     const void *q_norm, *k_norm;  // [D] weights of the heads' norms, nullptr: not normalised
     float eps;
     float *Ksc, *Vsc;  // 8-bit cache: scales [num_blocks, H_kv] (Kc, Vc: E4M3 codes)
-    // 1: the grid before on the stream is the other half of the same append, which has waited for what came before it and
-    // shares nothing with this one: it is waited for at the end, not at the start.
-    int late;
 };
 int launch_append_rope(int dtype, const RopeParams& p, const RopeTable& t, int sms, cudaStream_t s);
+// The queries' half of an 8-bit cache's append of many rows, behind the keys' (see LATE in kvc_rope.cuh).
+int launch_late_queries(int dtype, const RopeParams& p, const RopeTable& t, cudaStream_t s);
 
 }  // namespace kvc
