@@ -63,8 +63,16 @@ struct RaggedParams {
     int P;          // CTAs at most
     float qscale;   // log2(e) / sqrt(D)
     // 8-bit caches: entries with more than `wide` query rows per head are attended by the kernel of plain pools, the
-    // others by that on codes.  part: 0 all entries, 1 those with few rows, 2 the others.
+    // others by that on codes.  part: 0 all entries, 1 those with few rows, 2 the others: set by take().
     int wide, part;
+    unsigned T0, T1;  // this call's entries have T0 .. T0 + T1 new tokens
+    void take(int which, int rows) {
+        wide = rows;
+        part = which;
+        const unsigned few = (unsigned)rows >> lgG;
+        T0 = which == 2 ? few + 1 : 0;
+        T1 = which == 1 ? few : ~0u - T0;
+    }
 };
 
 // Scratch layout (bytes, 256-byte aligned parts), host side: P CTAs with `slots` slots of `rows` rows.
@@ -156,7 +164,7 @@ __device__ __forceinline__ Entry group_entry(const RaggedParams& p, int g) {
 
 // Is the entry this call's?
 __device__ __forceinline__ bool in_part(const RaggedParams& p, const Entry& s) {
-    return p.part == 0 || (((int64_t)s.T << p.lgG) > p.wide) == (p.part == 2);
+    return (unsigned)s.T - p.T0 <= p.T1;
 }
 
 // sum of ceil(x / 2^lg) for x = 1 .. X, modulo 2^32 (of far positions only differences fit: unsigned

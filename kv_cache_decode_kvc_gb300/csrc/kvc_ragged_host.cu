@@ -159,6 +159,7 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
     p.T_max = h->T_max;
     p.P = ragged_p(h, path);
     p.qscale = (float)(1.4426950408889634 / sqrt((double)h->D));
+    p.take(0, 0);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!h->quant) {
         if (path == Path::CC) return kvc::launch_ragged_cc(h->dtype, p, st) == 0 ? KVC_OK : KVC_ECUDA;
@@ -182,9 +183,8 @@ int attn_ragged(kvc_t h, int layer, const void* q, int64_t q_stride, void* out, 
         m.row_o = p.row_o;  // (the rows of shared prefixes are merged together)
         m.row_ml = p.row_ml;
         m.P = ragged_p(h, Path::TC5);
-        m.part = 2;
-        p.wide = m.wide;
-        p.part = 1;
+        m.take(2, m.wide);
+        p.take(1, m.wide);
         CUtensorMap mk, mv;
         const uint64_t rows = h->layer_bytes / h->D;
         const int box = h->bs < 128 ? h->bs : 128;
