@@ -235,8 +235,9 @@ __device__ __forceinline__ void append8_block(const RopeParams& p, const RopeTab
                 if (old >= x) x = old;
                 else down = exp2i(max(old - x, -60));
             }
-            // (a unit's warps have all read the old scale before one of them stores the new one)
+            // (a unit's lanes, and its warps, have all read the old scale before one of them stores the new one)
             if (grid.wpu > 1) __syncthreads();
+            else __syncwarp();
             if (live && part == 0 && lane == 0) *sc = exp2i(x);
             mul = exp2i(-x);
             if (infinite || x == Q8_EMAX) lim = x == Q8_EMAX ? 240.f : 448.f;  // (256 2^120 is past the largest float)
