@@ -10,6 +10,7 @@ There is no fallback: if the library is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 import struct
@@ -117,7 +118,7 @@ def header_symbols() -> list[str]:
 
 # ----------------------------------------------------------------------------- marshalling
 def _ptr(x) -> int:
-    if x is None or type(x) is int:
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
@@ -304,7 +305,15 @@ def kvc_rope_destroy(r) -> None:
 
 # The calls of a serving step go through kvc_call: their arguments as one block of 8-byte words.
 def _addr(x) -> int:
-    return 0 if x is None else x if type(x) is int else x.data_ptr()
+    """A tensor's address, an integer (of any subclass), a ctypes pointer's value, 0 for None."""
+    if type(x) is int:
+        return x
+    if x is None:
+        return 0
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return (x.value or 0) if isinstance(x, ctypes.c_void_p) else operator.index(x)
 
 
 _APPEND, _APPEND_NORM = struct.Struct("=18q").pack, struct.Struct("=5qd15q").pack
@@ -319,33 +328,33 @@ def _call(call, words, n, what):
 
 def kvc_paged_append_rope(h, layer, rope, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, positions,
                           pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _call(0, _APPEND(h or 0, layer, rope or 0, _addr(q), q_stride, _addr(q_out), q_out_stride, _addr(k), k_stride,
+    _call(0, _APPEND(_addr(h), layer, _addr(rope), _addr(q), q_stride, _addr(q_out), q_out_stride, _addr(k), k_stride,
                      _addr(v), v_stride, _addr(positions), pos_stride, _addr(block_table), _addr(cu_seqlens), _addr(lens),
                      N, _stream(stream)), 18, "kvc_paged_append_rope")
 
 
 def kvc_paged_append_norm_rope(h, layer, rope, q_norm, k_norm, eps, q, q_stride, q_out, q_out_stride, k, k_stride, v,
                                v_stride, positions, pos_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _call(1, _APPEND_NORM(h or 0, layer, rope or 0, _addr(q_norm), _addr(k_norm), eps, _addr(q), q_stride, _addr(q_out),
+    _call(1, _APPEND_NORM(_addr(h), layer, _addr(rope), _addr(q_norm), _addr(k_norm), eps, _addr(q), q_stride, _addr(q_out),
                           q_out_stride, _addr(k), k_stride, _addr(v), v_stride, _addr(positions), pos_stride,
                           _addr(block_table), _addr(cu_seqlens), _addr(lens), N, _stream(stream)), 21,
           "kvc_paged_append_norm_rope")
 
 
 def kvc_paged_read(h, layer, k_out, k_stride, v_out, v_stride, block_table, cu_seqlens, lens, N, stream=None) -> None:
-    _call(2, _READ(h or 0, layer, _addr(k_out), k_stride, _addr(v_out), v_stride, _addr(block_table), _addr(cu_seqlens),
+    _call(2, _READ(_addr(h), layer, _addr(k_out), k_stride, _addr(v_out), v_stride, _addr(block_table), _addr(cu_seqlens),
                    _addr(lens), N, _stream(stream)), 11, "kvc_paged_read")
 
 
 def kvc_paged_attn_ragged(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, ws, ws_bytes,
                           stream=None) -> None:
-    _call(3, _ATTN(h or 0, layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
+    _call(3, _ATTN(_addr(h), layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
                    _addr(lens), N, _addr(ws), ws_bytes, _stream(stream)), 13, "kvc_paged_attn_ragged")
 
 
 def kvc_paged_attn_shared(h, layer, q, q_stride, out, out_stride, block_table, cu_seqlens, lens, N, groups,
                           prefix_lens, NG, ws, ws_bytes, stream=None) -> None:
-    _call(4, _SHARED(h or 0, layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
+    _call(4, _SHARED(_addr(h), layer, _addr(q), q_stride, _addr(out), out_stride, _addr(block_table), _addr(cu_seqlens),
                      _addr(lens), N, _addr(groups), _addr(prefix_lens), NG, _addr(ws), ws_bytes, _stream(stream)), 16,
           "kvc_paged_attn_shared")
 
