@@ -361,7 +361,8 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * KV head (tokens x H_q / H_kv, of a prefix all its group's), as one (2^-8) for larger ones.  Every other shape, or math
  * mode 1, runs on CUDA cores in fp32.  On a paged 8-bit cache the tensor cores take the codes as they are: q as two E4M3
  * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights, times
- * their block's scale of V, as three E5M2 terms (within 2^-9 of one, or 2^-26 of the row's largest such product); a row
+ * their block's scale of V, as three E5M2 terms (within 2^-9 + 2^-11 of one, or 2^-26 + 2^-28 of the row's largest such
+ * product: beside a block of values 2^26 times as large, a position's own count for nothing); a row
  * whose q has an infinity or a NaN is NaN; sequences and prefixes of many query rows per KV head (more than 256, fewer where N, B and D tell that most have
  * many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N and the
  * cache's T_max leave room for much work; where the CUDA cores attend an 8-bit cache, all blocks are widened.  ws is device scratch of at least

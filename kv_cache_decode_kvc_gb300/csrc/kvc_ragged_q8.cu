@@ -10,8 +10,8 @@
 //     exact but for elements below 2^-13 of the row's largest (off by 2^-21 of that).  Each term has columns of its own.
 //   - O^T += V^T W (A = the same tile of V read MN-major, B = the weights): w_t = 2^{x_t - m} 2^{b_t} 2^{m - M + 4} as
 //     three E5M2 terms with columns of their own, w = u0 + u1 / 8 + u2 / 64: the top byte of w in f16, that of 8 times what
-//     is left, and of 8 times what is then left, rounded: within 2^-9 of w, or 2^-23 absolute with the row's largest
-//     above 2^3.  (A byte mask, a subtraction and a product each; E4M3 terms took conversions, and a weight had 2 binades
+//     is left, and of 8 times what is then left, rounded: within 2^-9 + 2^-11 of w (the last term's rounding and f16's; 1.09 2^-9
+//     at worst), or 2^-23 + 2^-25 absolute with the row's largest above 2^3.  (A byte mask, a subtraction and a product each; E4M3 terms took conversions, and a weight had 2 binades
 //     to grow until its reference had to be raised, here 10.)  m >= max x_t and M >= max(x_t + b_t) are integers: all
 //     factors between references are exact.  The denominator sums 2^{x_t - m} in fp32.
 // A thread is a key position (lane of S^T), its columns the rows.  The references are raised only if a weight

@@ -107,3 +107,22 @@ class Batch8(Batch):
             view.copy_(x)
         torch.cuda.synchronize()
         return c
+
+
+def smallest_weights(bt):
+    """What the outputs may be off by where weights are small: a weight times its block's scale of V, scaled so that a row's largest
+    is above 2^3, is cut into f16, off by half of 2^-24 there, and its third term, 1/64 of an E5M2 value, by half of 2^-16 / 64:
+    2^-23 + 2^-25 together, at most (2^-26 + 2^-28) of the row's largest.  It meets the code."""
+    out = torch.zeros(bt.rows, bt.H_q, bt.D, dtype=torch.float64)
+    G = bt.H_q // bt.H_kv
+    for b in range(bt.B):
+        for h in range(bt.H_kv):
+            t = torch.arange(bt.lens[b])
+            e = bt.table[b, t // bt.bs].long()
+            K, V, s = bt.K[e, h, t % bt.bs], bt.V[e, h, t % bt.bs], bt.Vs[e, h].double().clamp(min=2.0 ** -64)
+            for i in range(bt.new[b]):
+                n, r = bt.hist[b] + i + 1, bt.cu[b] + i
+                p = torch.softmax(bt.q[r, h * G:(h + 1) * G].double() @ K[:n].T / bt.D ** 0.5, -1)
+                codes = (V[:n].abs() / s[:n, None]).sum(0)
+                out[r, h * G:(h + 1) * G] = (2.0 ** -26 + 2.0 ** -28) * (p * s[:n]).amax(-1, keepdim=True) * codes
+    return out

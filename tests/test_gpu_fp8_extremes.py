@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from fp8_util import Batch8, values
+from fp8_util import Batch8, smallest_weights, values
 from ragged_util import attention64, check_attention
 
 pytestmark = pytest.mark.gpu
@@ -41,25 +41,6 @@ def test_tiny_queries_before_zero_keys(kvc, D, size, keys, shared):
     bt.Ks[some] = 0.0 if keys == "never written" else 2.0 ** -64
     bt.K = values(bt.K8, bt.Ks)
     check_attention(attend(kvc, bt, shared), bt, attention64(bt), tensor_cores=True)
-
-
-def smallest_weights(bt):
-    """What the outputs may be off by where weights are small: a weight times its block's scale of V, scaled so that a row's largest
-    is above 2^3, is cut into f16, off by half of 2^-24 there, and its third term, 1/64 of an E5M2 value, by half of 2^-16 / 64:
-    2^-23 + 2^-25 together, at most (2^-26 + 2^-28) of the row's largest.  It meets the code."""
-    out = torch.zeros(bt.rows, bt.H_q, bt.D, dtype=torch.float64)
-    G = bt.H_q // bt.H_kv
-    for b in range(bt.B):
-        for h in range(bt.H_kv):
-            t = torch.arange(bt.lens[b])
-            e = bt.table[b, t // bt.bs].long()
-            K, V, s = bt.K[e, h, t % bt.bs], bt.V[e, h, t % bt.bs], bt.Vs[e, h].double().clamp(min=2.0 ** -64)
-            for i in range(bt.new[b]):
-                n, r = bt.hist[b] + i + 1, bt.cu[b] + i
-                p = torch.softmax(bt.q[r, h * G:(h + 1) * G].double() @ K[:n].T / bt.D ** 0.5, -1)
-                codes = (V[:n].abs() / s[:n, None]).sum(0)
-                out[r, h * G:(h + 1) * G] = (2.0 ** -26 + 2.0 ** -28) * (p * s[:n]).amax(-1, keepdim=True) * codes
-    return out
 
 
 @pytest.mark.parametrize("D", [64, 128])
