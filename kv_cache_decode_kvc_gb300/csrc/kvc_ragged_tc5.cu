@@ -898,7 +898,7 @@ ragged_tc5_kernel(const RaggedParams p, const __grid_constant__ CUtensorMap tmQ,
                     return g.kv0 + j * C::KT;
                 };
                 // The row's maximum so far from this half's `top`; the reference is raised, and O with it, only if
-                // it grew by more than 2^8 (weights against a lower one keep their relative precision).
+                // it grew by more than `slack` binades.
                 // Returns the weights' offset.
                 auto agree = [&](float top, int j) {
                     *mine = top;
