@@ -362,11 +362,12 @@ int kvc_create_paged_fp8(kvc_t* out, int layers, int num_blocks, int block_size,
  * mode 1, runs on CUDA cores in fp32.  On a paged 8-bit cache the tensor cores take the codes as they are: q as two E4M3
  * terms (exact but for elements below 2^-13 of their row's largest, which are off by 2^-21 of that), weights, times
  * their block's scale of V, as three E5M2 terms (within 2^-9 + 2^-11 of one, or 2^-26 + 2^-28 of the row's largest such
- * product: beside a block of values 2^26 times as large, a position's own count for nothing); a row
- * whose q has an infinity or a NaN is NaN; sequences and prefixes of many query rows per KV head (more than 256, fewer where N, B and D tell that most have
- * many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N and the
- * cache's T_max leave room for much work; where the CUDA cores attend an 8-bit cache, all blocks are widened.  ws is device scratch of at least
- * kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
+ * product: where one block's values are 2^26 times another's, the other's count for nothing beside them); a row whose q
+ * has an infinity or a NaN is NaN; sequences and prefixes of many query rows per KV head (more than 256, fewer where N, B and D
+ * tell that most have many) are attended as on a bf16 cache, over blocks widened (exactly) in the scratch, where the call's N and
+ * the cache's B and T_max leave room for much work; where the CUDA cores attend an 8-bit cache, all blocks are widened.  Sums of
+ * weights times values are fp32, divided last; a weight may be 2^8 (over widened blocks 2^16) times its share of the row's
+ * largest, so values from some 2^100 on may overflow them.  ws is device scratch of at least kvc_paged_attn_workspace bytes, 256-byte aligned, owned by the caller and free for other use
  * once the call has completed on its stream; calls that may run at the same time need one each.
  * A call's work is counted in tiles: up to 256 query rows (tokens x heads of one KV head; 64 on
  * CUDA cores) by 128 positions (CUDA cores: 64 for D <= 64, else 32) that its last row sees.  A

@@ -28,8 +28,10 @@ __device__ __forceinline__ uint32_t q8_rescale4(uint32_t c, float mul) {
 // touch), so no sum over the sequences is needed.  The angles of 4096 pairs (64 rows at D = 128) are turned into
 // cosines and sines at a time, once for the CTA's heads where that is all of them.  K or V of a head is a unit of one warp (of two or four where heads are few or blocks long), which goes
 // over its rows twice: first for the largest |x| of K, normalised and rotated, or of V, which settles the scale, then, from
-// L1, for the codes.  Bound by its chain of lookups, first pass, maximum and second pass, beside the memory's: 9700 rows of
-// 32 + 8 heads take 75 us with the queries' grid beside it, 2.9 TB/s.  (Values held in registers between the passes
+// L1, for the codes.  Bound by its chain of lookups, first pass, maximum and second pass (0.43 of its issue slots, waits for
+// memory first among its stalls): 9700 rows of 32 + 8 heads, two groups of heads, take 73 us with the queries' grid, 3.0 TB/s.  That
+// grid begins as the last CTA of this one has begun, for there are 304 places, two an SM: 152 blocks of 64 rows take 69 us, 153
+// 87, 304 129, 308 148.  (Values held in registers between the passes
 // spilled, or left too few warps: 112 to 129 us, and 81 with a CTA's heads laid out as pieces and a maximum exchanged
 // for each.)  A block that holds earlier rows and needs a larger scale has their codes moved down.
 constexpr int APPEND8_THREADS = 256, APPEND8_WARPS = APPEND8_THREADS / 32;

@@ -66,8 +66,11 @@ int many_rows(const kvc_cache* h, int N) {
 // Is that worth its launches (13 to 16 us with nothing to do)?  The host knows how many rows an entry can have if every
 // sequence has a token, no more (a batch whose sequences have none, against that, is attended on codes all the same), and
 // how many positions it can see: where a CTA gets few tiles even then, codes are as quick.  (D = 128: up to 32, some 65 us:
-// one chunk of 200 tokens of 32 heads on 8 beside 23 single ones, all of 3000 to 6000 positions, 95 us on codes, 116 widened, of 300
-// 116 and 119; 64 sequences of 1 to 5 tokens on one KV head 90 and, with nothing widened, 106.)
+// one chunk of 200 tokens of 32 heads on 8 beside 23 single ones, all of 3000 to 6000 positions, 92 us on codes, 116 widened, of 300
+// 116 and 119; 64 sequences of 1 to 5 tokens on one KV head 90 and, with nothing widened, 106.)  What it knows are capacities, T_max
+// and B, and these times are of tables as long as their longest sequence: with tables of 131,072 positions that chunk of 200 is
+// widened all the same (116), and 24 sequences of 8 tokens take 84 us, not 72; a chunk of 1024 tokens behind 4000 positions alone among
+// 1024 slots, whose others N could give a token each, stays on codes (274 us; in a batch of one, widened, 105).
 bool split_rows(const kvc_cache* h, int N, int NG) {
     const int64_t most = (NG > 0 ? N : (int64_t)N - h->B + 1) * h->G;
     if (most <= 512) return false;
